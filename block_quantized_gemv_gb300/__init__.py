@@ -59,6 +59,15 @@ EXPORTS = {
     "bqg_status_string": (["i"], "str"),
     "bqg_version": ([], "str"),
     "bqg_last_cuda_error": ([], "str"),
+    "bqg_qk_norm_rope": (["p", "p", "i", "i64", "i64", "i64", "i", "i", "i", "i", "p", "p", "f", "p", "p", "i64", "i",
+                          "i", "p", "p", "p"], "i"),
+    "bqg_qk_norm_rope_kv_write": (["p", "p", "p", "i", "i64", "i64", "i64", "i64", "i", "i", "p", "p", "f", "p", "p",
+                                   "i64", "i", "i", "p", "p", "p", "p"], "i"),
+    "bqg_kv_write": (["p", "p", "i", "i64", "i64", "i64", "p", "p", "p"], "i"),
+    "bqg_kv_read": (["p", "p", "i64", "i", "p", "p", "p"], "i"),
+    "bqg_tree_attention": (["p", "i64", "p", "p", "i64", "p", "p", "i", "i64", "i", "i", "p", "f", "p", "p", "size",
+                            "p"], "i"),
+    "bqg_tree_attention_workspace_size": (["p", "i", "i", "i"], "size"),
     "bqg_gemv_q4_0_q8_1_noalloc": (["p", "p", "p", "i", "i64", "i64", "p"], "i"),
     "bqg_noalloc_scratch_bytes": ([], "size"),
 }
@@ -429,6 +438,232 @@ def debug_q4_0_q8_1_block_dots(Wp, Xq, N, K, out=None, stream=None):
 def debug_q4_0_q8_1_block_dots_kslice(Wp, Xq, N, K, out=None, stream=None):
     """The same dots from the K-slice kernel's routine."""
     return _block_dots("bqg_debug_q4_0_q8_1_block_dots_kslice", Wp, Xq, N, K, out, stream)
+
+
+# --- attention over a paged cache ------------------------------------------------
+DEVERR_SLOT, DEVERR_POSITION, DEVERR_PAGE, DEVERR_LENGTH = 16, 32, 64, 128
+_KV_DTYPE = {BF16: torch.bfloat16, Q8_0: torch.int8, Q4_0: torch.uint8}
+
+
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int), ("page_size", ctypes.c_int), ("n_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class KVCache:
+    """A paged cache of keys and values over tensors of the caller
+    (include/bqgemv.h, bqg_kv_cache): k, v [n_pages, n_kv, page_size, row]
+    with rows of head_dim bf16 values (BF16), head_dim int8 codes (Q8_0) or
+    head_dim / 2 uint8 code pairs (Q4_0); k_scale, v_scale
+    [n_pages, n_kv, page_size, head_dim / 32] fp16 for the quantized formats.
+    Keeps the tensors alive; the shapes are checked once, here."""
+
+    def __init__(self, fmt: int, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        if fmt not in _KV_DTYPE:
+            raise ValueError("fmt must be BF16, Q8_0 or Q4_0")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must both be [n_pages, n_kv, page_size, row]")
+        n_pages, n_kv, page, row = k.shape
+        self.fmt, self.n_pages, self.n_kv, self.page_size = fmt, n_pages, n_kv, page
+        self.head_dim = 2 * row if fmt == Q4_0 else row
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        ptrs = [_dev(k, "k", _KV_DTYPE[fmt]), _dev(v, "v", _KV_DTYPE[fmt])]
+        if fmt != BF16:
+            shape = (n_pages, n_kv, page, self.head_dim // QK)
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if t is None or tuple(t.shape) != shape:
+                    raise ValueError(f"{name} must be {list(shape)}")
+                ptrs.append(_dev(t, name, torch.float16))
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a BF16 cache has no scales")
+        self._struct = _KVCacheStruct(fmt, page, n_kv, self.head_dim, n_pages, *ptrs)
+        self._ptr = ctypes.addressof(self._struct)
+        self.device_index = k.device.index
+
+    def _handle(self) -> int:
+        check_device(self.device_index, _current_device(), "cache")
+        return self._ptr
+
+
+def kv_cache(fmt: int, n_pages: int, n_kv: int, page_size: int, head_dim: int, device="cuda") -> KVCache:
+    """A zero-filled cache of n_pages pages."""
+    if fmt not in _KV_DTYPE:
+        raise ValueError("fmt must be BF16, Q8_0 or Q4_0")
+    row = head_dim // 2 if fmt == Q4_0 else head_dim
+    t = [torch.zeros((n_pages, n_kv, page_size, row), dtype=_KV_DTYPE[fmt], device=device) for _ in range(2)]
+    if fmt != BF16:
+        t += [torch.zeros((n_pages, n_kv, page_size, head_dim // QK), dtype=torch.float16, device=device)
+              for _ in range(2)]
+    return KVCache(fmt, *t)
+
+
+_X_DTYPE = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _tokens(t: torch.Tensor, name: str, heads: int | None = None, dim: int | None = None, T: int | None = None,
+            dtype=None):
+    """(pointer, token stride) of [tokens, heads, head_dim] rows whose tokens
+    may lie apart (a part of a fused projection's rows)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    check_device(t.device.index, _current_device(), name)
+    return t.data_ptr(), _token_stride(t, name, heads, dim, T, dtype)
+
+
+def _token_stride(t, name, heads, dim, T, dtype):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (dim is not None and d != dim) or (T is not None and n != T):
+        raise ValueError(f"{name} is {list(t.shape)}, needs [{'T' if T is None else T}, "
+                         f"{'heads' if heads is None else heads}, {'head_dim' if dim is None else dim}]")
+    s = t.stride()
+    if t.numel() and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+        raise ValueError(f"each token's heads of {name} must be contiguous")
+    return s[0] if n > 1 else h * d
+
+
+def _rotation(pos, table, T):
+    if table is None:
+        if pos is not None:
+            raise ValueError("pos without table")
+        return None, None, 0, 0
+    if table.dim() != 2:
+        raise ValueError("table must be [n_pos, rot_dim]")
+    return (_vector(pos, "pos", torch.int32, T), _dev(table, "table", torch.float32), table.shape[0], table.shape[1])
+
+
+def _vector(t, name, dtype, n):
+    p = _dev(t, name, dtype)
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} values, needs {n}")
+    return p
+
+
+def _gains(gamma_q, gamma_k, eps, dim):
+    if eps is None:
+        if gamma_q is not None or gamma_k is not None:
+            raise ValueError("gamma without eps (no norm)")
+        return 0, None, None, 0.0
+    return (1, None if gamma_q is None else _vector(gamma_q, "gamma_q", torch.float32, dim),
+            None if gamma_k is None else _vector(gamma_k, "gamma_k", torch.float32, dim), float(eps))
+
+
+def qk_norm_rope(q, k, pos=None, table=None, gamma_q=None, gamma_k=None, eps=None, interleaved=False, out=None,
+                 stream=None):
+    """Per-head RMSNorm (when eps is given) and rotation (when a table is) of
+    queries [T, n_q, head_dim] and keys [T, n_kv, head_dim], bf16 or fp32,
+    tokens possibly apart.  table: fp32 [n_pos, rot_dim], cos of the pair
+    angles then their sines; pos: int32 [T].  Returns (q, k) in bf16."""
+    T, n_q, dim = q.shape
+    n_kv = k.shape[1]
+    dt = _X_DTYPE.get(q.dtype)
+    if dt is None:
+        raise TypeError("q must be bf16 or fp32")
+    qp, qs = _tokens(q, "q")
+    kp, ks = _tokens(k, "k", dim=dim, T=T, dtype=q.dtype)
+    norm, gq, gk, eps = _gains(gamma_q, gamma_k, eps, dim)
+    pp, tp, n_pos, rot = _rotation(pos, table, T)
+    if out is None:
+        out = (torch.empty((T, n_q, dim), dtype=torch.bfloat16, device=q.device),
+               torch.empty((T, n_kv, dim), dtype=torch.bfloat16, device=q.device))
+    _check(load().bqg_qk_norm_rope(qp, kp, dt, qs, ks, T, n_q, n_kv, dim, norm, gq, gk, eps, pp, tp, n_pos, rot,
+                                   1 if interleaved else 0, _dev(out[0], "out[0]", torch.bfloat16, T * n_q * dim * 2),
+                                   _dev(out[1], "out[1]", torch.bfloat16, T * n_kv * dim * 2), _stream(stream)),
+           "bqg_qk_norm_rope")
+    return out
+
+
+def qk_norm_rope_kv_write(q, k, v, slots, cache: KVCache, pos=None, table=None, gamma_q=None, gamma_k=None, eps=None,
+                          interleaved=False, out=None, stream=None):
+    """qk_norm_rope with the keys, and the values v, going into `cache` at
+    int64 `slots` (page * page_size + place; negative: not stored) in the same
+    launch.  Returns the queries in bf16."""
+    T, n_q, dim = q.shape
+    dt = _X_DTYPE.get(q.dtype)
+    if dt is None:
+        raise TypeError("q must be bf16 or fp32")
+    qp, qs = _tokens(q, "q", dim=cache.head_dim)
+    kp, ks = _tokens(k, "k", cache.n_kv, dim, T, q.dtype)
+    vp, vs = _tokens(v, "v", cache.n_kv, dim, T, q.dtype)
+    norm, gq, gk, eps = _gains(gamma_q, gamma_k, eps, dim)
+    pp, tp, n_pos, rot = _rotation(pos, table, T)
+    if out is None:
+        out = torch.empty((T, n_q, dim), dtype=torch.bfloat16, device=q.device)
+    _check(load().bqg_qk_norm_rope_kv_write(qp, kp, vp, dt, qs, ks, vs, T, n_q, norm, gq, gk, eps, pp, tp, n_pos, rot,
+                                            1 if interleaved else 0,
+                                            _dev(out, "out", torch.bfloat16, T * n_q * dim * 2),
+                                            _vector(slots, "slots", torch.int64, T), cache._handle(), _stream(stream)),
+           "bqg_qk_norm_rope_kv_write")
+    return out
+
+
+def kv_write(k, v, slots, cache: KVCache, stream=None) -> None:
+    """Keys and values [T, n_kv, head_dim] (bf16 or fp32) into `cache` at `slots`."""
+    dt = _X_DTYPE.get(k.dtype)
+    if dt is None:
+        raise TypeError("k must be bf16 or fp32")
+    T = k.shape[0]
+    kp, ks = _tokens(k, "k", cache.n_kv, cache.head_dim)
+    vp, vs = _tokens(v, "v", cache.n_kv, cache.head_dim, T, k.dtype)
+    _check(load().bqg_kv_write(kp, vp, dt, ks, vs, T, _vector(slots, "slots", torch.int64, T), cache._handle(),
+                               _stream(stream)), "bqg_kv_write")
+
+
+def kv_read(cache: KVCache, slots, dtype=torch.bfloat16, out=None, stream=None):
+    """The cache's keys and values at `slots`, each [T, n_kv, head_dim] bf16
+    or fp32; a negative slot reads as zeros."""
+    T = slots.numel()
+    dt = _X_DTYPE.get(dtype)
+    if dt is None:
+        raise TypeError("dtype must be bf16 or fp32")
+    if out is None:
+        out = tuple(torch.empty((T, cache.n_kv, cache.head_dim), dtype=dtype, device=slots.device) for _ in range(2))
+    n = T * cache.n_kv * cache.head_dim * dtype.itemsize
+    _check(load().bqg_kv_read(cache._handle(), _vector(slots, "slots", torch.int64, T), T, dt,
+                              _dev(out[0], "out[0]", dtype, n), _dev(out[1], "out[1]", dtype, n), _stream(stream)),
+           "bqg_kv_read")
+    return out
+
+
+def tree_attention_workspace(cache: KVCache, n_q: int, n_seq: int, max_q: int) -> torch.Tensor:
+    """A zero-filled workspace for tree_attention calls of these sizes."""
+    n = int(load().bqg_tree_attention_workspace_size(cache._handle(), n_q, n_seq, max_q))
+    if n == 0:
+        raise ValueError("not a tree_attention call on this device")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def tree_attention(q, cache: KVCache, block_table, ctx_len, q_start, max_q: int, mask=None, scale=None, out=None,
+                   ws=None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's newest tokens (at most max_q <= 64 each)
+    over its ctx_len context tokens and themselves, all already in `cache`.
+
+    q: bf16 [n_tokens, n_q, head_dim], sequence after sequence, q_start int32
+    [n_seq + 1] their first tokens; block_table int32 [n_seq, max_pages];
+    ctx_len int32 [n_seq]; mask int64 [n_tokens], bit j set where new token j
+    of the sequence is seen (a tree of drafted tokens), or None for causal;
+    scale defaults to head_dim ** -0.5.  Returns bf16 [n_tokens, n_q, head_dim]."""
+    n, n_q, dim = q.shape
+    qp, qs = _tokens(q, "q", dim=cache.head_dim, dtype=torch.bfloat16)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_seq, max_pages]")
+    n_seq, max_pages = block_table.shape
+    if out is None:
+        out = torch.empty((n, n_q, dim), dtype=torch.bfloat16, device=q.device)
+    wsp, wsb = _ws(ws)
+    _check(load().bqg_tree_attention(qp, qs, cache._handle(), _dev(block_table, "block_table", torch.int32), max_pages,
+                                     _vector(ctx_len, "ctx_len", torch.int32, n_seq),
+                                     _vector(q_start, "q_start", torch.int32, n_seq + 1), n_seq, n, max_q, n_q,
+                                     None if mask is None else _vector(mask, "mask", torch.int64, n),
+                                     dim ** -0.5 if scale is None else float(scale),
+                                     _dev(out, "out", torch.bfloat16, n * n_q * dim * 2), wsp, wsb, _stream(stream)),
+           "bqg_tree_attention")
+    return out
 
 
 # --- utilities -----------------------------------------------------------------

@@ -11,6 +11,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "bqg_attn_launch.cuh"
 #include "bqg_gemv.cuh"
 #include "bqg_gemv_mma.cuh"
 
@@ -51,6 +52,12 @@ cudaError_t launch_splitk_reduce(const GemvParams &, int, int, int, cudaStream_t
 int gemm_bf16(int, const void *, const void *, float *, int, int64_t, int64_t, cudaStream_t, int);
 size_t gemm_workspace(int, int64_t, int64_t);
 int gemm_read_error(cudaStream_t, int *);
+cudaError_t attn_launch_bf16(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
+cudaError_t attn_launch_q8_0(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
+cudaError_t attn_launch_q4_0(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
+cudaError_t attn_take_error_bf16(int *);
+cudaError_t attn_take_error_q8_0(int *);
+cudaError_t attn_take_error_q4_0(int *);
 }  // namespace bqg
 
 using namespace bqg;
@@ -705,6 +712,88 @@ int gemv_plain(int wf, int xf, int fmt, const void *Wp, const void *X, float *Y,
     return run_gemv(wf, xf, p, M, K, EPI_STORE, ws, ws_bytes, stream);
 }
 
+// ---- paged cache ----------------------------------------------------------
+bool valid_head_dim(int D) { return D == 64 || D == 128 || D == 256; }
+
+// The cache a caller described, checked, as the kernels take it.
+int check_cache(const bqg_kv_cache *c, KvCacheDev *out)
+{
+    if (!c || (c->fmt != BQG_BF16 && c->fmt != BQG_Q8_0 && c->fmt != BQG_Q4_0)) return BQG_ERR_INVALID_ARG;
+    const bool scales = c->fmt != BQG_BF16;
+    if (!c->k || !c->v || (scales && (!c->k_scale || !c->v_scale))) return BQG_ERR_INVALID_ARG;
+    if (c->n_kv < 1 || c->n_pages < 1) return BQG_ERR_INVALID_ARG;
+    if (!valid_head_dim(c->head_dim) || c->n_kv > 1024) return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1))) return BQG_ERR_UNSUPPORTED_SHAPE;
+    int lp = 4;
+    while ((1 << lp) < c->page_size) lp++;
+    if (c->n_pages > ((int64_t)1 << 40 >> lp)) return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(c->k) || !aligned16(c->v) || (scales && (!aligned16(c->k_scale) || !aligned16(c->v_scale))))
+        return BQG_ERR_MISALIGNED;
+    *out = KvCacheDev{(uint8_t *)c->k, (uint8_t *)c->v, (uint16_t *)c->k_scale, (uint16_t *)c->v_scale, c->n_pages,
+                      c->n_kv, lp};
+    return BQG_OK;
+}
+
+// Token strides in values: at least a token's own, and whole 16-byte pieces.
+int check_tokens(const void *x, int64_t stride, int heads, int D, int x_dtype)
+{
+    const int64_t own = (int64_t)heads * D;
+    if (stride < own || stride > ((int64_t)1 << 40)) return BQG_ERR_INVALID_ARG;
+    if (!aligned16(x) || stride % (x_dtype == BQG_F32 ? 4 : 8)) return BQG_ERR_MISALIGNED;
+    return BQG_OK;
+}
+
+int check_norm_rope(const NormRopeParams &p, int D)
+{
+    if (p.norm != 0 && p.norm != 1) return BQG_ERR_INVALID_ARG;
+    if (p.norm && (!(p.eps >= 0.0f) || !std::isfinite(p.eps))) return BQG_ERR_INVALID_ARG;
+    if (p.interleaved != 0 && p.interleaved != 1) return BQG_ERR_INVALID_ARG;
+    if (p.rot < 0 || p.rot > D || p.rot % 16) return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (p.rot && (!p.table || (!p.pos && p.T) || p.n_pos < 1)) return BQG_ERR_INVALID_ARG;
+    if ((p.norm && p.gamma_q && !aligned16(p.gamma_q)) || (p.norm && p.gamma_k && !aligned16(p.gamma_k)) ||
+        (p.rot && (!aligned16(p.table) || !aligned(p.pos, 4))))
+        return BQG_ERR_MISALIGNED;
+    return BQG_OK;
+}
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 31;
+
+// The checked parameters of a tree attention call, except its workspace.
+int attn_params(const void *q, int64_t q_stride, const bqg_kv_cache *cache, const int32_t *block_table, int64_t max_pages,
+                const int32_t *ctx_len, const int32_t *q_start, int n_seq, int64_t n_tokens, int max_q, int n_q,
+                const uint64_t *mask, float scale, void *out, AttnParams *p)
+{
+    if (int st = check_cache(cache, &p->cache)) return st;
+    if (n_seq < 0 || n_tokens < 0 || max_q < 1 || max_pages < 1 || n_q < 1 || n_q % cache->n_kv) return BQG_ERR_INVALID_ARG;
+    if (max_q > 64 || n_q / cache->n_kv > 64 || n_tokens > (int64_t)64 * n_seq || max_pages > ((int64_t)1 << 31) ||
+        n_tokens >= kMaxTokens)
+        return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return BQG_ERR_INVALID_ARG;
+    p->q = (const uint16_t *)q;
+    p->q_stride = q_stride;
+    p->table = block_table;
+    p->max_pages = max_pages;
+    p->ctx_len = ctx_len;
+    p->q_start = q_start;
+    p->n_seq = n_seq;
+    p->n_tokens = n_tokens;
+    p->max_q = max_q;
+    p->n_q = n_q;
+    p->group = n_q / cache->n_kv;
+    p->mask = (const unsigned long long *)mask;
+    p->scale_log2 = scale * 1.44269504f;
+    p->out = (uint16_t *)out;
+    return BQG_OK;
+}
+
+cudaError_t attn_run(int fmt, const AttnParams &p, int D, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    const int rows = p.max_q * p.group;
+    return fmt == BQG_BF16 ? attn_launch_bf16(p, D, rows, plan, s, pdl)
+         : fmt == BQG_Q8_0 ? attn_launch_q8_0(p, D, rows, plan, s, pdl)
+                           : attn_launch_q4_0(p, D, rows, plan, s, pdl);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1050,6 +1139,126 @@ int bqg_debug_q4_0_q8_1_block_dots_kslice(const void *Wp, const void *Xq, int32_
     return cuda_status(launch_block_dots(Wp, Xq, dots, N, K, repacked_row_bytes(BQG_Q4_0, K), stream));
 }
 
+int bqg_qk_norm_rope(const void *q, const void *k, int x_dtype, int64_t q_stride, int64_t k_stride, int64_t T, int n_q,
+                     int n_kv, int head_dim, int norm, const float *gamma_q, const float *gamma_k, float eps,
+                     const int32_t *pos, const float *table, int64_t n_pos, int rot_dim, int interleaved, void *q_out,
+                     void *k_out, cudaStream_t stream)
+{
+    if (T < 0 || n_q < 0 || n_kv < 0 || (x_dtype != BQG_BF16 && x_dtype != BQG_F32)) return BQG_ERR_INVALID_ARG;
+    if (T && ((n_q && (!q || !q_out)) || (n_kv && (!k || !k_out)))) return BQG_ERR_INVALID_ARG;
+    if (!valid_head_dim(head_dim) || n_q > 1024 || n_kv > 1024 || T >= kMaxTokens) return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (n_q)
+        if (int st = check_tokens(q, q_stride, n_q, head_dim, x_dtype)) return st;
+    if (n_kv)
+        if (int st = check_tokens(k, k_stride, n_kv, head_dim, x_dtype)) return st;
+    if ((n_q && !aligned16(q_out)) || (n_kv && !aligned16(k_out))) return BQG_ERR_MISALIGNED;
+    NormRopeParams p{};
+    p.q = q; p.k = n_kv ? k : nullptr;
+    p.x_f32 = x_dtype == BQG_F32;
+    p.q_stride = q_stride; p.k_stride = k_stride;
+    p.T = T; p.n_q = n_q; p.n_kv = n_kv;
+    p.norm = norm; p.gamma_q = gamma_q; p.gamma_k = gamma_k; p.eps = eps;
+    p.pos = pos; p.table = table; p.n_pos = n_pos; p.rot = rot_dim; p.interleaved = interleaved;
+    p.q_out = (uint16_t *)q_out; p.k_out = (uint16_t *)k_out;
+    if (int st = check_norm_rope(p, head_dim)) return st;
+    DevInfo dev;
+    if (int st = current_device(&dev)) return st;
+    return cuda_status(launch_norm_rope(p, BQG_BF16, head_dim, dev.sms, stream, g_pdl.load() != 0));
+}
+
+int bqg_qk_norm_rope_kv_write(const void *q, const void *k, const void *v, int x_dtype, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int64_t T, int n_q, int norm, const float *gamma_q,
+                              const float *gamma_k, float eps, const int32_t *pos, const float *table, int64_t n_pos,
+                              int rot_dim, int interleaved, void *q_out, const int64_t *slots,
+                              const bqg_kv_cache *cache, cudaStream_t stream)
+{
+    NormRopeParams p{};
+    if (int st = check_cache(cache, &p.cache)) return st;
+    const int D = cache->head_dim;
+    if (T < 0 || n_q < 0 || (x_dtype != BQG_BF16 && x_dtype != BQG_F32)) return BQG_ERR_INVALID_ARG;
+    if (T && (!k || !v || !slots || (n_q && (!q || !q_out)))) return BQG_ERR_INVALID_ARG;
+    if (n_q > 1024 || T >= kMaxTokens) return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (n_q)
+        if (int st = check_tokens(q, q_stride, n_q, D, x_dtype)) return st;
+    if (int st = check_tokens(k, k_stride, cache->n_kv, D, x_dtype)) return st;
+    if (int st = check_tokens(v, v_stride, cache->n_kv, D, x_dtype)) return st;
+    if ((n_q && !aligned16(q_out)) || !aligned(slots, 8)) return BQG_ERR_MISALIGNED;
+    p.q = q; p.k = k; p.v = v;
+    p.x_f32 = x_dtype == BQG_F32;
+    p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.T = T; p.n_q = n_q; p.n_kv = cache->n_kv;
+    p.norm = norm; p.gamma_q = gamma_q; p.gamma_k = gamma_k; p.eps = eps;
+    p.pos = pos; p.table = table; p.n_pos = n_pos; p.rot = rot_dim; p.interleaved = interleaved;
+    p.q_out = (uint16_t *)q_out;
+    p.slots = slots;
+    if (int st = check_norm_rope(p, D)) return st;
+    DevInfo dev;
+    if (int st = current_device(&dev)) return st;
+    return cuda_status(launch_norm_rope(p, cache->fmt, D, dev.sms, stream, g_pdl.load() != 0));
+}
+
+int bqg_kv_write(const void *k, const void *v, int x_dtype, int64_t k_stride, int64_t v_stride, int64_t T,
+                 const int64_t *slots, const bqg_kv_cache *cache, cudaStream_t stream)
+{
+    return bqg_qk_norm_rope_kv_write(nullptr, k, v, x_dtype, 0, k_stride, v_stride, T, 0, 0, nullptr, nullptr, 0.0f,
+                                     nullptr, nullptr, 0, 0, 0, nullptr, slots, cache, stream);
+}
+
+int bqg_kv_read(const bqg_kv_cache *cache, const int64_t *slots, int64_t T, int out_dtype, void *k_out, void *v_out,
+                cudaStream_t stream)
+{
+    KvReadParams p{};
+    if (int st = check_cache(cache, &p.cache)) return st;
+    if (T < 0 || (out_dtype != BQG_BF16 && out_dtype != BQG_F32) || (T && (!slots || !k_out || !v_out)))
+        return BQG_ERR_INVALID_ARG;
+    if (T >= kMaxTokens) return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(slots, 8) || !aligned16(k_out) || !aligned16(v_out)) return BQG_ERR_MISALIGNED;
+    p.slots = slots;
+    p.T = T;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    DevInfo dev;
+    if (int st = current_device(&dev)) return st;
+    return cuda_status(launch_kv_read(p, cache->fmt, cache->head_dim, out_dtype == BQG_F32, dev.sms, stream, g_pdl.load() != 0));
+}
+
+int bqg_tree_attention(const void *q, int64_t q_stride, const bqg_kv_cache *cache, const int32_t *block_table,
+                       int64_t max_pages, const int32_t *ctx_len, const int32_t *q_start, int n_seq, int64_t n_tokens,
+                       int max_q, int n_q, const uint64_t *mask, float scale, void *out, void *ws, size_t ws_bytes,
+                       cudaStream_t stream)
+{
+    AttnParams p{};
+    if (int st = attn_params(q, q_stride, cache, block_table, max_pages, ctx_len, q_start, n_seq, n_tokens, max_q, n_q,
+                             mask, scale, out, &p))
+        return st;
+    if (n_tokens && (!q || !out || !block_table || !ctx_len || !q_start)) return BQG_ERR_INVALID_ARG;
+    const int D = cache->head_dim;
+    if (n_tokens)
+        if (int st = check_tokens(q, q_stride, n_q, D, BQG_BF16)) return st;
+    if (!aligned16(out) || !aligned(block_table, 4) || !aligned(ctx_len, 4) || !aligned(q_start, 4) || !aligned(mask, 8) ||
+        !aligned16(ws))
+        return BQG_ERR_MISALIGNED;
+    DevInfo dev;
+    if (int st = current_device(&dev)) return st;
+    if (n_tokens == 0) return BQG_OK;
+    AttnPlan plan;
+    if (cudaError_t e = attn_run(cache->fmt, p, D, &plan, stream, false)) return cuda_status(e);
+    if (!ws || ws_bytes < plan.ws_bytes) return BQG_ERR_WORKSPACE;
+    p.counters = (int *)ws;
+    return cuda_status(attn_run(cache->fmt, p, D, nullptr, stream, g_pdl.load() != 0));
+}
+
+size_t bqg_tree_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int n_seq, int max_q)
+{
+    AttnParams p{};
+    DevInfo dev;
+    if (attn_params(nullptr, 0, cache, nullptr, 1, nullptr, nullptr, n_seq, 0, max_q, n_q, nullptr, 1.0f, nullptr, &p) ||
+        current_device(&dev))
+        return 0;
+    AttnPlan plan;
+    return attn_run(cache->fmt, p, cache->head_dim, &plan, 0, false) == cudaSuccess ? plan.ws_bytes : 0;
+}
+
 size_t bqg_workspace_size(int op, int M, int64_t N, int64_t K)
 {
     if (N <= 0 || K <= 0 || K % QK || K > kMaxK) return 0;
@@ -1126,7 +1335,8 @@ int bqg_last_device_error(cudaStream_t stream, int *out)
     int word = 0;
     if (int st = gemm_read_error(stream, &word)) return st;
     int w = 0;
-    for (auto fn : {gemv_error_bf16, gemv_error_q8_0, gemv_error_q4_0, gemv_error_q4_0_q8_1, layer_take_error}) {
+    for (auto fn : {gemv_error_bf16, gemv_error_q8_0, gemv_error_q4_0, gemv_error_q4_0_q8_1, layer_take_error, kv_take_error,
+                    attn_take_error_bf16, attn_take_error_q8_0, attn_take_error_q4_0}) {
         if (fn(&w) != cudaSuccess) return BQG_ERR_CUDA;
         word |= w;
     }

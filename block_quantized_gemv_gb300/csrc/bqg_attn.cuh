@@ -1,0 +1,816 @@
+// bqg_attn.cuh -- attention of each sequence's newest tokens over a paged cache.
+//
+//   out[i, h] = sum_j p_j v_j,   p = softmax over the visible j of scale * q[i, h] . k_j
+//
+// The rows that share a KV head (new tokens x query heads of the group)
+// share its keys and values, so a unit of work is (sequence, KV head, row
+// tile, 64 cached tokens), and the floor is reading every cached row once:
+// with few rows the kernel streams.
+//
+//  * Work is split evenly: the units of all sequences in one line, each CTA a
+//    contiguous range of them, so ragged lengths and few (sequence, head)
+//    pairs fill the GPU alike.  A range that begins or ends inside a
+//    (sequence, head, row tile) leaves a partial result (maximum, sum,
+//    unnormalised output rows) in the workspace; the CTA whose counted
+//    arrival completes the set joins it, in the order of the ranges, so the
+//    bits do not depend on timing.
+//  * Each warp feeds itself: of a unit's 64 tokens it takes 16 (a strip, always
+//    inside one page), copied with cp.async into its own ring, 16-byte
+//    chunks permuted so that fragment loads meet no bank conflicts.
+//    Tokens behind a sequence's end are filled with zeros, never read.
+//  * The products go to the tensor cores (mma.sync m16n8k16, fp32
+//    accumulate), rows as the M side in tiles of 16, tokens as N of the
+//    first product and K of the second, so the probabilities go from one
+//    product's accumulators to the other's operand in registers.
+//    bf16: as stored.  q8_0 / q4_0: the codes are built as exact fp16 integers
+//    (a byte under 0x64 is 1024 + byte); a key block's two products give an
+//    exact block sum that is scaled by its fp16 scale in fp32; a value is
+//    q d rounded once to fp16 (relative 2^-12).  The queries then are fp16
+//    too: each row is scaled by a power of two (exact) so that its largest
+//    value lies in [1, 2), which keeps a bf16 value's eight bits down to 2^-16
+//    of the largest; the power goes into the row's softmax scale.
+//  * The running maximum is raised only when a score exceeds it by more than
+//    kSlack (in powers of two), so the common strip needs no exchange between
+//    lanes and no rescaling.  Probabilities relative to that maximum are at
+//    most 2^kSlack; for fp16 they carry a factor 2^kShift, which keeps ten
+//    bits down to 2^-22 of the maximum and cancels in the division.
+#pragma once
+
+#include "bqg_kv.cuh"
+
+namespace bqg {
+
+constexpr int kAttnWarps = 4;            // warps per CTA
+constexpr int kStrip = 16;               // tokens per warp and unit
+constexpr int kUnit = kAttnWarps * kStrip;
+constexpr float kSlack = 6.0f;
+
+struct AttnParams {
+    const uint16_t *q;                   // bf16
+    int64_t q_stride;
+    KvCacheDev cache;
+    const int32_t *table;                // [n_seq][max_pages]
+    int64_t max_pages;
+    const int32_t *ctx_len, *q_start;
+    int n_seq;
+    int64_t n_tokens;
+    int max_q, n_q, group;               // group = n_q / n_kv
+    const unsigned long long *mask;
+    float scale_log2;                    // scale * log2(e)
+    uint16_t *out;                       // bf16 [n_tokens][n_q][D]
+    int *counters;                       // one per CTA, zero between calls
+    float *part;                         // [2 * CTAs][rows of a tile][D], then (maximum, sum) pairs
+};
+
+// Geometry of one instantiation: MT row tiles of 16 per CTA.
+template <int FMT, int D, int MT> struct AttnGeom {
+    static constexpr int ROWS = 16 * MT;
+    static constexpr int RB = KvRow<FMT, D>::BYTES;                     // bytes of a cached row
+    static constexpr int NB = D / QK;                                   // blocks of a row
+    static constexpr int CPT = RB / 16;                                 // 16-byte chunks of a row
+    static constexpr int SCALES = (FMT == BQG_BF16) ? 0 : kStrip * NB * 2;
+    static constexpr int STAGE = 2 * (kStrip * RB + SCALES);            // keys and values of a strip
+    // strips in flight per warp: about 64 KiB per SM and CTA pair or trio (see attn_stages)
+    static constexpr int S = (STAGE >= 16384) ? 3 : (STAGE >= 8192) ? 3 : (STAGE >= 4096) ? 4 : 6;
+    static constexpr int KS = D / 16;                                   // MMA steps of the first product
+    static constexpr bool QREG = MT * D <= 128;                         // query fragments held in registers
+    static constexpr int PAD = 16;                                      // floats between merged rows
+    static constexpr int RING = kAttnWarps * S * STAGE;
+    static constexpr int MERGE = kAttnWarps * ROWS * (D + PAD) * 4;     // the ring's memory again, once drained
+    static constexpr int OFF_Q = (RING > MERGE ? RING : MERGE);         // query fragments
+    static constexpr int OFF_P = OFF_Q + (QREG ? 0 : MT * KS * 512);    // probabilities of the exact path
+    static constexpr int OFF_ML = OFF_P + kAttnWarps * 16 * kStrip * 4; // (maximum, sum) per warp and row
+    static constexpr int OFF_RS = OFF_ML + kAttnWarps * ROWS * 8;       // softmax scale per row
+    static constexpr int OFF_FLAG = OFF_RS + ROWS * 4;
+    static constexpr int SMEM = OFF_FLAG + 16;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) { uint32_t v; asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory"); return v; }
+__device__ __forceinline__ uint2 lds64(uint32_t a) { uint2 v; asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory"); return v; }
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+template <bool BF> __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool BF> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) { uint32_t r; asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b)); return r; }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { uint32_t r; asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b)); return r; }
+__device__ __forceinline__ float ex2(float x) { float r; asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x)); return r; }
+
+// Chunk c of token `tok` in a staged strip: the position of its 16 bytes.
+// Eight consecutive tokens' chunk c, and the chunk pairs (2i, 2i + 1) of
+// four consecutive tokens, lie in distinct banks.
+template <int CPT> __device__ __forceinline__ uint32_t chunk_at(int tok, int c)
+{
+    int f;
+    if constexpr (CPT >= 8) f = ((tok & 3) << 1) | ((tok >> 2) & 1);
+    else if constexpr (CPT == 4) f = (tok & 2) | ((tok >> 2) & 1);
+    else f = (tok >> 2) & 1;
+    return (uint32_t)(tok * CPT + (c ^ f)) * 16;
+}
+
+// One sequence as the kernel works on it.
+struct AttnSeq {
+    int b, q0, T, ctx, len;      // first query token, new tokens, context and all cached tokens
+    int tiles, row_tiles;
+};
+
+template <int FMT, int D, int MT> struct AttnKernel {
+    using G = AttnGeom<FMT, D, MT>;
+    static constexpr bool BF = (FMT == BQG_BF16);
+    static constexpr float kShift = BF ? 0.0f : 8.0f;
+    static constexpr int NT = D / 8;                          // n-tiles of the output
+
+    // Sequence b with its lengths made to fit; `bad` collects BQG_DEVERR_LENGTH.
+    static __device__ __forceinline__ AttnSeq load_seq(const AttnParams &p, int b, int &bad)
+    {
+        AttnSeq s;
+        s.b = b;
+        const int64_t cap = min((int64_t)0x7fff0000, p.max_pages << p.cache.lp);
+        const int64_t a = p.q_start[b], e = p.q_start[b + 1], c = p.ctx_len[b];
+        const int64_t q0 = min(max(a, (int64_t)0), p.n_tokens), q1 = min(max(e, q0), p.n_tokens);
+        const int64_t T = min(q1 - q0, (int64_t)p.max_q);
+        const int64_t ctx = min(max(c, (int64_t)0), max(cap - T, (int64_t)0));
+        if (q0 != a || q1 != e || T != q1 - q0 || ctx != c || T > cap) bad |= BQG_DEVERR_LENGTH;
+        s.q0 = (int)q0; s.T = (int)T; s.ctx = (int)ctx;
+        s.len = (int)min(ctx + T, cap);
+        s.tiles = T > 0 ? (s.len + kUnit - 1) / kUnit : 0;
+        s.row_tiles = ((int)T * p.group + G::ROWS - 1) / G::ROWS;
+        return s;
+    }
+    static __device__ __forceinline__ int64_t units(const AttnParams &p, const AttnSeq &s)
+    {
+        return (int64_t)p.cache.n_kv * s.row_tiles * s.tiles;
+    }
+
+    // One query value pair of row (token, head) in fp32.
+    static __device__ __forceinline__ const uint16_t *q_row(const AttnParams &p, const AttnSeq &s, int h, int row)
+    {
+        const int i = row / p.group, hh = row - i * p.group;
+        return (i < s.T) ? p.q + (s.q0 + i) * p.q_stride + (int64_t)(h * p.group + hh) * D : nullptr;
+    }
+
+    // The query fragments of row tile rows row0 .. row0 + 15 (KS steps x 4
+    // registers), and the softmax scales of this lane's two rows.
+    static __device__ __forceinline__ void load_q(const AttnParams &p, const AttnSeq &s, int h, int row0, int lane,
+                                                  uint32_t (&qf)[G::KS][4], float (&rs)[2])
+    {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            const uint16_t *src = q_row(p, s, h, row0 + g + 8 * r);
+            rs[r] = p.scale_log2;
+            if constexpr (BF) {
+#pragma unroll
+                for (int ks = 0; ks < G::KS; ks++) {
+                    qf[ks][r] = src ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t) : 0u;
+                    qf[ks][2 + r] = src ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 8 + 2 * t) : 0u;
+                }
+            } else {
+                // the order of the values within a block follows the codes' words:
+                // q8_0 lane t values 8t .. 8t + 7; q4_0 values 4t .. and 16 + 4t ..,
+                // even ones first
+                uint32_t w[G::NB][4];
+                float top = 0.f;
+#pragma unroll
+                for (int b = 0; b < G::NB; b++) {
+                    if constexpr (FMT == BQG_Q8_0) {
+                        const uint4 a = src ? *reinterpret_cast<const uint4 *>(src + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
+                        w[b][0] = a.x; w[b][1] = a.y; w[b][2] = a.z; w[b][3] = a.w;
+                    } else {
+                        const uint2 a = src ? *reinterpret_cast<const uint2 *>(src + 32 * b + 4 * t) : make_uint2(0, 0);
+                        const uint2 c = src ? *reinterpret_cast<const uint2 *>(src + 32 * b + 16 + 4 * t) : make_uint2(0, 0);
+                        w[b][0] = __byte_perm(a.x, a.y, 0x5410); w[b][1] = __byte_perm(a.x, a.y, 0x7632);
+                        w[b][2] = __byte_perm(c.x, c.y, 0x5410); w[b][3] = __byte_perm(c.x, c.y, 0x7632);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; j++) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[b][j])), fabsf(bf16_hi(w[b][j]))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                float inv = 1.f;
+                if (top > 0.f && top < __int_as_float(0x7f800000)) {
+                    const uint32_t ex = min(__float_as_uint(top) >> 23, 253u);
+                    inv = __uint_as_float((254u - ex) << 23);                       // 2^(127 - ex)
+                    rs[r] = fmaxf(p.scale_log2 * (1.0f / inv), 1.17549435e-38f);    // 1 / inv: a power of two
+                }
+#pragma unroll
+                for (int b = 0; b < G::NB; b++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const uint32_t f = pack2<false>(bf16_lo(w[b][j]) * inv, bf16_hi(w[b][j]) * inv);
+                        qf[2 * b + (j >> 1)][r + 2 * (j & 1)] = f;
+                    }
+            }
+        }
+    }
+
+    // Copies of strip tokens tok0 .. tok0 + 15 of (sequence, head) into `st`.
+    static __device__ __forceinline__ void issue(const AttnParams &p, const AttnSeq &s, int h, int tok0, int page, bool ok,
+                                                 uint32_t st, int lane)
+    {
+        const int at = tok0 & ((1 << p.cache.lp) - 1);
+        const int64_t row = ok ? ((((int64_t)page * p.cache.n_kv + h) << p.cache.lp) + at) : 0;
+        const int n = ok ? min(kStrip, s.len - tok0) : 0;                        // tokens to fetch
+        const uint8_t *k = p.cache.k + row * G::RB, *v = p.cache.v + row * G::RB;
+#pragma unroll
+        for (int i = 0; i < G::CPT / 2; i++) {
+            const int x = i * 32 + lane, tok = x / G::CPT, c = x % G::CPT;
+            const uint32_t d = st + chunk_at<G::CPT>(tok, c);
+            const int bytes = tok < n ? 16 : 0;
+            cp_async16(d, k + (bytes ? x * 16 : 0), bytes);
+            cp_async16(d + kStrip * G::RB, v + (bytes ? x * 16 : 0), bytes);
+        }
+        if constexpr (!BF) {
+            constexpr int CH = G::SCALES / 16;                                   // chunks of one side's scales
+            const uint32_t d = st + 2 * kStrip * G::RB;
+            const uint8_t *ks = reinterpret_cast<const uint8_t *>(p.cache.k_scale + row * G::NB);
+            const uint8_t *vs = reinterpret_cast<const uint8_t *>(p.cache.v_scale + row * G::NB);
+            if (lane < 2 * CH) {
+                const int c = lane % CH;
+                const int bytes = min(max(n * G::NB * 2 - 16 * c, 0), 16);
+                cp_async16(d + lane * 16, (lane < CH ? ks : vs) + (bytes ? 16 * c : 0), bytes);
+            }
+        }
+    }
+
+    // Scores of the strip in stage `st` for MT row tiles: s[m][token tile][4].
+    template <typename QF> static __device__ __forceinline__ void scores(uint32_t st, int lane, const QF &qf, float (&s)[MT][2][4])
+    {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) s[m][x][i] = 0.f;
+        if constexpr (BF) {
+            const int tok = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+            for (int ks = 0; ks < G::KS; ks++) {
+                uint32_t b[4];
+                ldsm_x4(st + chunk_at<G::CPT>(tok, 2 * ks + half), b);
+#pragma unroll
+                for (int m = 0; m < MT; m++) {
+                    uint32_t a[4];
+                    qf.get(m, ks, a);
+                    mma16816<true>(s[m][0], a, b[0], b[1]);
+                    mma16816<true>(s[m][1], a, b[2], b[3]);
+                }
+            }
+        } else {
+            const uint32_t sc = st + 2 * kStrip * G::RB;
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                uint32_t dw[G::NB];                      // scales of tokens 8x + 2t (first half) and + 1
+#pragma unroll
+                for (int i = 0; i < G::NB; i += 2) {
+                    const uint2 v = lds64(sc + ((8 * x + 2 * t) * G::NB + 2 * i) * 2);
+                    dw[i] = v.x; dw[i + 1] = v.y;
+                }
+#pragma unroll
+                for (int b = 0; b < G::NB; b++) {
+                    uint32_t e[4];
+                    if constexpr (FMT == BQG_Q8_0) {
+                        uint2 w = lds64(st + chunk_at<G::CPT>(8 * x + g, 2 * b + (t >> 1)) + (t & 1) * 8);
+                        w.x ^= 0x80808080u; w.y ^= 0x80808080u;              // q + 128
+                        e[0] = hsub2(__byte_perm(w.x, 0x64646464u, 0x4140), 0x64806480u);
+                        e[1] = hsub2(__byte_perm(w.x, 0x64646464u, 0x4342), 0x64806480u);
+                        e[2] = hsub2(__byte_perm(w.y, 0x64646464u, 0x4140), 0x64806480u);
+                        e[3] = hsub2(__byte_perm(w.y, 0x64646464u, 0x4342), 0x64806480u);
+                    } else {
+                        const uint32_t w = lds32(st + chunk_at<G::CPT>(8 * x + g, b) + t * 4);
+                        e[0] = hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        e[1] = hsub2(((w >> 8) & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        e[2] = hsub2(((w >> 4) & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        e[3] = hsub2(((w >> 12) & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                    }
+                    const uint32_t h0 = dw[b >> 1], h1 = dw[(G::NB + b) >> 1];
+                    const float d0 = half_bits_to_float((b & 1) ? h0 >> 16 : h0 & 0xffffu);
+                    const float d1 = half_bits_to_float((b & 1) ? h1 >> 16 : h1 & 0xffffu);
+#pragma unroll
+                    for (int m = 0; m < MT; m++) {
+                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        uint32_t a[4];
+                        qf.get(m, 2 * b, a);
+                        mma16816<false>(acc, a, e[0], e[1]);
+                        qf.get(m, 2 * b + 1, a);
+                        mma16816<false>(acc, a, e[2], e[3]);
+                        s[m][x][0] = fmaf(acc[0], d0, s[m][x][0]);
+                        s[m][x][1] = fmaf(acc[1], d1, s[m][x][1]);
+                        s[m][x][2] = fmaf(acc[2], d0, s[m][x][2]);
+                        s[m][x][3] = fmaf(acc[3], d1, s[m][x][3]);
+                    }
+                }
+            }
+        }
+    }
+
+    // o += P V for the strip in stage `st`.
+    static __device__ __forceinline__ void add_values(uint32_t st, int lane, const uint32_t (&pa)[MT][4], float (&o)[MT][NT][4])
+    {
+        const int t = lane & 3;
+        const uint32_t vst = st + kStrip * G::RB;
+        const int tok = lane & 15, hi = lane >> 4;       // ldmatrix rows: tokens 0..15 of chunk c, then of c + 1
+        if constexpr (BF) {
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t b[4];
+                ldsm_x4_trans(vst + chunk_at<G::CPT>(tok, n + hi), b);
+#pragma unroll
+                for (int m = 0; m < MT; m++) {
+                    mma16816<true>(o[m][n], pa[m], b[0], b[1]);
+                    mma16816<true>(o[m][n + 1], pa[m], b[2], b[3]);
+                }
+            }
+        } else {
+            const uint32_t sc = st + 2 * kStrip * G::RB + G::SCALES;
+            uint32_t dw[2][G::NB];                       // scales of tokens 8x + 2t and 8x + 2t + 1
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+                for (int i = 0; i < G::NB; i += 2) {
+                    const uint2 v = lds64(sc + ((8 * x + 2 * t) * G::NB + 2 * i) * 2);
+                    dw[x][i] = v.x; dw[x][i + 1] = v.y;
+                }
+            auto pair = [&](int x, int b) {              // (scale of token 8x + 2t, of 8x + 2t + 1) of block b
+                return __byte_perm(dw[x][b >> 1], dw[x][(G::NB + b) >> 1], (b & 1) ? 0x7632 : 0x5410);
+            };
+            // sixteen values (n-tiles 2 i and 2 i + 1: even and odd ones): word lo of tokens 0..7, hi of 8..15,
+            // one biased code per byte
+            auto tiles = [&](int i, uint32_t lo, uint32_t up, uint32_t bias, uint32_t s0, uint32_t s1) {
+                const uint32_t b00 = hmul2(hsub2(__byte_perm(lo, 0x64646464u, 0x4240), bias), s0);
+                const uint32_t b01 = hmul2(hsub2(__byte_perm(up, 0x64646464u, 0x4240), bias), s1);
+                const uint32_t b10 = hmul2(hsub2(__byte_perm(lo, 0x64646464u, 0x4341), bias), s0);
+                const uint32_t b11 = hmul2(hsub2(__byte_perm(up, 0x64646464u, 0x4341), bias), s1);
+#pragma unroll
+                for (int m = 0; m < MT; m++) {
+                    mma16816<false>(o[m][2 * i], pa[m], b00, b01);
+                    mma16816<false>(o[m][2 * i + 1], pa[m], b10, b11);
+                }
+            };
+            if constexpr (FMT == BQG_Q8_0) {
+#pragma unroll
+                for (int b = 0; b < G::NB; b++) {
+                    uint32_t r[4];
+                    ldsm_x4_trans(vst + chunk_at<G::CPT>(tok, 2 * b + hi), r);
+                    const uint32_t s0 = pair(0, b), s1 = pair(1, b);
+                    tiles(2 * b, r[0] ^ 0x80808080u, r[1] ^ 0x80808080u, 0x64806480u, s0, s1);
+                    tiles(2 * b + 1, r[2] ^ 0x80808080u, r[3] ^ 0x80808080u, 0x64806480u, s0, s1);
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < G::NB; b += 2) {
+                    uint32_t r[4];
+                    ldsm_x4_trans(vst + chunk_at<G::CPT>(tok, b + hi), r);
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        const uint32_t s0 = pair(0, b + j), s1 = pair(1, b + j);
+                        tiles(2 * (b + j), r[2 * j] & 0x0f0f0f0fu, r[2 * j + 1] & 0x0f0f0f0fu, 0x64086408u, s0, s1);
+                        tiles(2 * (b + j) + 1, (r[2 * j] >> 4) & 0x0f0f0f0fu, (r[2 * j + 1] >> 4) & 0x0f0f0f0fu, 0x64086408u, s0, s1);
+                    }
+                }
+            }
+        }
+    }
+
+    // Value `dim` of the output that element i of n-tile n is, for lane % 4 = t.
+    static __device__ __forceinline__ int dim_of(int n, int i, int t)
+    {
+        return BF ? 8 * n + 2 * t + i : 16 * (n >> 1) + 4 * t + 2 * i + (n & 1);
+    }
+    // Value `dim` of token `tok` of the staged strip, in fp32.
+    static __device__ __forceinline__ float value_of(uint32_t st, int tok, int dim)
+    {
+        const uint32_t vst = st + kStrip * G::RB;
+        if constexpr (BF) {
+            const uint32_t w = lds32(vst + chunk_at<G::CPT>(tok, dim / 8) + (dim % 8) / 2 * 4);
+            return (dim & 1) ? bf16_hi(w) : bf16_lo(w);
+        } else {
+            const uint32_t sa = st + 2 * kStrip * G::RB + G::SCALES + (tok * G::NB + (dim / QK & ~1)) * 2;
+            const uint32_t dw = lds32(sa);
+            const float d = half_bits_to_float((dim / QK & 1) ? dw >> 16 : dw & 0xffffu);
+            const int byte = (FMT == BQG_Q8_0) ? dim : dim / QK * 16 + dim % 16;
+            const uint32_t w = lds32(vst + chunk_at<G::CPT>(tok, byte / 16) + (byte % 16) / 4 * 4) >> (8 * (byte % 4));
+            if constexpr (FMT == BQG_Q8_0) return (float)(int8_t)(w & 0xffu) * d;
+            else return (float)((int)((dim % QK < 16 ? w : w >> 4) & 15u) - 8) * d;
+        }
+    }
+    // Some value of the staged strip is an infinity or NaN (the same answer in every lane).
+    static __device__ __forceinline__ bool any_nonfinite(uint32_t st, int lane)
+    {
+        bool bad = false;
+        if constexpr (BF) {
+#pragma unroll 1
+            for (int i = lane; i < kStrip * G::RB / 4; i += 32) {
+                const uint32_t w = lds32(st + kStrip * G::RB + 4 * i);
+                bad |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+            }
+        } else {
+#pragma unroll 1
+            for (int i = lane; i < G::SCALES / 4; i += 32) {
+                const uint32_t w = lds32(st + 2 * kStrip * G::RB + G::SCALES + 4 * i);
+                bad |= (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+            }
+        }
+        return __any_sync(0xffffffffu, bad);
+    }
+};
+
+// Query fragments in registers, or shared by the CTA's warps in shared memory.
+template <int MT, int KS> struct QRegs {
+    uint32_t f[MT][KS][4];
+    __device__ __forceinline__ void get(int m, int ks, uint32_t (&a)[4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; i++) a[i] = f[m][ks][i];
+    }
+};
+template <int MT, int KS> struct QShared {
+    uint32_t addr;      // this lane's 16 bytes of fragment (0, 0)
+    __device__ __forceinline__ void get(int m, int ks, uint32_t (&a)[4]) const
+    {
+        const uint4 v = lds128(addr + (m * KS + ks) * 512);
+        a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
+    }
+};
+
+template <int FMT, int D, int MT>
+__global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams p, int *error)
+{
+    using G = AttnGeom<FMT, D, MT>;
+    using A = AttnKernel<FMT, D, MT>;
+    constexpr int S = G::S, NT = A::NT;
+    constexpr float NEG = -__builtin_huge_valf();
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    float *const ml = reinterpret_cast<float *>(smem + G::OFF_ML);            // [warp][row][2]
+    float *const row_scale = reinterpret_cast<float *>(smem + G::OFF_RS);
+    float *const merged = reinterpret_cast<float *>(smem);                    // [warp][row][D + PAD]
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // this CTA's range of units
+    int bad = 0;
+    int64_t total = 0;
+    for (int b = lane; b < p.n_seq; b += 32) total += A::units(p, A::load_seq(p, b, bad));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (bad && blockIdx.x == 0 && warp == 0) atomicOr(error, bad);
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    int64_t u = per * blockIdx.x;
+    const int64_t u_end = min(u + per, total);
+    if (u >= u_end) return;
+    // the sequence that holds unit u, and its first unit
+    int b = 0;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+        const int64_t mine = b0 + lane < p.n_seq ? A::units(p, A::load_seq(p, b0 + lane, bad)) : 0;
+        int64_t sum = mine;                                                   // inclusive over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + sum > u);
+        if (past) {
+            const int first = __ffs(past) - 1;
+            b = b0 + first;
+            base += __shfl_sync(0xffffffffu, sum - mine, first);
+            break;
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    AttnSeq s = A::load_seq(p, b, bad);
+    int pages_bad = 0;
+
+    while (u < u_end) {
+        while (u - base >= A::units(p, s)) {                                  // next sequence with work
+            base += A::units(p, s);
+            s = A::load_seq(p, ++b, bad);
+        }
+        const int64_t off = u - base;
+        const int pair = (int)(off / s.tiles), tile0 = (int)(off - (int64_t)pair * s.tiles);
+        const int h = pair / s.row_tiles, row0 = (pair - h * s.row_tiles) * G::ROWS;
+        const int n = (int)min((int64_t)(s.tiles - tile0), u_end - u);        // units of this piece
+        const int64_t seg0 = u - tile0;                                       // first unit of the whole (sequence, head, row tile)
+        const int rows = min(G::ROWS, s.T * p.group - row0);
+
+        // queries
+        float rs[MT][2];
+        unsigned long long vis[MT][2];                                        // new tokens that each row sees
+        std::conditional_t<G::QREG, QRegs<MT, G::KS>, QShared<MT, G::KS>> qf;
+        if constexpr (G::QREG) {
+#pragma unroll
+            for (int m = 0; m < MT; m++) A::load_q(p, s, h, row0 + 16 * m, lane, qf.f[m], rs[m]);
+        } else {
+            qf.addr = sb + G::OFF_Q + lane * 16;
+            for (int m = warp; m < MT; m += kAttnWarps) {
+                uint32_t f[G::KS][4];
+                float r2[2];
+                A::load_q(p, s, h, row0 + 16 * m, lane, f, r2);
+#pragma unroll
+                for (int ks = 0; ks < G::KS; ks++)
+                    *reinterpret_cast<uint4 *>(smem + G::OFF_Q + (m * G::KS + ks) * 512 + lane * 16) =
+                        make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
+                if (t == 0) { row_scale[16 * m + g] = r2[0]; row_scale[16 * m + g + 8] = r2[1]; }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int m = 0; m < MT; m++) { rs[m][0] = row_scale[16 * m + g]; rs[m][1] = row_scale[16 * m + g + 8]; }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const int i = (row0 + 16 * m + g + 8 * r) / p.group;
+                vis[m][r] = 0;
+                if (i < s.T) vis[m][r] = p.mask ? p.mask[s.q0 + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
+            }
+
+        float o[MT][NT][4], top[MT][2], sum[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+            top[m][0] = top[m][1] = NEG;
+            sum[m][0] = sum[m][1] = 0.f;
+#pragma unroll
+            for (int x = 0; x < NT; x++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) o[m][x][i] = 0.f;
+        }
+
+        // strips of this warp: tokens 64 (tile0 + j) + 16 warp ..
+        const uint32_t ring = sb + warp * S * G::STAGE;
+        const int32_t *table = p.table + (int64_t)s.b * p.max_pages;
+        auto page_of = [&](int j) {
+            const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
+            return (j < n && tok0 < s.len) ? table[tok0 >> p.cache.lp] : -1;
+        };
+        unsigned valid = 0;                                                   // stages whose page is in the cache
+        int page = page_of(0);
+        auto issue = [&](int j) {
+            const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
+            const int st = j % S;
+            valid &= ~(1u << st);
+            if (j < n && tok0 < s.len) {
+                const bool ok = page >= 0 && page < p.cache.n_pages;
+                if (!ok) pages_bad = BQG_DEVERR_PAGE;
+                valid |= (unsigned)ok << st;
+                A::issue(p, s, h, tok0, page, ok, ring + st * G::STAGE, lane);
+            }
+            cp_async_commit();
+            page = page_of(j + 1);
+        };
+#pragma unroll 1
+        for (int j = 0; j < S - 1; j++) issue(j);
+#pragma unroll 1
+        for (int j = 0; j < n; j++) {
+            cp_async_wait<S - 2>();
+            __syncwarp();
+            issue(j + S - 1);
+            const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
+            if (tok0 >= s.len) break;
+            const uint32_t st = ring + (j % S) * G::STAGE;
+            const bool ok = (valid >> (j % S)) & 1;
+
+            float sc[MT][2][4];
+            A::scores(st, lane, qf, sc);
+            const bool edge = tok0 + kStrip > s.ctx || !ok;                   // new tokens, the end, or no page
+            if (edge) {
+#pragma unroll
+                for (int m = 0; m < MT; m++)
+#pragma unroll
+                    for (int x = 0; x < 2; x++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int tok = tok0 + 8 * x + 2 * t + (i & 1);
+                            const bool see = ok && (tok < s.ctx || (tok < s.len && ((vis[m][i >> 1] >> (tok - s.ctx)) & 1)));
+                            if (!see) sc[m][x][i] = NEG;
+                        }
+            }
+            // raise the running maximum where a score is well above it
+            bool raise = false;
+            float lm[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    lm[m][r] = fmaxf(fmaxf(sc[m][0][2 * r], sc[m][0][2 * r + 1]), fmaxf(sc[m][1][2 * r], sc[m][1][2 * r + 1])) * rs[m][r];
+                    raise |= lm[m][r] > top[m][r] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int m = 0; m < MT; m++)
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        float v = fmaxf(lm[m][r], __shfl_xor_sync(0xffffffffu, lm[m][r], 1));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                        v = fmaxf(v, top[m][r]);
+                        const float c = (v == top[m][r]) ? 1.f : ex2(top[m][r] - v);
+                        top[m][r] = v;
+                        sum[m][r] *= c;
+#pragma unroll
+                        for (int x = 0; x < NT; x++) { o[m][x][2 * r] *= c; o[m][x][2 * r + 1] *= c; }
+                    }
+            }
+            uint32_t pa[MT][4];
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    const float off = A::kShift - (top[m][r] == NEG ? 0.f : top[m][r]);
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const float e0 = ex2(fmaf(sc[m][x][2 * r], rs[m][r], off)), e1 = ex2(fmaf(sc[m][x][2 * r + 1], rs[m][r], off));
+                        sum[m][r] += e0 + e1;
+                        pa[m][2 * x + r] = pack2<A::BF>(e0, e1);
+                        sc[m][x][2 * r] = sc[m][x][2 * r] == NEG ? -1.f : e0;        // for the exact path
+                        sc[m][x][2 * r + 1] = sc[m][x][2 * r + 1] == NEG ? -1.f : e1;
+                    }
+                }
+            if (edge && A::any_nonfinite(st, lane)) {
+                // an infinity or NaN among tokens that some rows do not see: 0 x inf must
+                // not reach them, so this strip's products are taken one by one in fp32
+                float *const pw = reinterpret_cast<float *>(smem + G::OFF_P) + warp * 16 * kStrip;
+#pragma unroll
+                for (int m = 0; m < MT; m++) {
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 2; x++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) pw[(g + 8 * (i >> 1)) * kStrip + 8 * x + 2 * t + (i & 1)] = sc[m][x][i];
+                    __syncwarp();
+#pragma unroll 1
+                    for (int k = 0; k < kStrip; k++) {
+                        const float p0 = pw[g * kStrip + k], p1 = pw[(g + 8) * kStrip + k];
+#pragma unroll
+                        for (int x = 0; x < NT; x++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++) {
+                                const float v = A::value_of(st, k, A::dim_of(x, i, t));
+                                if (!(p0 < 0.f)) o[m][x][i] = fmaf(p0, v, o[m][x][i]);
+                                if (!(p1 < 0.f)) o[m][x][2 + i] = fmaf(p1, v, o[m][x][2 + i]);
+                            }
+                    }
+                }
+            } else {
+                A::add_values(st, lane, pa, o);
+            }
+        }
+        cp_async_wait<0>();
+        __syncthreads();                                                      // the ring's memory is free
+
+        // the four warps' results of this piece, joined
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 1);
+                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 2);
+                const int row = 16 * m + g + 8 * r;
+                if (t == 0) {
+                    ml[(warp * G::ROWS + row) * 2] = top[m][r];
+                    ml[(warp * G::ROWS + row) * 2 + 1] = sum[m][r];
+                }
+                float *dst = merged + (warp * G::ROWS + row) * (D + G::PAD);
+                if constexpr (A::BF) {
+#pragma unroll
+                    for (int x = 0; x < NT; x++) *reinterpret_cast<float2 *>(dst + 8 * x + 2 * t) = make_float2(o[m][x][2 * r], o[m][x][2 * r + 1]);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < NT; x += 2)
+                        *reinterpret_cast<float4 *>(dst + 8 * x + 4 * t) =
+                            make_float4(o[m][x][2 * r], o[m][x + 1][2 * r], o[m][x][2 * r + 1], o[m][x + 1][2 * r + 1]);
+                }
+            }
+        __syncthreads();
+        const int c0 = (int)(seg0 / per), c1 = (int)((seg0 + s.tiles - 1) / per);  // CTAs that share the segment
+        const int cta = (int)blockIdx.x;
+        constexpr int E = D / 32;                                             // values per lane of a row
+        float *const part_ml = p.part + (int64_t)2 * gridDim.x * G::ROWS * D;
+        auto store_row = [&](int row, const float (&v)[E], float total_sum) { // a finished row
+            const int i = (row0 + row) / p.group, hh = row0 + row - i * p.group;
+            uint16_t *dst = p.out + ((int64_t)(s.q0 + i) * p.n_q + h * p.group + hh) * D + lane * E;
+            const float inv = total_sum == 0.f ? 0.f : 1.0f / total_sum;
+            uint32_t w[E / 2];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) w[e / 2] = pack2<true>(v[e] * inv, v[e + 1] * inv);
+            if constexpr (E == 2) *reinterpret_cast<uint32_t *>(dst) = w[0];
+            else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        for (int row = warp; row < rows; row += kAttnWarps) {
+            float mt = NEG;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; w++) mt = fmaxf(mt, ml[(w * G::ROWS + row) * 2]);
+            float v[E], l = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; e++) v[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; w++) {
+                const float mw = ml[(w * G::ROWS + row) * 2];
+                const float c = (mw == mt) ? 1.f : ex2(mw - mt);
+                l += c * ml[(w * G::ROWS + row) * 2 + 1];
+                const float *src = merged + (w * G::ROWS + row) * (D + G::PAD) + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; e++) v[e] += c * src[e];
+            }
+            if (c0 == c1) {
+                store_row(row, v, l);
+            } else {
+                const int64_t slot = 2 * cta + (cta == c0);
+                float *dst = p.part + (slot * G::ROWS + row) * D + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; e++) dst[e] = v[e];
+                if (lane == 0) *reinterpret_cast<float2 *>(part_ml + (slot * G::ROWS + row) * 2) = make_float2(mt, l);
+            }
+        }
+        if (c0 != c1) {
+            int *flag = reinterpret_cast<int *>(smem + G::OFF_FLAG);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) *flag = atomicAdd(p.counters + c0, 1) == c1 - c0;
+            __syncthreads();
+            if (*flag) {                                                      // every piece is in the workspace
+                __threadfence();
+                if (tid == 0) p.counters[c0] = 0;
+                for (int row = warp; row < rows; row += kAttnWarps) {
+                    auto ml_of = [&](int c) {
+                        return __ldcg(reinterpret_cast<const float2 *>(part_ml + ((2 * c + (c == c0)) * (int64_t)G::ROWS + row) * 2));
+                    };
+                    float mt = NEG;
+                    for (int c = c0 + lane; c <= c1; c += 32) mt = fmaxf(mt, ml_of(c).x);
+                    mt = warp_max(mt);
+                    float l = 0.f, v[E];
+#pragma unroll
+                    for (int e = 0; e < E; e++) v[e] = 0.f;
+#pragma unroll 4
+                    for (int c = c0; c <= c1; c++) {
+                        const float2 q = ml_of(c);
+                        const float w = (q.x == mt) ? 1.f : ex2(q.x - mt);
+                        const float *src = p.part + ((2 * c + (c == c0)) * (int64_t)G::ROWS + row) * D + lane * E;
+                        l += w * q.y;
+                        if constexpr (E == 2) {
+                            const float2 a = __ldcg(reinterpret_cast<const float2 *>(src));
+                            v[0] += w * a.x; v[1] += w * a.y;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < E; e += 4) {
+                                const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + e));
+                                v[e] += w * a.x; v[e + 1] += w * a.y; v[e + 2] += w * a.z; v[e + 3] += w * a.w;
+                            }
+                        }
+                    }
+                    store_row(row, v, l);
+                }
+            }
+        }
+        __syncthreads();                                                      // before the ring is filled again
+        u += n;
+    }
+    if (pages_bad) atomicOr(error, pages_bad);
+}
+
+// What a launch needs of one instantiation.
+struct AttnFn {
+    void (*kern)(const AttnParams, int *);
+    int rows, smem;
+};
+template <int FMT, int D, int MT> AttnFn attn_fn() { return {attn_kernel<FMT, D, MT>, AttnGeom<FMT, D, MT>::ROWS, AttnGeom<FMT, D, MT>::SMEM}; }
+
+}  // namespace bqg

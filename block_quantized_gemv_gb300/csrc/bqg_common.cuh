@@ -179,6 +179,69 @@ __device__ __forceinline__ void q8_1_encode_warp(float v, int lane, uint8_t *out
     }
 }
 
+// ---------------------------------------------------------------------------
+// sums of squares and 1 / sqrt(mean + eps) beyond fp32, without fp64
+// ---------------------------------------------------------------------------
+// Knuth's TwoSum: s + e == a + b exactly (round-to-nearest, no contraction).
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e)
+{
+    s = __fadd_rn(a, b);
+    const float bb = __fsub_rn(s, a);
+    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+}
+
+// Sum of squares as an unevaluated pair hi + lo of fp32 values, plus an fp64
+// part for magnitudes whose square or its rounding error would leave the
+// normal fp32 range.  Each square is exact as p + e (e = fma(v, v, -p); zero
+// for bf16 inputs), hi takes the exact TwoSum of p, lo the rest.
+struct SumSq {
+    float hi = 0.f, lo = 0.f;
+    double wide = 0.0;
+    __device__ __forceinline__ void add(float v)
+    {
+        const uint32_t ex = (__float_as_uint(v) >> 23) & 0xFFu;
+        if (ex - 77u <= 176u - 77u) {                 // 2^-50 <= |v| < 2^50
+            const float p = __fmul_rn(v, v);
+            const float ep = fmaf(v, v, -p);
+            float t;
+            two_sum(hi, p, hi, t);
+            lo = __fadd_rn(lo, __fadd_rn(t, ep));
+        } else if (v != 0.f) {
+            wide = fma((double)v, (double)v, wide);   // exact square in fp64
+        }
+    }
+    __device__ __forceinline__ void merge(float ohi, float olo)
+    {
+        float t;
+        two_sum(hi, ohi, hi, t);
+        lo = __fadd_rn(lo, __fadd_rn(olo, t));
+    }
+};
+
+// r = 1 / sqrt(s / K + eps) rounded once to fp32, from s = sh + sl, without
+// fp64: u = s / K + eps is formed as an fp32 pair (q1 = RN(sh / K), whose
+// remainder sh - q1 K an fma gives exactly), then y = rsqrtf(u) is refined by
+// one Newton step for u^-1/2 with its second-order term,
+// y (1 + d/2 + 3 d^2 / 8), d = 1 - u y^2, the products split exactly by fma.
+// Before the last rounding the value is within about 2^-44 of the exact one.
+__device__ __forceinline__ float rms_recip_pair(float sh, float sl, float Kf, float eps)
+{
+    const float q1 = __fdiv_rn(sh, Kf);
+    const float rem = fmaf(-q1, Kf, sh);
+    const float q2 = __fdiv_rn(__fadd_rn(rem, sl), Kf);
+    float uh, ul;
+    two_sum(q1, eps, uh, ul);
+    ul = __fadd_rn(ul, q2);
+    const float t = __fadd_rn(uh, ul);                 // renormalise (|uh| >= |ul|)
+    ul = __fsub_rn(ul, __fsub_rn(t, uh));
+    uh = t;
+    const float y = rsqrtf(uh);
+    const float p = __fmul_rn(y, y), pe = fmaf(y, y, -p);
+    const float wh = __fmul_rn(uh, p), we = fmaf(uh, p, -wh);
+    const float d = __fsub_rn(__fsub_rn(__fsub_rn(1.0f, wh), we), fmaf(uh, pe, __fmul_rn(ul, p)));
+    return __fadd_rn(y, __fmul_rn(y, __fmul_rn(d, fmaf(0.375f, d, 0.5f))));
+}
+
 // Bulk copy global -> this CTA's shared memory, completing `bytes` on `bar`.
 // dst, src 16-byte aligned; bytes a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)

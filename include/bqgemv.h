@@ -264,6 +264,129 @@ int bqg_decode_layer_q4_0_q8_1(const void *xa, const void *xb, int x_dtype, cons
                                float *Yv, float *Y, int M, int64_t Nq, int64_t Nkv, int64_t Nff, int64_t K, void *ws,
                                size_t ws_bytes, cudaStream_t stream);
 
+/* ---- attention over a paged cache ------------------------------------- */
+
+/* The part of a decode layer between its QKV projections and its output
+ * projection: per-head norm and rotation of queries and keys, a paged cache
+ * of keys and values (bf16 or block-quantized), and attention of the newest
+ * tokens over it.  The pages have no counterpart of these entries beyond
+ * naming the steps ("MI50 megakernel", hypothesis ledger: position rotation
+ * and cache write folded into one dispatch).
+ *
+ * A cache is n_pages pages of page_size tokens for each of n_kv heads, keys
+ * and values alike, in plain row-major arrays (fmt BQG_BF16, BQG_Q8_0 or
+ * BQG_Q4_0):
+ *   k, v             [n_pages][n_kv][page_size][row], row = head_dim bf16
+ *                    values, head_dim int8 codes (q8_0), or head_dim / 2
+ *                    bytes (q4_0: per block of 32 values 16 bytes, byte j
+ *                    holding value j in its low nibble, j + 16 in its high)
+ *   k_scale, v_scale [n_pages][n_kv][page_size][head_dim / 32] fp16 block
+ *                    scales; ignored for BQG_BF16
+ * with the value formulas and rounding rules of the block formats above.
+ * head_dim 64, 128 or 256; page_size a power of two from 16 to 4096;
+ * n_pages * page_size at most 2^40.  The struct is read on the host during the call; the arrays are
+ * device memory, 16-byte aligned.  A token's place ("slot") is
+ * page * page_size + place within the page. */
+typedef struct bqg_kv_cache {
+    int fmt;
+    int page_size;
+    int n_kv;
+    int head_dim;
+    int64_t n_pages;
+    void *k, *v;
+    void *k_scale, *v_scale;
+} bqg_kv_cache;
+
+/* Bits of the device error word (bqg_last_device_error) that these entries
+ * set when an index in device memory is out of range.  The access is skipped. */
+enum {
+    BQG_DEVERR_SLOT = 16,       /* a slot beyond the cache: not stored, read as zeros          */
+    BQG_DEVERR_POSITION = 32,   /* a position outside the table: zeros out, not stored         */
+    BQG_DEVERR_PAGE = 64,       /* a page index outside the cache: its tokens are not seen     */
+    BQG_DEVERR_LENGTH = 128     /* lengths or query offsets that do not fit: clamped to fit    */
+};
+
+/* Per-head RMSNorm and rotation of queries and keys.  q: T tokens of n_q
+ * heads, k: T tokens of n_kv heads, each head's D = head_dim values
+ * together, consecutive tokens q_stride and k_stride values apart (so q and
+ * k may be parts of one fused projection's rows); x_dtype BQG_BF16 or
+ * BQG_F32.  For each head:
+ *   norm = 1:  r = fp32(1 / sqrt(sum x^2 / D + eps))    (as bqg_rmsnorm_quantize_q8_1)
+ *              y = fp32(fp32(x r) gamma)                (gamma NULL: no gain)
+ *   norm = 0:  y = x                                    (gammas and eps unused)
+ *   for pair i < R / 2 of the first R = rot_dim values, (a, b) = (y[i], y[i + R/2]),
+ *   or (y[2i], y[2i + 1]) when interleaved, c = table[pos][i], s = table[pos][R/2 + i]:
+ *              a' = fp32(fp32(a c) - fp32(b s)),  b' = fp32(fp32(a s) + fp32(b c))
+ * and values from R on stay y.  pos: T int32 positions; table: n_pos rows of
+ * R fp32, cos of the R/2 pair angles and then their sines, made once by the
+ * caller.  R = 0 rotates nothing (pos and table unused).  Outputs bf16,
+ * contiguous: q_out T x n_q x D, k_out T x n_kv x D (not overlapping inputs).
+ * Pointers and token strides 16-byte aligned (pos 4); head_dim 64, 128 or
+ * 256; R a multiple of 16 up to head_dim; n_q, n_kv >= 0, T >= 0; n_q and
+ * n_kv at most 1024. */
+int bqg_qk_norm_rope(const void *q, const void *k, int x_dtype, int64_t q_stride, int64_t k_stride, int64_t T, int n_q,
+                     int n_kv, int head_dim, int norm, const float *gamma_q, const float *gamma_k, float eps,
+                     const int32_t *pos, const float *table, int64_t n_pos, int rot_dim, int interleaved, void *q_out,
+                     void *k_out, cudaStream_t stream);
+
+/* The same with the keys, and the values v, going into the cache in the same
+ * launch: key and value rows are encoded from the fp32 results with the
+ * cache format's rules (bf16: rounded to nearest even).  slots: T int64
+ * slots; a negative one stores nothing (padding).  Two tokens of a call must
+ * not name the same slot.  n_kv and head_dim are the cache's. */
+int bqg_qk_norm_rope_kv_write(const void *q, const void *k, const void *v, int x_dtype, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int64_t T, int n_q, int norm, const float *gamma_q,
+                              const float *gamma_k, float eps, const int32_t *pos, const float *table, int64_t n_pos,
+                              int rot_dim, int interleaved, void *q_out, const int64_t *slots,
+                              const bqg_kv_cache *cache, cudaStream_t stream);
+
+/* Keys and values of T tokens into the cache as they are (k, v as above). */
+int bqg_kv_write(const void *k, const void *v, int x_dtype, int64_t k_stride, int64_t v_stride, int64_t T,
+                 const int64_t *slots, const bqg_kv_cache *cache, cudaStream_t stream);
+
+/* The cache's values at T slots, as k_out and v_out, T x n_kv x head_dim,
+ * out_dtype BQG_BF16 (each value rounded once, to nearest even) or BQG_F32
+ * (exact).  A negative slot reads as zeros. */
+int bqg_kv_read(const bqg_kv_cache *cache, const int64_t *slots, int64_t T, int out_dtype, void *k_out, void *v_out,
+                cudaStream_t stream);
+
+/* Attention of each sequence's newest tokens over its cached tokens:
+ *   out[i, h] = sum_j p_j v_j,  p = softmax over the visible j of scale * q[i, h] . k_j
+ * Sequence b has context tokens 0 .. ctx_len[b] - 1 and T_b new ones behind
+ * them, query tokens q_start[b] .. q_start[b + 1] - 1 (T_b = their count, at
+ * most max_q), all of them already in the cache: token j is at place
+ * j % page_size of page block_table[b][j / page_size].  Every query sees the
+ * whole context.  Among the new tokens, query i of its sequence (i from 0)
+ * sees new token j when bit j of its word in `mask` (one uint64 per query
+ * token: a tree of drafted tokens gives each its ancestors and itself), or,
+ * mask NULL, when j <= i (causal).  A query that sees nothing gives zeros;
+ * a key or value that it does not see does not reach it, not even an infinity or NaN.
+ * Query heads h of n_q share KV head h / (n_q / n_kv); n_q a multiple of n_kv, at most 64 times it.
+ * q: bf16, n_tokens x n_q x head_dim, tokens q_stride values apart; out:
+ * bf16, contiguous.  q_start: n_seq + 1 int32, ascending from 0, the last
+ * one n_tokens.  ctx_len: n_seq int32.  block_table: n_seq rows of max_pages int32.
+ * 1 <= max_q <= 64.  scale > 0 and finite.
+ * Keys enter the products exactly (bf16, or integer codes whose block sums
+ * are scaled in fp32).  Values enter as they are (bf16) or as q d rounded
+ * once to fp16 (quantized), so quantized values beyond fp16's range (65504)
+ * are out of range here.
+ * Scores, softmax sums and outputs accumulate in fp32; the probabilities are
+ * rounded to the values' type (bf16 or fp16) for the second product; in fp16
+ * (quantized) one below 2^-22 of its row's largest loses bits, and below 2^-33
+ * it counts as zero.
+ * ws: bqg_tree_attention_workspace_size(...) bytes, 16-byte aligned, ZERO
+ * before the first call on it (every call leaves its counters zero).  Calls
+ * that share a workspace must not overlap.  Results do not depend on timing:
+ * two calls on the same data give the same bits. */
+int bqg_tree_attention(const void *q, int64_t q_stride, const bqg_kv_cache *cache, const int32_t *block_table,
+                       int64_t max_pages, const int32_t *ctx_len, const int32_t *q_start, int n_seq, int64_t n_tokens,
+                       int max_q, int n_q, const uint64_t *mask, float scale, void *out, void *ws, size_t ws_bytes,
+                       cudaStream_t stream);
+
+/* Workspace bytes of bqg_tree_attention for these arguments on the current
+ * device; 0 when they are not valid. */
+size_t bqg_tree_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int n_seq, int max_q);
+
 /* Prefill GEMM ("llama-3x-prompt-speed", "the tile"): each weight tile is
  * dequantized once to bf16 into the tensor memory the MMA reads and fed to
  * the tensor cores with fp32 accumulation.  For K >= 1024 each weight
