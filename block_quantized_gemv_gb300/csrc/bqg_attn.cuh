@@ -129,7 +129,8 @@ template <bool BF> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 }
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) { uint32_t r; asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b)); return r; }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { uint32_t r; asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b)); return r; }
-__device__ __forceinline__ float ex2(float x) { float r; asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x)); return r; }
+// 2^x; results below 2^-126 are zero (a probability that far below its row's largest counts as none)
+__device__ __forceinline__ float ex2(float x) { float r; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x)); return r; }
 
 // Chunk c of token `tok` in a staged strip: the position of its 16 bytes.
 // Eight consecutive tokens' chunk c, and the chunk pairs (2i, 2i + 1) of
@@ -143,11 +144,122 @@ template <int CPT> __device__ __forceinline__ uint32_t chunk_at(int tok, int c)
     return (uint32_t)(tok * CPT + (c ^ f)) * 16;
 }
 
-// One sequence as the kernel works on it.
+// One sequence as the kernels work on it.
 struct AttnSeq {
     int b, q0, T, ctx, len;      // first query token, new tokens, context and all cached tokens
-    int tiles, row_tiles;
 };
+
+// Sequence b with its lengths made to fit; `bad` collects BQG_DEVERR_LENGTH.
+__device__ __forceinline__ AttnSeq attn_seq(const AttnParams &p, int b, int &bad)
+{
+    AttnSeq s;
+    s.b = b;
+    const int64_t cap = min((int64_t)0x7fff0000, p.max_pages << p.cache.lp);
+    const int64_t a = p.q_start[b], e = p.q_start[b + 1], c = p.ctx_len[b];
+    const int64_t q0 = min(max(a, (int64_t)0), p.n_tokens), q1 = min(max(e, q0), p.n_tokens);
+    const int64_t T = min(q1 - q0, (int64_t)p.max_q);
+    const int64_t ctx = min(max(c, (int64_t)0), max(cap - T, (int64_t)0));
+    if (q0 != a || q1 != e || T != q1 - q0 || ctx != c || T > cap) bad |= BQG_DEVERR_LENGTH;
+    s.q0 = (int)q0; s.T = (int)T; s.ctx = (int)ctx;
+    s.len = (int)min(ctx + T, cap);
+    return s;
+}
+
+// Row `row` (new token row / group, head row % group) of (sequence, KV head): its query, or null past the last.
+__device__ __forceinline__ const uint16_t *attn_q_row(const AttnParams &p, const AttnSeq &s, int h, int row, int D)
+{
+    const int i = row / p.group, hh = row - i * p.group;
+    return (i < s.T) ? p.q + (s.q0 + i) * p.q_stride + (int64_t)(h * p.group + hh) * D : nullptr;
+}
+// The new tokens that a row sees.
+__device__ __forceinline__ unsigned long long attn_sees(const AttnParams &p, const AttnSeq &s, int row)
+{
+    const int i = row / p.group;
+    if (i >= s.T) return 0;
+    return p.mask ? p.mask[s.q0 + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
+}
+// The sequence whose units (weight(sequence) of them) hold number u of the line of all sequences' units;
+// `base`: the number of its first.  Called by whole warps.
+template <typename W> __device__ __forceinline__ int attn_find(const AttnParams &p, int64_t u, int lane, W weight, int64_t &base)
+{
+    base = 0;
+    for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
+        int bad = 0;
+        const int64_t mine = b0 + lane < p.n_seq ? weight(attn_seq(p, b0 + lane, bad)) : 0;
+        int64_t sum = mine;                                                   // inclusive over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, base + sum > u);
+        if (past) {
+            const int first = __ffs(past) - 1;
+            base += __shfl_sync(0xffffffffu, sum - mine, first);
+            return b0 + first;
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return p.n_seq;      // not reached for u below the total
+}
+// The units of all sequences, and BQG_DEVERR_LENGTH in `bad` of some lanes.
+template <typename W> __device__ __forceinline__ int64_t attn_total(const AttnParams &p, int lane, W weight, int &bad)
+{
+    int64_t total = 0;
+    for (int b = lane; b < p.n_seq; b += 32) total += weight(attn_seq(p, b, bad));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    return total;
+}
+
+// A finished row: E = D / 32 values per lane, divided by their sum of weights, in bf16.
+template <int E> __device__ __forceinline__ void attn_store_row(uint16_t *dst, const float (&v)[E], float sum)
+{
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) w[e / 2] = pack2<true>(v[e] * inv, v[e + 1] * inv);
+    if constexpr (E == 2) *reinterpret_cast<uint32_t *>(dst) = w[0];
+    else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Where row `row` of CTA c's piece of a set that begins in CTA c0 lies (rows of ROWS): a CTA has at most one
+// piece that a former CTA began and one that it begins and does not end.
+template <int ROWS> __device__ __forceinline__ int64_t attn_slot_row(int c, int c0, int row)
+{
+    return (int64_t)(2 * c + (c == c0)) * ROWS + row;
+}
+// Row `row` of the pieces of CTAs c0 .. c1, joined in their order by one warp: E values per lane and the sum.
+template <int E, int ROWS>
+__device__ __forceinline__ void attn_join_row(const float *part, const float *part_ml, int c0, int c1, int row, int lane,
+                                              float (&v)[E], float &l)
+{
+    constexpr int D = 32 * E;
+    auto ml_of = [&](int c) { return __ldcg(reinterpret_cast<const float2 *>(part_ml + attn_slot_row<ROWS>(c, c0, row) * 2)); };
+    float mt = -__builtin_huge_valf();
+    for (int c = c0 + lane; c <= c1; c += 32) mt = fmaxf(mt, ml_of(c).x);
+    mt = warp_max(mt);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; e++) v[e] = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; c++) {
+        const float2 q = ml_of(c);
+        const float w = (q.x == mt) ? 1.f : ex2(q.x - mt);
+        const float *src = part + attn_slot_row<ROWS>(c, c0, row) * D + lane * E;
+        l += w * q.y;
+        if constexpr (E == 2) {
+            const float2 a = __ldcg(reinterpret_cast<const float2 *>(src));
+            v[0] += w * a.x; v[1] += w * a.y;
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + e));
+                v[e] += w * a.x; v[e + 1] += w * a.y; v[e + 2] += w * a.z; v[e + 3] += w * a.w;
+            }
+        }
+    }
+}
 
 template <int FMT, int D, int MT> struct AttnKernel {
     using G = AttnGeom<FMT, D, MT>;
@@ -155,33 +267,15 @@ template <int FMT, int D, int MT> struct AttnKernel {
     static constexpr float kShift = BF ? 0.0f : 8.0f;
     static constexpr int NT = D / 8;                          // n-tiles of the output
 
-    // Sequence b with its lengths made to fit; `bad` collects BQG_DEVERR_LENGTH.
-    static __device__ __forceinline__ AttnSeq load_seq(const AttnParams &p, int b, int &bad)
+    // 64-token tiles and row tiles of a sequence, and its units.
+    static __device__ __forceinline__ int tiles_of(const AttnSeq &s) { return (s.len + kUnit - 1) / kUnit; }
+    static __device__ __forceinline__ int row_tiles_of(const AttnParams &p, const AttnSeq &s)
     {
-        AttnSeq s;
-        s.b = b;
-        const int64_t cap = min((int64_t)0x7fff0000, p.max_pages << p.cache.lp);
-        const int64_t a = p.q_start[b], e = p.q_start[b + 1], c = p.ctx_len[b];
-        const int64_t q0 = min(max(a, (int64_t)0), p.n_tokens), q1 = min(max(e, q0), p.n_tokens);
-        const int64_t T = min(q1 - q0, (int64_t)p.max_q);
-        const int64_t ctx = min(max(c, (int64_t)0), max(cap - T, (int64_t)0));
-        if (q0 != a || q1 != e || T != q1 - q0 || ctx != c || T > cap) bad |= BQG_DEVERR_LENGTH;
-        s.q0 = (int)q0; s.T = (int)T; s.ctx = (int)ctx;
-        s.len = (int)min(ctx + T, cap);
-        s.tiles = T > 0 ? (s.len + kUnit - 1) / kUnit : 0;
-        s.row_tiles = ((int)T * p.group + G::ROWS - 1) / G::ROWS;
-        return s;
+        return (s.T * p.group + G::ROWS - 1) / G::ROWS;
     }
     static __device__ __forceinline__ int64_t units(const AttnParams &p, const AttnSeq &s)
     {
-        return (int64_t)p.cache.n_kv * s.row_tiles * s.tiles;
-    }
-
-    // One query value pair of row (token, head) in fp32.
-    static __device__ __forceinline__ const uint16_t *q_row(const AttnParams &p, const AttnSeq &s, int h, int row)
-    {
-        const int i = row / p.group, hh = row - i * p.group;
-        return (i < s.T) ? p.q + (s.q0 + i) * p.q_stride + (int64_t)(h * p.group + hh) * D : nullptr;
+        return (int64_t)p.cache.n_kv * row_tiles_of(p, s) * tiles_of(s);
     }
 
     // The query fragments of row tile rows row0 .. row0 + 15 (KS steps x 4
@@ -192,7 +286,7 @@ template <int FMT, int D, int MT> struct AttnKernel {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int r = 0; r < 2; r++) {
-            const uint16_t *src = q_row(p, s, h, row0 + g + 8 * r);
+            const uint16_t *src = attn_q_row(p, s, h, row0 + g + 8 * r, D);
             rs[r] = p.scale_log2;
             if constexpr (BF) {
 #pragma unroll
@@ -487,47 +581,28 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
 
     // this CTA's range of units
     int bad = 0;
-    int64_t total = 0;
-    for (int b = lane; b < p.n_seq; b += 32) total += A::units(p, A::load_seq(p, b, bad));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    auto weight = [&](const AttnSeq &q) { return A::units(p, q); };
+    const int64_t total = attn_total(p, lane, weight, bad);
     if (bad && blockIdx.x == 0 && warp == 0) atomicOr(error, bad);
     const int64_t per = (total + gridDim.x - 1) / gridDim.x;
     int64_t u = per * blockIdx.x;
     const int64_t u_end = min(u + per, total);
     if (u >= u_end) return;
-    // the sequence that holds unit u, and its first unit
-    int b = 0;
-    int64_t base = 0;
-    for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
-        const int64_t mine = b0 + lane < p.n_seq ? A::units(p, A::load_seq(p, b0 + lane, bad)) : 0;
-        int64_t sum = mine;                                                   // inclusive over the lanes
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, base + sum > u);
-        if (past) {
-            const int first = __ffs(past) - 1;
-            b = b0 + first;
-            base += __shfl_sync(0xffffffffu, sum - mine, first);
-            break;
-        }
-        base += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    AttnSeq s = A::load_seq(p, b, bad);
+    int64_t base;
+    int b = attn_find(p, u, lane, weight, base);
+    AttnSeq s = attn_seq(p, b, bad);
     int pages_bad = 0;
 
     while (u < u_end) {
         while (u - base >= A::units(p, s)) {                                  // next sequence with work
             base += A::units(p, s);
-            s = A::load_seq(p, ++b, bad);
+            s = attn_seq(p, ++b, bad);
         }
         const int64_t off = u - base;
-        const int pair = (int)(off / s.tiles), tile0 = (int)(off - (int64_t)pair * s.tiles);
-        const int h = pair / s.row_tiles, row0 = (pair - h * s.row_tiles) * G::ROWS;
-        const int n = (int)min((int64_t)(s.tiles - tile0), u_end - u);        // units of this piece
+        const int tiles = A::tiles_of(s), row_tiles = A::row_tiles_of(p, s);
+        const int pair = (int)(off / tiles), tile0 = (int)(off - (int64_t)pair * tiles);
+        const int h = pair / row_tiles, row0 = (pair - h * row_tiles) * G::ROWS;
+        const int n = (int)min((int64_t)(tiles - tile0), u_end - u);          // units of this piece
         const int64_t seg0 = u - tile0;                                       // first unit of the whole (sequence, head, row tile)
         const int rows = min(G::ROWS, s.T * p.group - row0);
 
@@ -557,11 +632,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                const int i = (row0 + 16 * m + g + 8 * r) / p.group;
-                vis[m][r] = 0;
-                if (i < s.T) vis[m][r] = p.mask ? p.mask[s.q0 + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
-            }
+            for (int r = 0; r < 2; r++) vis[m][r] = attn_sees(p, s, row0 + 16 * m + g + 8 * r);
 
         float o[MT][NT][4], top[MT][2], sum[MT][2];
 #pragma unroll
@@ -719,20 +790,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                 }
             }
         __syncthreads();
-        const int c0 = (int)(seg0 / per), c1 = (int)((seg0 + s.tiles - 1) / per);  // CTAs that share the segment
+        const int c0 = (int)(seg0 / per), c1 = (int)((seg0 + tiles - 1) / per);    // CTAs that share the segment
         const int cta = (int)blockIdx.x;
         constexpr int E = D / 32;                                             // values per lane of a row
         float *const part_ml = p.part + (int64_t)2 * gridDim.x * G::ROWS * D;
-        auto store_row = [&](int row, const float (&v)[E], float total_sum) { // a finished row
+        auto out_row = [&](int row) {
             const int i = (row0 + row) / p.group, hh = row0 + row - i * p.group;
-            uint16_t *dst = p.out + ((int64_t)(s.q0 + i) * p.n_q + h * p.group + hh) * D + lane * E;
-            const float inv = total_sum == 0.f ? 0.f : 1.0f / total_sum;
-            uint32_t w[E / 2];
-#pragma unroll
-            for (int e = 0; e < E; e += 2) w[e / 2] = pack2<true>(v[e] * inv, v[e + 1] * inv);
-            if constexpr (E == 2) *reinterpret_cast<uint32_t *>(dst) = w[0];
-            else if constexpr (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            return p.out + ((int64_t)(s.q0 + i) * p.n_q + h * p.group + hh) * D + lane * E;
         };
         for (int row = warp; row < rows; row += kAttnWarps) {
             float mt = NEG;
@@ -751,13 +815,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                 for (int e = 0; e < E; e++) v[e] += c * src[e];
             }
             if (c0 == c1) {
-                store_row(row, v, l);
+                attn_store_row<E>(out_row(row), v, l);
             } else {
-                const int64_t slot = 2 * cta + (cta == c0);
-                float *dst = p.part + (slot * G::ROWS + row) * D + lane * E;
+                const int64_t at = attn_slot_row<G::ROWS>(cta, c0, row);
+                float *dst = p.part + at * D + lane * E;
 #pragma unroll
                 for (int e = 0; e < E; e++) dst[e] = v[e];
-                if (lane == 0) *reinterpret_cast<float2 *>(part_ml + (slot * G::ROWS + row) * 2) = make_float2(mt, l);
+                if (lane == 0) *reinterpret_cast<float2 *>(part_ml + at * 2) = make_float2(mt, l);
             }
         }
         if (c0 != c1) {
@@ -770,33 +834,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                 __threadfence();
                 if (tid == 0) p.counters[c0] = 0;
                 for (int row = warp; row < rows; row += kAttnWarps) {
-                    auto ml_of = [&](int c) {
-                        return __ldcg(reinterpret_cast<const float2 *>(part_ml + ((2 * c + (c == c0)) * (int64_t)G::ROWS + row) * 2));
-                    };
-                    float mt = NEG;
-                    for (int c = c0 + lane; c <= c1; c += 32) mt = fmaxf(mt, ml_of(c).x);
-                    mt = warp_max(mt);
-                    float l = 0.f, v[E];
-#pragma unroll
-                    for (int e = 0; e < E; e++) v[e] = 0.f;
-#pragma unroll 4
-                    for (int c = c0; c <= c1; c++) {
-                        const float2 q = ml_of(c);
-                        const float w = (q.x == mt) ? 1.f : ex2(q.x - mt);
-                        const float *src = p.part + ((2 * c + (c == c0)) * (int64_t)G::ROWS + row) * D + lane * E;
-                        l += w * q.y;
-                        if constexpr (E == 2) {
-                            const float2 a = __ldcg(reinterpret_cast<const float2 *>(src));
-                            v[0] += w * a.x; v[1] += w * a.y;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < E; e += 4) {
-                                const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + e));
-                                v[e] += w * a.x; v[e + 1] += w * a.y; v[e + 2] += w * a.z; v[e + 3] += w * a.w;
-                            }
-                        }
-                    }
-                    store_row(row, v, l);
+                    float v[E], l;
+                    attn_join_row<E, G::ROWS>(p.part, part_ml, c0, c1, row, lane, v, l);
+                    attn_store_row<E>(out_row(row), v, l);
                 }
             }
         }
@@ -805,12 +845,5 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
     }
     if (pages_bad) atomicOr(error, pages_bad);
 }
-
-// What a launch needs of one instantiation.
-struct AttnFn {
-    void (*kern)(const AttnParams, int *);
-    int rows, smem;
-};
-template <int FMT, int D, int MT> AttnFn attn_fn() { return {attn_kernel<FMT, D, MT>, AttnGeom<FMT, D, MT>::ROWS, AttnGeom<FMT, D, MT>::SMEM}; }
 
 }  // namespace bqg

@@ -1,19 +1,27 @@
-// bqg_attn_launch.cuh -- host side of the attention kernel, one cache format per translation unit.
+// bqg_attn_launch.cuh -- host side of the attention kernels, one cache format per translation unit.
 #pragma once
 
 #include <algorithm>
+#include <cstdlib>
 #include <mutex>
 
-#include "bqg_attn.cuh"
+#include <cudaTypedefs.h>
+
+#include "bqg_attn_tc.cuh"
 
 namespace bqg {
 
-// Counters at the start of every workspace: the same bytes whatever the
-// call's instantiation, so calls of different shapes can take turns on one.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// A workspace: the same bytes at its start whatever the call's kernel, so
+// that calls of different shapes can take turns on one.  One arrival counter per
+// CTA of the mma.sync kernel (zero between calls), then the sets
+// that CTAs of the tcgen05 kernel share, then partial results.
 constexpr int kAttnMaxCtas = 4096;
 constexpr size_t kAttnCounterBytes = kAttnMaxCtas * sizeof(int);
+constexpr size_t kAttnSetBytes = 1024 * sizeof(TcSet);
+constexpr size_t kAttnHead = kAttnCounterBytes + kAttnSetBytes;
 
-// The workspace of a call: counters, partial rows, their maxima and sums.
 struct AttnPlan {
     size_t ws_bytes;
 };
@@ -28,67 +36,144 @@ inline cudaError_t take_error(int &word, int *out)
     return cudaSuccess;
 }
 
-// rows: the most rows (new tokens x heads of a group) of any sequence.  Up
-// to 16 one row tile, more two per CTA where the accumulators fit in
-// registers (head_dim <= 128), so that a row of the cache is read from L2
-// once for each 32 rows.
-template <int FMT> AttnFn attn_pick(int D, int rows)
+// Rows from which the tcgen05 kernel serves a call (BQG_ATTN_TC_ROWS; read once).
+inline int attn_tc_rows()
 {
-    if (D == 64) return rows <= 16 ? attn_fn<FMT, 64, 1>() : attn_fn<FMT, 64, 2>();
-    if (D == 128) return rows <= 16 ? attn_fn<FMT, 128, 1>() : attn_fn<FMT, 128, 2>();
-    return attn_fn<FMT, 256, 1>();
+    static const int n = [] {
+        const char *v = getenv("BQG_ATTN_TC_ROWS");
+        return (v && *v) ? std::max(1, atoi(v)) : 17;
+    }();
+    return n;
 }
 
-// Plans the call (plan) or, plan null, launches it.
-template <int FMT>
-cudaError_t attn_launch(const AttnParams &params, int D, int rows, int &error_word, AttnPlan *plan, cudaStream_t s, bool pdl)
+inline void attn_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int threads, int smem, cudaStream_t s,
+                        bool pdl)
 {
-    const AttnFn fn = attn_pick<FMT>(D, rows);
-    // occupancy of each instantiation, once per device
-    static std::mutex mu;
-    static int occ[64][6];
-    int dev = 0, sms = 0;
-    if (cudaError_t e = cudaGetDevice(&dev)) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
-    const int which = (D == 64 ? 0 : D == 128 ? 2 : 4) + (fn.rows > 16);
-    int n = 0;
-    {
-        std::lock_guard<std::mutex> lk(mu);
-        if (occ[dev][which] == 0) {
-            if (cudaError_t e = cudaFuncSetAttribute(fn.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fn.smem)) return e;
-            int k = 0;
-            if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, fn.kern, 32 * kAttnWarps, fn.smem)) return e;
-            if (k < 1) return cudaErrorLaunchOutOfResources;
-            occ[dev][which] = k;
-        }
-        n = occ[dev][which];
-    }
-    const int ctas = std::min(sms * n, kAttnMaxCtas);                     // all resident at once
-    if (plan) {
-        plan->ws_bytes = kAttnCounterBytes + (size_t)2 * ctas * fn.rows * (D + 2) * sizeof(float);
-        return cudaSuccess;
-    }
-    void *word = nullptr;
-    if (cudaError_t e = cudaGetSymbolAddress(&word, error_word)) return e;
-    AttnParams p = params;
-    p.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.counters) + kAttnCounterBytes);
-    // never more CTAs than units could exist
-    const int64_t cap = std::min<int64_t>(p.max_pages << p.cache.lp, 0x7fff0000);
-    const int64_t per_row_tile = (cap + kUnit - 1) / kUnit;
-    const int64_t row_tiles = ((int64_t)p.max_q * p.group + fn.rows - 1) / fn.rows;
-    const double most = (double)p.n_seq * p.cache.n_kv * (double)row_tiles * (double)per_row_tile;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::max(1.0, std::min((double)ctas, most)));
-    cfg.blockDim = dim3(32 * kAttnWarps);
-    cfg.dynamicSmemBytes = fn.smem;
+    cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fn.kern, p, (int *)word);
+}
+
+// CTAs of a kernel that are resident together on this device: looked up once.
+template <typename K> cudaError_t attn_ctas(K kern, int threads, int smem, int *ctas)
+{
+    static std::mutex mu;
+    static int known[64];      // per instantiation of this template: see the tag types below
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(mu);
+    if (known[dev] == 0) {
+        int sms = 0, n = 0;
+        if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
+        if (cudaError_t e = cudaFuncSetAttribute(kern.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) return e;
+        if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern.fn, threads, smem)) return e;
+        if (n < 1) return cudaErrorLaunchOutOfResources;
+        known[dev] = std::min(sms * n, kern.most);
+    }
+    *ctas = known[dev];
+    return cudaSuccess;
+}
+
+// Units of `tile` tokens x `rows` rows that the call's arguments allow at most.
+inline double attn_most(const AttnParams &p, int tile, int rows)
+{
+    const int64_t cap = std::min<int64_t>(p.max_pages << p.cache.lp, 0x7fff0000);
+    const int64_t row_tiles = ((int64_t)p.max_q * p.group + rows - 1) / rows;
+    return (double)p.n_seq * p.cache.n_kv * (double)row_tiles * (double)((cap + tile - 1) / tile);
+}
+
+// mma.sync kernel: plans the call (plan) or, plan null, launches it.
+template <int FMT, int D, int MT>
+cudaError_t attn_rows_call(AttnParams p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    using G = AttnGeom<FMT, D, MT>;
+    struct Kern {
+        void (*fn)(const AttnParams, int *) = attn_kernel<FMT, D, MT>;
+        int most = kAttnMaxCtas;
+    } kern;
+    int ctas = 0;
+    if (cudaError_t e = attn_ctas(kern, 32 * kAttnWarps, G::SMEM, &ctas)) return e;
+    if (plan) {
+        plan->ws_bytes = kAttnHead + (size_t)2 * ctas * G::ROWS * (D + 2) * sizeof(float);
+        return cudaSuccess;
+    }
+    p.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.counters) + kAttnHead);
+    const unsigned grid = (unsigned)std::max(1.0, std::min((double)ctas, attn_most(p, kUnit, G::ROWS)));
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    attn_config(cfg, attr, dim3(grid), 32 * kAttnWarps, G::SMEM, s, pdl);
+    return cudaLaunchKernelEx(&cfg, kern.fn, p, error);
+}
+
+// tcgen05 kernel and its join.
+template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    using G = TcGeom<FMT, D>;
+    struct Kern {
+        void (*fn)(const AttnParams, const CUtensorMap, const CUtensorMap, int *) = attn_tc_kernel<FMT, D>;
+        int most = (int)(kAttnSetBytes / sizeof(TcSet));
+    } kern;
+    int ctas = 0;
+    if (cudaError_t e = attn_ctas(kern, G::THREADS, G::SMEM, &ctas)) return e;
+    if (plan) {
+        plan->ws_bytes = kAttnHead + (size_t)2 * ctas * kTcRows * (D + 2) * sizeof(float);
+        return cudaSuccess;
+    }
+    // the cache as rows of D bf16 values: boxes of 64 values x the tokens of a page (at most a tile)
+    CUtensorMap kmap{}, vmap{};
+    if (FMT == BQG_BF16) {
+        auto enc = tensor_map_encoder();
+        if (!enc) return cudaErrorNotSupported;
+        const int64_t rows = (p.cache.n_pages * p.cache.n_kv) << p.cache.lp;
+        if (rows > 0x7fffffff) return cudaErrorInvalidValue;        // beyond any GPU's memory at 128 bytes a row
+        const cuuint64_t dim[2] = {(cuuint64_t)D, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)D * 2};
+        const cuuint32_t box[2] = {64, (cuuint32_t)std::min(1 << p.cache.lp, kTcTile)}, one[2] = {1, 1};
+        for (int i = 0; i < 2; i++)
+            if (enc(i ? &vmap : &kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, i ? p.cache.v : p.cache.k, dim, stride, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorInvalidValue;
+    }
+    uint8_t *ws = reinterpret_cast<uint8_t *>(p.counters);
+    p.counters = reinterpret_cast<int *>(ws + kAttnCounterBytes);
+    p.part = reinterpret_cast<float *>(ws + kAttnHead);
+    const int grid = (int)std::max(1.0, std::min((double)ctas, attn_most(p, kTcTile, kTcTile)));
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    attn_config(cfg, attr, dim3(grid), G::THREADS, G::SMEM, s, pdl);
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern.fn, p, kmap, vmap, error)) return e;
+    if (grid == 1) return cudaSuccess;                              // nothing is shared
+    // the join may be set up while the first kernel runs: it waits for it before it reads
+    const int rows = std::min(kTcRows, p.max_q * p.group);
+    attn_config(cfg, attr, dim3(grid, (rows + 31) / 32), 256, 0, s, true);
+    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D>, p, grid);
+}
+
+// rows: the most rows (new tokens x heads of a group) of any sequence.  Up
+// to 16 one mma.sync row tile; more on tcgen05 for head_dim 64 and 128 (at 256
+// two streams' accumulators do not fit in tensor memory).
+template <int FMT>
+cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    void *word = nullptr;
+    if (!plan)
+        if (cudaError_t e = cudaGetSymbolAddress(&word, error_word)) return e;
+    int *error = static_cast<int *>(word);
+    const bool tc = rows >= attn_tc_rows();
+    if (D == 64)
+        return tc ? attn_tc_call<FMT, 64>(p, error, plan, s, pdl)
+             : rows <= 16 ? attn_rows_call<FMT, 64, 1>(p, error, plan, s, pdl) : attn_rows_call<FMT, 64, 2>(p, error, plan, s, pdl);
+    if (D == 128)
+        return tc ? attn_tc_call<FMT, 128>(p, error, plan, s, pdl)
+             : rows <= 16 ? attn_rows_call<FMT, 128, 1>(p, error, plan, s, pdl) : attn_rows_call<FMT, 128, 2>(p, error, plan, s, pdl);
+    return attn_rows_call<FMT, 256, 1>(p, error, plan, s, pdl);
 }
 
 }  // namespace bqg

@@ -50,6 +50,7 @@
 #include <cudaTypedefs.h>
 
 #include "bqg_common.cuh"
+#include "bqg_tc.cuh"
 
 namespace bqg {
 
@@ -117,35 +118,10 @@ template <int WF, int TERMS> using SmemOf = GemmSmem<WF, Pipe<TERMS>::NSTAGE, Pi
 constexpr uint32_t IDESC_BASE = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TM >> 4) << 24);
 __device__ __forceinline__ uint32_t idesc_n(int n) { return IDESC_BASE | ((uint32_t)(n >> 3) << 17); }
 
-// K-major, 128-byte swizzle smem descriptor: rows of 128 bytes in atoms of
-// 8 rows (1024 bytes); consecutive atoms along M/N are 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr)
-{
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3fff);            // start address
-    d |= (uint64_t)1 << 16;                            // leading byte offset (unused with swizzle)
-    d |= (uint64_t)(1024 >> 4) << 32;                  // stride byte offset: next 8-row atom
-    d |= (uint64_t)1 << 46;                            // descriptor version for tcgen05
-    d |= (uint64_t)2 << 61;                            // 128-byte swizzle
-    return d;
-}
-
-
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
-                 : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem descriptor]
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                             uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
                  : "memory");
 }
 
@@ -159,32 +135,6 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint4 (&v
                    "r"(v[1].z), "r"(v[1].w), "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x),
                    "r"(v[3].y), "r"(v[3].z), "r"(v[3].w)
                  : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-
-// 32 lanes x 32 columns of fp32 from tensor memory (this warp's lane quarter)
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
-{
-    uint32_t r[32];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
 }
 
 // two fp32 -> bf16x2, round to nearest even (lo in the low half)
@@ -491,7 +441,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_bf16_kernel(const __grid_
                         const uint64_t bdesc = sw128_desc(bx + kk * 32);
 #pragma unroll
                         for (int j = 0; j < TERMS; j++)      // the weight's bf16 terms, one MMA each
-                            umma_bf16_ts(dacc, aw + j * A_COLS + kk * 8, bdesc, idesc,
+                            umma_f16_ts(dacc, aw + j * A_COLS + kk * 8, bdesc, idesc,
                                          (k > 0 || kk > 0 || j > 0) ? 1u : 0u);
                     }
                     umma_commit(bar_empty(s));               // stage s is free when these MMAs finish
