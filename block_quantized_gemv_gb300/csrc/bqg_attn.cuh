@@ -178,14 +178,33 @@ __device__ __forceinline__ unsigned long long attn_sees(const AttnParams &p, con
     if (i >= s.T) return 0;
     return p.mask ? p.mask[s.q0 + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
 }
-// The sequence whose units (weight(sequence) of them) hold number u of the line of all sequences' units;
-// `base`: the number of its first.  Called by whole warps.
-template <typename W> __device__ __forceinline__ int attn_find(const AttnParams &p, int64_t u, int lane, W weight, int64_t &base)
+// a / b for a >= 0, b > 0: in 32 bits where both fit (a 64-bit division is a
+// hundred dependent instructions, and several stand before a CTA's first load).
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b)
+{
+    if ((uint64_t)(a | b) >> 32) return a / b;
+    return (int64_t)((uint32_t)a / (uint32_t)b);
+}
+// The units (weight(sequence) of them) of all sequences, and BQG_DEVERR_LENGTH in `bad` of some lanes; `mine`: of
+// sequence `lane`.  Called by whole warps, as attn_find is.
+template <typename W>
+__device__ __forceinline__ int64_t attn_total(const AttnParams &p, int lane, W weight, int &bad, int64_t &mine)
+{
+    mine = lane < p.n_seq ? weight(attn_seq(p, lane, bad)) : 0;
+    int64_t total = mine;
+    for (int b = lane + 32; b < p.n_seq; b += 32) total += weight(attn_seq(p, b, bad));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    return total;
+}
+// The sequence that holds number u of the line of all sequences' units; `base`: the number of its first.
+template <typename W>
+__device__ __forceinline__ int attn_find(const AttnParams &p, int64_t u, int lane, W weight, int64_t mine, int64_t &base)
 {
     base = 0;
     for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
         int bad = 0;
-        const int64_t mine = b0 + lane < p.n_seq ? weight(attn_seq(p, b0 + lane, bad)) : 0;
+        if (b0) mine = b0 + lane < p.n_seq ? weight(attn_seq(p, b0 + lane, bad)) : 0;
         int64_t sum = mine;                                                   // inclusive over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -201,15 +220,6 @@ template <typename W> __device__ __forceinline__ int attn_find(const AttnParams 
         base += __shfl_sync(0xffffffffu, sum, 31);
     }
     return p.n_seq;      // not reached for u below the total
-}
-// The units of all sequences, and BQG_DEVERR_LENGTH in `bad` of some lanes.
-template <typename W> __device__ __forceinline__ int64_t attn_total(const AttnParams &p, int lane, W weight, int &bad)
-{
-    int64_t total = 0;
-    for (int b = lane; b < p.n_seq; b += 32) total += weight(attn_seq(p, b, bad));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    return total;
 }
 
 // A finished row: E = D / 32 values per lane, divided by their sum of weights, in bf16.
@@ -582,14 +592,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
     // this CTA's range of units
     int bad = 0;
     auto weight = [&](const AttnSeq &q) { return A::units(p, q); };
-    const int64_t total = attn_total(p, lane, weight, bad);
+    int64_t mine;
+    const int64_t total = attn_total(p, lane, weight, bad, mine);
     if (bad && blockIdx.x == 0 && warp == 0) atomicOr(error, bad);
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t per = div_pos(total + gridDim.x - 1, gridDim.x);
     int64_t u = per * blockIdx.x;
     const int64_t u_end = min(u + per, total);
     if (u >= u_end) return;
     int64_t base;
-    int b = attn_find(p, u, lane, weight, base);
+    int b = attn_find(p, u, lane, weight, mine, base);
     AttnSeq s = attn_seq(p, b, bad);
     int pages_bad = 0;
 
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
         }
         const int64_t off = u - base;
         const int tiles = A::tiles_of(s), row_tiles = A::row_tiles_of(p, s);
-        const int pair = (int)(off / tiles), tile0 = (int)(off - (int64_t)pair * tiles);
+        const int pair = (int)div_pos(off, tiles), tile0 = (int)(off - (int64_t)pair * tiles);
         const int h = pair / row_tiles, row0 = (pair - h * row_tiles) * G::ROWS;
         const int n = (int)min((int64_t)(tiles - tile0), u_end - u);          // units of this piece
         const int64_t seg0 = u - tile0;                                       // first unit of the whole (sequence, head, row tile)
@@ -790,7 +801,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                 }
             }
         __syncthreads();
-        const int c0 = (int)(seg0 / per), c1 = (int)((seg0 + tiles - 1) / per);    // CTAs that share the segment
+        const int c0 = (int)div_pos(seg0, per), c1 = (int)div_pos(seg0 + tiles - 1, per);  // CTAs that share the segment
         const int cta = (int)blockIdx.x;
         constexpr int E = D / 32;                                             // values per lane of a row
         float *const part_ml = p.part + (int64_t)2 * gridDim.x * G::ROWS * D;

@@ -123,7 +123,7 @@ template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, Att
     int ctas = 0;
     if (cudaError_t e = attn_ctas(kern, G::THREADS, G::SMEM, &ctas)) return e;
     if (plan) {
-        plan->ws_bytes = kAttnHead + (size_t)2 * ctas * kTcRows * (D + 2) * sizeof(float);
+        plan->ws_bytes = kAttnHead + (size_t)2 * ctas * G::ROWS * (D + 2) * sizeof(float);
         return cudaSuccess;
     }
     // the cache as rows of D bf16 values: boxes of 64 values x the tokens of a page (at most a tile)
@@ -144,16 +144,16 @@ template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, Att
     uint8_t *ws = reinterpret_cast<uint8_t *>(p.counters);
     p.counters = reinterpret_cast<int *>(ws + kAttnCounterBytes);
     p.part = reinterpret_cast<float *>(ws + kAttnHead);
-    const int grid = (int)std::max(1.0, std::min((double)ctas, attn_most(p, kTcTile, kTcTile)));
+    const int grid = (int)std::max(1.0, std::min((double)ctas, attn_most(p, kTcTile, kTcHalf)));
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     attn_config(cfg, attr, dim3(grid), G::THREADS, G::SMEM, s, pdl);
     if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern.fn, p, kmap, vmap, error)) return e;
     if (grid == 1) return cudaSuccess;                              // nothing is shared
     // the join may be set up while the first kernel runs: it waits for it before it reads
-    const int rows = std::min(kTcRows, p.max_q * p.group);
+    const int rows = std::min(G::ROWS, p.max_q * p.group);
     attn_config(cfg, attr, dim3(grid, (rows + 31) / 32), 256, 0, s, true);
-    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D>, p, grid);
+    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D, G::ROWS>, p, grid);
 }
 
 // rows: the most rows (new tokens x heads of a group) of any sequence.  Up
