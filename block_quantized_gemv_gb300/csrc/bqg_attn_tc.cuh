@@ -785,17 +785,35 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             bool ok = true;
             auto build = [&](int x) {
                 const int rs = x % NR, slot = x % NS;
-                if (!(ok = wait(bar_rawf(rs), (x / NR) & 1))) return;
-                if (x >= NS && !(ok = wait(bar_empty(slot), ((x / NS) - 1) & 1))) return;
+                // lane 0 waits for the side, lane 1 for the slot's last products
+                {
+                    const uint32_t bar = lane == 0 ? bar_rawf(rs) : bar_empty(slot), ph = lane == 0 ? x / NR : x / NS - 1;
+                    bool there = lane > 1 || (lane == 1 && x < NS) || mbar_try_wait_nohint(bar, ph & 1);
+                    if (!__all_sync(0xffffffffu, there)) {
+                        if (!there) there = mbar_wait_spin(bar, ph & 1);
+                        if (!(ok = __all_sync(0xffffffffu, there))) {
+                            if (lane == 0) atomicOr(error, 2);
+                            return;
+                        }
+                    }
+                }
                 const int4 side = *reinterpret_cast<const int4 *>(smem + G::OFF_SIDES + 16 * rs);
-                const uint32_t src = sb + G::OFF_RAW + rs * G::RAW, dst = sb + G::OFF_RING + slot * G::TILE;
+                const uint32_t dst = sb + G::OFF_RING + slot * G::TILE;
+                const uint8_t *src = smem + G::OFF_RAW + rs * G::RAW;
+                constexpr int N = G::CHUNKS / 256;
+                uint4 codes[N];
+                uint32_t scale[N];
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    codes[i] = *reinterpret_cast<const uint4 *>(src + (i * 256 + lt) * 16);
+                    scale[i] = *reinterpret_cast<const uint16_t *>(src + kTcTile * G::RB + ((r0 + i * STEP) * G::NB + (FMT == BQG_Q8_0 ? c >> 1 : c)) * 2);
+                }
                 bool hit = false;
 #pragma unroll
-                for (int i = 0; i < G::CHUNKS / 256; i++) {
+                for (int i = 0; i < N; i++) {
                     const int r = r0 + i * STEP;
-                    const uint4 q = lds128(src + (i * 256 + lt) * 16);
-                    uint32_t d;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(d) : "r"(src + kTcTile * G::RB + (r * G::NB + (FMT == BQG_Q8_0 ? c >> 1 : c)) * 2) : "memory");
+                    const uint4 q = codes[i];
+                    uint32_t d = scale[i];
                     // no token: zeros; a new token's infinite or NaN scale: zeros, and marked
                     if (r >= side.x || ((side.z >> (r >> 4)) & 1)) d = 0;
                     if (r >= side.y && (d & 0x7c00u) == 0x7c00u) { d = 0; hit = true; }
