@@ -18,10 +18,13 @@
 //    inside one page), copied with cp.async into its own ring, 16-byte
 //    chunks permuted so that fragment loads meet no bank conflicts.
 //    Tokens behind a sequence's end are filled with zeros, never read.
-//  * The products go to the tensor cores (mma.sync m16n8k16, fp32
-//    accumulate), rows as the M side in tiles of 16, tokens as N of the
-//    first product and K of the second, so the probabilities go from one
-//    product's accumulators to the other's operand in registers.
+//  * The products go to the tensor cores (mma.sync m16n8k16, fp32 accumulate),
+//    transposed: S^T = K Q^T with the strip's 16 tokens as the M side and tiles of 8
+//    rows as N, then O^T = V^T P^T with the values as M, the tokens as K.  What a token costs
+//    then grows in steps of 8 rows, and one token has few (with the rows
+//    as M, 16 at least, half the products, scores, exponentials and
+//    accumulators of 8 rows were padding: 637 instructions per strip).  P^T
+//    goes from accumulators to operand with one movmatrix per 8 x 8.
 //    bf16: as stored.  q8_0 / q4_0: the codes are built as exact fp16 integers
 //    (a byte under 0x64 is 1024 + byte); a key block's two products give an
 //    exact block sum that is scaled by its fp16 scale in fp32; a value is
@@ -62,25 +65,26 @@ struct AttnParams {
     float *part;                         // [2 * CTAs][rows of a tile][D], then (maximum, sum) pairs
 };
 
-// Geometry of one instantiation: MT row tiles of 16 per CTA.
-template <int FMT, int D, int MT> struct AttnGeom {
-    static constexpr int ROWS = 16 * MT;
+// Geometry of one instantiation: RT row tiles of 8 per CTA.
+template <int FMT, int D, int RT> struct AttnGeom {
+    static constexpr int ROWS = 8 * RT;
     static constexpr int RB = KvRow<FMT, D>::BYTES;                     // bytes of a cached row
     static constexpr int NB = D / QK;                                   // blocks of a row
     static constexpr int CPT = RB / 16;                                 // 16-byte chunks of a row
     static constexpr int SCALES = (FMT == BQG_BF16) ? 0 : kStrip * NB * 2;
     static constexpr int STAGE = 2 * (kStrip * RB + SCALES);            // keys and values of a strip
-    // strips in flight per warp: about 64 KiB per SM and CTA pair or trio (see attn_stages)
-    static constexpr int S = (STAGE >= 16384) ? 3 : (STAGE >= 8192) ? 3 : (STAGE >= 4096) ? 4 : 6;
+    // strips in flight per warp, one less than stages
+    static constexpr int S = (STAGE >= 4096) ? 3 : 4;
     static constexpr int KS = D / 16;                                   // MMA steps of the first product
-    static constexpr bool QREG = MT * D <= 128;                         // query fragments held in registers
-    static constexpr int PAD = 16;                                      // floats between merged rows
+    static constexpr bool QREG = RT * D <= 256;                         // query fragments held in registers
+    static constexpr int PAD = 4;                                       // floats between merged rows: distinct banks
     static constexpr int RING = kAttnWarps * S * STAGE;
     static constexpr int MERGE = kAttnWarps * ROWS * (D + PAD) * 4;     // the ring's memory again, once drained
     static constexpr int OFF_Q = (RING > MERGE ? RING : MERGE);         // query fragments
-    static constexpr int OFF_P = OFF_Q + (QREG ? 0 : MT * KS * 512);    // probabilities of the exact path
-    static constexpr int OFF_ML = OFF_P + kAttnWarps * 16 * kStrip * 4; // (maximum, sum) per warp and row
-    static constexpr int OFF_RS = OFF_ML + kAttnWarps * ROWS * 8;       // softmax scale per row
+    static constexpr int OFF_P = OFF_Q + (QREG ? 0 : RT * KS * 256);    // probabilities of the exact path
+    static constexpr int OFF_ML = OFF_P + kAttnWarps * 8 * kStrip * 4;  // (maximum, sum) per warp and row
+    static constexpr int OFF_VIS = OFF_ML + kAttnWarps * ROWS * 8;      // new tokens that each row sees
+    static constexpr int OFF_RS = OFF_VIS + ROWS * 8;                   // softmax scale per row
     static constexpr int OFF_FLAG = OFF_RS + ROWS * 4;
     static constexpr int SMEM = OFF_FLAG + 16;
 };
@@ -119,6 +123,13 @@ template <bool BF> __device__ __forceinline__ void mma16816(float (&c)[4], const
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// (8 x 8 of 16 bits, row lane / 4, columns 2 (lane % 4)): transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
 }
 template <bool BF> __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -271,11 +282,11 @@ __device__ __forceinline__ void attn_join_row(const float *part, const float *pa
     }
 }
 
-template <int FMT, int D, int MT> struct AttnKernel {
-    using G = AttnGeom<FMT, D, MT>;
+template <int FMT, int D, int RT> struct AttnKernel {
+    using G = AttnGeom<FMT, D, RT>;
     static constexpr bool BF = (FMT == BQG_BF16);
     static constexpr float kShift = BF ? 0.0f : 8.0f;
-    static constexpr int NT = D / 8;                          // n-tiles of the output
+    static constexpr int MT = D / 16;                         // M tiles of the second product
 
     // 64-token tiles and row tiles of a sequence, and its units.
     static __device__ __forceinline__ int tiles_of(const AttnSeq &s) { return (s.len + kUnit - 1) / kUnit; }
@@ -288,178 +299,188 @@ template <int FMT, int D, int MT> struct AttnKernel {
         return (int64_t)p.cache.n_kv * row_tiles_of(p, s) * tiles_of(s);
     }
 
-    // The query fragments of row tile rows row0 .. row0 + 15 (KS steps x 4
-    // registers), and the softmax scales of this lane's two rows.
+    // The query fragments of rows row0 .. row0 + 7 (KS steps x 2 registers: row
+    // lane / 4), and the softmax scale of this lane's row.
     static __device__ __forceinline__ void load_q(const AttnParams &p, const AttnSeq &s, int h, int row0, int lane,
-                                                  uint32_t (&qf)[G::KS][4], float (&rs)[2])
+                                                  uint32_t (&qf)[G::KS][2], float &rs)
     {
-        const int g = lane >> 2, t = lane & 3;
+        const int t = lane & 3;
+        const uint16_t *src = attn_q_row(p, s, h, row0 + (lane >> 2), D);
+        rs = p.scale_log2;
+        if constexpr (BF) {
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-            const uint16_t *src = attn_q_row(p, s, h, row0 + g + 8 * r, D);
-            rs[r] = p.scale_log2;
-            if constexpr (BF) {
-#pragma unroll
-                for (int ks = 0; ks < G::KS; ks++) {
-                    qf[ks][r] = src ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t) : 0u;
-                    qf[ks][2 + r] = src ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 8 + 2 * t) : 0u;
-                }
-            } else {
-                // the order of the values within a block follows the codes' words:
-                // q8_0 lane t values 8t .. 8t + 7; q4_0 values 4t .. and 16 + 4t ..,
-                // even ones first
-                uint32_t w[G::NB][4];
-                float top = 0.f;
-#pragma unroll
-                for (int b = 0; b < G::NB; b++) {
-                    if constexpr (FMT == BQG_Q8_0) {
-                        const uint4 a = src ? *reinterpret_cast<const uint4 *>(src + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
-                        w[b][0] = a.x; w[b][1] = a.y; w[b][2] = a.z; w[b][3] = a.w;
-                    } else {
-                        const uint2 a = src ? *reinterpret_cast<const uint2 *>(src + 32 * b + 4 * t) : make_uint2(0, 0);
-                        const uint2 c = src ? *reinterpret_cast<const uint2 *>(src + 32 * b + 16 + 4 * t) : make_uint2(0, 0);
-                        w[b][0] = __byte_perm(a.x, a.y, 0x5410); w[b][1] = __byte_perm(a.x, a.y, 0x7632);
-                        w[b][2] = __byte_perm(c.x, c.y, 0x5410); w[b][3] = __byte_perm(c.x, c.y, 0x7632);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; j++) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[b][j])), fabsf(bf16_hi(w[b][j]))));
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                float inv = 1.f;
-                if (top > 0.f && top < __int_as_float(0x7f800000)) {
-                    const uint32_t ex = min(__float_as_uint(top) >> 23, 253u);
-                    inv = __uint_as_float((254u - ex) << 23);                       // 2^(127 - ex)
-                    rs[r] = fmaxf(p.scale_log2 * (1.0f / inv), 1.17549435e-38f);    // 1 / inv: a power of two
-                }
-#pragma unroll
-                for (int b = 0; b < G::NB; b++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const uint32_t f = pack2<false>(bf16_lo(w[b][j]) * inv, bf16_hi(w[b][j]) * inv);
-                        qf[2 * b + (j >> 1)][r + 2 * (j & 1)] = f;
-                    }
+            for (int ks = 0; ks < G::KS; ks++) {
+                qf[ks][0] = src ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t) : 0u;
+                qf[ks][1] = src ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 8 + 2 * t) : 0u;
             }
+        } else {
+            // the order of the values within a block follows the codes' words:
+            // q8_0 lane t values 8t .. 8t + 7; q4_0 values 4t .. and 16 + 4t ..,
+            // even ones first
+            uint32_t w[G::NB][4];
+            float top = 0.f;
+#pragma unroll
+            for (int b = 0; b < G::NB; b++) {
+                if constexpr (FMT == BQG_Q8_0) {
+                    const uint4 a = src ? *reinterpret_cast<const uint4 *>(src + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
+                    w[b][0] = a.x; w[b][1] = a.y; w[b][2] = a.z; w[b][3] = a.w;
+                } else {
+                    const uint2 a = src ? *reinterpret_cast<const uint2 *>(src + 32 * b + 4 * t) : make_uint2(0, 0);
+                    const uint2 c = src ? *reinterpret_cast<const uint2 *>(src + 32 * b + 16 + 4 * t) : make_uint2(0, 0);
+                    w[b][0] = __byte_perm(a.x, a.y, 0x5410); w[b][1] = __byte_perm(a.x, a.y, 0x7632);
+                    w[b][2] = __byte_perm(c.x, c.y, 0x5410); w[b][3] = __byte_perm(c.x, c.y, 0x7632);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[b][j])), fabsf(bf16_hi(w[b][j]))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            float inv = 1.f;
+            if (top > 0.f && top < __int_as_float(0x7f800000)) {
+                const uint32_t ex = min(__float_as_uint(top) >> 23, 253u);
+                inv = __uint_as_float((254u - ex) << 23);                       // 2^(127 - ex)
+                rs = fmaxf(p.scale_log2 * (1.0f / inv), 1.17549435e-38f);       // 1 / inv: a power of two
+            }
+#pragma unroll
+            for (int b = 0; b < G::NB; b++)
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    qf[2 * b + (j >> 1)][j & 1] = pack2<false>(bf16_lo(w[b][j]) * inv, bf16_hi(w[b][j]) * inv);
         }
     }
 
-    // Copies of strip tokens tok0 .. tok0 + 15 of (sequence, head) into `st`.
+    // Copies of strip tokens tok0 .. tok0 + 15 of (sequence, head) into `st`; ok: the page is in the cache.
     static __device__ __forceinline__ void issue(const AttnParams &p, const AttnSeq &s, int h, int tok0, int page, bool ok,
                                                  uint32_t st, int lane)
     {
         const int at = tok0 & ((1 << p.cache.lp) - 1);
         const int64_t row = ok ? ((((int64_t)page * p.cache.n_kv + h) << p.cache.lp) + at) : 0;
-        const int n = ok ? min(kStrip, s.len - tok0) : 0;                        // tokens to fetch
-        const uint8_t *k = p.cache.k + row * G::RB, *v = p.cache.v + row * G::RB;
+        const int n = ok ? s.len - tok0 : 0;                                     // tokens to fetch, if under 16
+        const uint8_t *k = p.cache.k + row * G::RB + lane * 16, *v = p.cache.v + row * G::RB + lane * 16;
+        constexpr int CH = BF ? 1 : G::SCALES / 16;                              // chunks of one side's scales
+        const uint8_t *sc = nullptr;
+        if constexpr (!BF)
+            sc = reinterpret_cast<const uint8_t *>((lane < CH ? p.cache.k_scale : p.cache.v_scale) + row * G::NB) + lane % CH * 16;
+        if (n >= kStrip) {
 #pragma unroll
-        for (int i = 0; i < G::CPT / 2; i++) {
-            const int x = i * 32 + lane, tok = x / G::CPT, c = x % G::CPT;
-            const uint32_t d = st + chunk_at<G::CPT>(tok, c);
-            const int bytes = tok < n ? 16 : 0;
-            cp_async16(d, k + (bytes ? x * 16 : 0), bytes);
-            cp_async16(d + kStrip * G::RB, v + (bytes ? x * 16 : 0), bytes);
-        }
-        if constexpr (!BF) {
-            constexpr int CH = G::SCALES / 16;                                   // chunks of one side's scales
-            const uint32_t d = st + 2 * kStrip * G::RB;
-            const uint8_t *ks = reinterpret_cast<const uint8_t *>(p.cache.k_scale + row * G::NB);
-            const uint8_t *vs = reinterpret_cast<const uint8_t *>(p.cache.v_scale + row * G::NB);
-            if (lane < 2 * CH) {
-                const int c = lane % CH;
-                const int bytes = min(max(n * G::NB * 2 - 16 * c, 0), 16);
-                cp_async16(d + lane * 16, (lane < CH ? ks : vs) + (bytes ? 16 * c : 0), bytes);
+            for (int i = 0; i < G::CPT / 2; i++) {
+                const uint32_t d = st + chunk_at<G::CPT>((i * 32 + lane) / G::CPT, lane % G::CPT);
+                cp_async16(d, k + i * 512, 16);
+                cp_async16(d + kStrip * G::RB, v + i * 512, 16);
             }
+            if constexpr (!BF)
+                if (lane < 2 * CH) cp_async16(st + 2 * kStrip * G::RB + lane * 16, sc, 16);
+        } else {                                                                 // zeros behind the end
+#pragma unroll
+            for (int i = 0; i < G::CPT / 2; i++) {
+                const int tok = (i * 32 + lane) / G::CPT;
+                const uint32_t d = st + chunk_at<G::CPT>(tok, lane % G::CPT);
+                const int bytes = tok < n ? 16 : 0;
+                cp_async16(d, bytes ? k + i * 512 : p.cache.k, bytes);
+                cp_async16(d + kStrip * G::RB, bytes ? v + i * 512 : p.cache.v, bytes);
+            }
+            if constexpr (!BF)
+                if (lane < 2 * CH) {
+                    const int bytes = min(max(n * G::NB * 2 - lane % CH * 16, 0), 16);
+                    cp_async16(st + 2 * kStrip * G::RB + lane * 16, bytes ? sc : reinterpret_cast<const uint8_t *>(p.cache.k_scale), bytes);
+                }
         }
     }
 
-    // Scores of the strip in stage `st` for MT row tiles: s[m][token tile][4].
-    template <typename QF> static __device__ __forceinline__ void scores(uint32_t st, int lane, const QF &qf, float (&s)[MT][2][4])
+    // Scores of the strip in stage `st`: s[row tile] = tokens lane / 4 (elements 0, 1) and 8 on (2, 3) x
+    // rows 2 (lane % 4) and the next.
+    template <typename QF> static __device__ __forceinline__ void scores(uint32_t st, int lane, const QF &qf, float (&s)[RT][4])
     {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int m = 0; m < MT; m++)
+        for (int m = 0; m < RT; m++)
 #pragma unroll
-            for (int x = 0; x < 2; x++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) s[m][x][i] = 0.f;
+            for (int i = 0; i < 4; i++) s[m][i] = 0.f;
         if constexpr (BF) {
-            const int tok = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+            const int tok = lane & 15, hi = lane >> 4;
 #pragma unroll
             for (int ks = 0; ks < G::KS; ks++) {
-                uint32_t b[4];
-                ldsm_x4(st + chunk_at<G::CPT>(tok, 2 * ks + half), b);
+                uint32_t a[4];
+                ldsm_x4(st + chunk_at<G::CPT>(tok, 2 * ks + hi), a);
 #pragma unroll
-                for (int m = 0; m < MT; m++) {
-                    uint32_t a[4];
-                    qf.get(m, ks, a);
-                    mma16816<true>(s[m][0], a, b[0], b[1]);
-                    mma16816<true>(s[m][1], a, b[2], b[3]);
+                for (int m = 0; m < RT; m++) {
+                    uint32_t b[2];
+                    qf.get(m, ks, b);
+                    mma16816<true>(s[m], a, b[0], b[1]);
                 }
             }
         } else {
             const uint32_t sc = st + 2 * kStrip * G::RB;
+            uint32_t dw[2][G::NB / 2];                   // scales of tokens g and g + 8
 #pragma unroll
             for (int x = 0; x < 2; x++) {
-                uint32_t dw[G::NB];                      // scales of tokens 8x + 2t (first half) and + 1
+                const uint32_t at = sc + (8 * x + g) * G::NB * 2;
+                if constexpr (G::NB == 2) {
+                    dw[x][0] = lds32(at);
+                } else {
 #pragma unroll
-                for (int i = 0; i < G::NB; i += 2) {
-                    const uint2 v = lds64(sc + ((8 * x + 2 * t) * G::NB + 2 * i) * 2);
-                    dw[i] = v.x; dw[i + 1] = v.y;
+                    for (int i = 0; i < G::NB / 2; i += 2) {
+                        const uint2 v = lds64(at + 4 * i);
+                        dw[x][i] = v.x; dw[x][i + 1] = v.y;
+                    }
                 }
+            }
 #pragma unroll
-                for (int b = 0; b < G::NB; b++) {
-                    uint32_t e[4];
+            for (int b = 0; b < G::NB; b++) {
+                uint32_t e[2][4];                        // of tokens g, g + 8: the operand's value pairs, MMA 0 then 1
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
                     if constexpr (FMT == BQG_Q8_0) {
                         uint2 w = lds64(st + chunk_at<G::CPT>(8 * x + g, 2 * b + (t >> 1)) + (t & 1) * 8);
                         w.x ^= 0x80808080u; w.y ^= 0x80808080u;              // q + 128
-                        e[0] = hsub2(__byte_perm(w.x, 0x64646464u, 0x4140), 0x64806480u);
-                        e[1] = hsub2(__byte_perm(w.x, 0x64646464u, 0x4342), 0x64806480u);
-                        e[2] = hsub2(__byte_perm(w.y, 0x64646464u, 0x4140), 0x64806480u);
-                        e[3] = hsub2(__byte_perm(w.y, 0x64646464u, 0x4342), 0x64806480u);
+                        e[x][0] = hsub2(__byte_perm(w.x, 0x64646464u, 0x4140), 0x64806480u);
+                        e[x][1] = hsub2(__byte_perm(w.x, 0x64646464u, 0x4342), 0x64806480u);
+                        e[x][2] = hsub2(__byte_perm(w.y, 0x64646464u, 0x4140), 0x64806480u);
+                        e[x][3] = hsub2(__byte_perm(w.y, 0x64646464u, 0x4342), 0x64806480u);
                     } else {
-                        const uint32_t w = lds32(st + chunk_at<G::CPT>(8 * x + g, b) + t * 4);
-                        e[0] = hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                        e[1] = hsub2(((w >> 8) & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                        e[2] = hsub2(((w >> 4) & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                        e[3] = hsub2(((w >> 12) & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        // a nibble at bits 0..3 under 0x64 is 1024 + n, at bits 4..7 under 0x54 it is 64 + n
+                        const uint32_t w = lds32(st + chunk_at<G::CPT>(8 * x + g, b) + t * 4), w8 = w >> 8;
+                        e[x][0] = hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        e[x][1] = hsub2((w8 & 0x000f000fu) | 0x64006400u, 0x64086408u);
+                        e[x][2] = hsub2((w & 0x00f000f0u) | 0x54005400u, 0x54805480u);
+                        e[x][3] = hsub2((w8 & 0x00f000f0u) | 0x54005400u, 0x54805480u);
                     }
-                    const uint32_t h0 = dw[b >> 1], h1 = dw[(G::NB + b) >> 1];
-                    const float d0 = half_bits_to_float((b & 1) ? h0 >> 16 : h0 & 0xffffu);
-                    const float d1 = half_bits_to_float((b & 1) ? h1 >> 16 : h1 & 0xffffu);
+                }
+                const uint32_t h0 = dw[0][b >> 1], h1 = dw[1][b >> 1];
+                const float d0 = half_bits_to_float((b & 1) ? h0 >> 16 : h0 & 0xffffu);
+                const float d1 = half_bits_to_float((b & 1) ? h1 >> 16 : h1 & 0xffffu);
+                const uint32_t a0[4] = {e[0][0], e[1][0], e[0][1], e[1][1]}, a1[4] = {e[0][2], e[1][2], e[0][3], e[1][3]};
 #pragma unroll
-                    for (int m = 0; m < MT; m++) {
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                        uint32_t a[4];
-                        qf.get(m, 2 * b, a);
-                        mma16816<false>(acc, a, e[0], e[1]);
-                        qf.get(m, 2 * b + 1, a);
-                        mma16816<false>(acc, a, e[2], e[3]);
-                        s[m][x][0] = fmaf(acc[0], d0, s[m][x][0]);
-                        s[m][x][1] = fmaf(acc[1], d1, s[m][x][1]);
-                        s[m][x][2] = fmaf(acc[2], d0, s[m][x][2]);
-                        s[m][x][3] = fmaf(acc[3], d1, s[m][x][3]);
-                    }
+                for (int m = 0; m < RT; m++) {
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t q[2];
+                    qf.get(m, 2 * b, q);
+                    mma16816<false>(acc, a0, q[0], q[1]);
+                    qf.get(m, 2 * b + 1, q);
+                    mma16816<false>(acc, a1, q[0], q[1]);
+                    s[m][0] = fmaf(acc[0], d0, s[m][0]);
+                    s[m][1] = fmaf(acc[1], d0, s[m][1]);
+                    s[m][2] = fmaf(acc[2], d1, s[m][2]);
+                    s[m][3] = fmaf(acc[3], d1, s[m][3]);
                 }
             }
         }
     }
 
-    // o += P V for the strip in stage `st`.
-    static __device__ __forceinline__ void add_values(uint32_t st, int lane, const uint32_t (&pa)[MT][4], float (&o)[MT][NT][4])
+    // o += V^T P^T for the strip in stage `st`.
+    static __device__ __forceinline__ void add_values(uint32_t st, int lane, const uint32_t (&pb)[RT][2], float (&o)[RT][MT][4])
     {
         const int t = lane & 3;
         const uint32_t vst = st + kStrip * G::RB;
         const int tok = lane & 15, hi = lane >> 4;       // ldmatrix rows: tokens 0..15 of chunk c, then of c + 1
         if constexpr (BF) {
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t b[4];
-                ldsm_x4_trans(vst + chunk_at<G::CPT>(tok, n + hi), b);
+            for (int n = 0; n < MT; n++) {
+                uint32_t r[4];
+                ldsm_x4_trans(vst + chunk_at<G::CPT>(tok, 2 * n + hi), r);
+                const uint32_t a[4] = {r[0], r[2], r[1], r[3]};
 #pragma unroll
-                for (int m = 0; m < MT; m++) {
-                    mma16816<true>(o[m][n], pa[m], b[0], b[1]);
-                    mma16816<true>(o[m][n + 1], pa[m], b[2], b[3]);
-                }
+                for (int m = 0; m < RT; m++) mma16816<true>(o[m][n], a, pb[m][0], pb[m][1]);
             }
         } else {
             const uint32_t sc = st + 2 * kStrip * G::RB + G::SCALES;
@@ -474,18 +495,15 @@ template <int FMT, int D, int MT> struct AttnKernel {
             auto pair = [&](int x, int b) {              // (scale of token 8x + 2t, of 8x + 2t + 1) of block b
                 return __byte_perm(dw[x][b >> 1], dw[x][(G::NB + b) >> 1], (b & 1) ? 0x7632 : 0x5410);
             };
-            // sixteen values (n-tiles 2 i and 2 i + 1: even and odd ones): word lo of tokens 0..7, hi of 8..15,
-            // one biased code per byte
-            auto tiles = [&](int i, uint32_t lo, uint32_t up, uint32_t bias, uint32_t s0, uint32_t s1) {
-                const uint32_t b00 = hmul2(hsub2(__byte_perm(lo, 0x64646464u, 0x4240), bias), s0);
-                const uint32_t b01 = hmul2(hsub2(__byte_perm(up, 0x64646464u, 0x4240), bias), s1);
-                const uint32_t b10 = hmul2(hsub2(__byte_perm(lo, 0x64646464u, 0x4341), bias), s0);
-                const uint32_t b11 = hmul2(hsub2(__byte_perm(up, 0x64646464u, 0x4341), bias), s1);
+            // sixteen values, the even ones as the tile's rows 0..7, the odd ones as 8..15: word lo of tokens 0..7,
+            // up of 8..15, one biased code per byte
+            auto tile = [&](int n, uint32_t lo, uint32_t up, uint32_t bias, uint32_t s0, uint32_t s1) {
+                const uint32_t a[4] = {hmul2(hsub2(__byte_perm(lo, 0x64646464u, 0x4240), bias), s0),
+                                       hmul2(hsub2(__byte_perm(lo, 0x64646464u, 0x4341), bias), s0),
+                                       hmul2(hsub2(__byte_perm(up, 0x64646464u, 0x4240), bias), s1),
+                                       hmul2(hsub2(__byte_perm(up, 0x64646464u, 0x4341), bias), s1)};
 #pragma unroll
-                for (int m = 0; m < MT; m++) {
-                    mma16816<false>(o[m][2 * i], pa[m], b00, b01);
-                    mma16816<false>(o[m][2 * i + 1], pa[m], b10, b11);
-                }
+                for (int m = 0; m < RT; m++) mma16816<false>(o[m][n], a, pb[m][0], pb[m][1]);
             };
             if constexpr (FMT == BQG_Q8_0) {
 #pragma unroll
@@ -493,8 +511,8 @@ template <int FMT, int D, int MT> struct AttnKernel {
                     uint32_t r[4];
                     ldsm_x4_trans(vst + chunk_at<G::CPT>(tok, 2 * b + hi), r);
                     const uint32_t s0 = pair(0, b), s1 = pair(1, b);
-                    tiles(2 * b, r[0] ^ 0x80808080u, r[1] ^ 0x80808080u, 0x64806480u, s0, s1);
-                    tiles(2 * b + 1, r[2] ^ 0x80808080u, r[3] ^ 0x80808080u, 0x64806480u, s0, s1);
+                    tile(2 * b, r[0] ^ 0x80808080u, r[1] ^ 0x80808080u, 0x64806480u, s0, s1);
+                    tile(2 * b + 1, r[2] ^ 0x80808080u, r[3] ^ 0x80808080u, 0x64806480u, s0, s1);
                 }
             } else {
 #pragma unroll
@@ -504,19 +522,16 @@ template <int FMT, int D, int MT> struct AttnKernel {
 #pragma unroll
                     for (int j = 0; j < 2; j++) {
                         const uint32_t s0 = pair(0, b + j), s1 = pair(1, b + j);
-                        tiles(2 * (b + j), r[2 * j] & 0x0f0f0f0fu, r[2 * j + 1] & 0x0f0f0f0fu, 0x64086408u, s0, s1);
-                        tiles(2 * (b + j) + 1, (r[2 * j] >> 4) & 0x0f0f0f0fu, (r[2 * j + 1] >> 4) & 0x0f0f0f0fu, 0x64086408u, s0, s1);
+                        tile(2 * (b + j), r[2 * j] & 0x0f0f0f0fu, r[2 * j + 1] & 0x0f0f0f0fu, 0x64086408u, s0, s1);
+                        tile(2 * (b + j) + 1, (r[2 * j] >> 4) & 0x0f0f0f0fu, (r[2 * j + 1] >> 4) & 0x0f0f0f0fu, 0x64086408u, s0, s1);
                     }
                 }
             }
         }
     }
 
-    // Value `dim` of the output that element i of n-tile n is, for lane % 4 = t.
-    static __device__ __forceinline__ int dim_of(int n, int i, int t)
-    {
-        return BF ? 8 * n + 2 * t + i : 16 * (n >> 1) + 4 * t + 2 * i + (n & 1);
-    }
+    // The output's value that row g (hi: g + 8) of M tile n is.
+    static __device__ __forceinline__ int dim_of(int n, int g, int hi) { return BF ? 16 * n + 8 * hi + g : 16 * n + 2 * g + hi; }
     // Value `dim` of token `tok` of the staged strip, in fp32.
     static __device__ __forceinline__ float value_of(uint32_t st, int tok, int dim)
     {
@@ -556,35 +571,32 @@ template <int FMT, int D, int MT> struct AttnKernel {
 };
 
 // Query fragments in registers, or shared by the CTA's warps in shared memory.
-template <int MT, int KS> struct QRegs {
-    uint32_t f[MT][KS][4];
-    __device__ __forceinline__ void get(int m, int ks, uint32_t (&a)[4]) const
-    {
-#pragma unroll
-        for (int i = 0; i < 4; i++) a[i] = f[m][ks][i];
-    }
+template <int RT, int KS> struct QRegs {
+    uint32_t f[RT][KS][2];
+    __device__ __forceinline__ void get(int m, int ks, uint32_t (&b)[2]) const { b[0] = f[m][ks][0]; b[1] = f[m][ks][1]; }
 };
-template <int MT, int KS> struct QShared {
-    uint32_t addr;      // this lane's 16 bytes of fragment (0, 0)
-    __device__ __forceinline__ void get(int m, int ks, uint32_t (&a)[4]) const
+template <int RT, int KS> struct QShared {
+    uint32_t addr;      // this lane's 8 bytes of fragment (0, 0)
+    __device__ __forceinline__ void get(int m, int ks, uint32_t (&b)[2]) const
     {
-        const uint4 v = lds128(addr + (m * KS + ks) * 512);
-        a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
+        const uint2 v = lds64(addr + (m * KS + ks) * 256);
+        b[0] = v.x; b[1] = v.y;
     }
 };
 
-template <int FMT, int D, int MT>
+template <int FMT, int D, int RT>
 __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams p, int *error)
 {
-    using G = AttnGeom<FMT, D, MT>;
-    using A = AttnKernel<FMT, D, MT>;
-    constexpr int S = G::S, NT = A::NT;
+    using G = AttnGeom<FMT, D, RT>;
+    using A = AttnKernel<FMT, D, RT>;
+    constexpr int S = G::S, MT = A::MT;
     constexpr float NEG = -__builtin_huge_valf();
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     float *const ml = reinterpret_cast<float *>(smem + G::OFF_ML);            // [warp][row][2]
     float *const row_scale = reinterpret_cast<float *>(smem + G::OFF_RS);
+    unsigned long long *const row_sees = reinterpret_cast<unsigned long long *>(smem + G::OFF_VIS);
     float *const merged = reinterpret_cast<float *>(smem);                    // [warp][row][D + PAD]
     pdl_wait();
     pdl_launch_dependents();
@@ -617,45 +629,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
         const int64_t seg0 = u - tile0;                                       // first unit of the whole (sequence, head, row tile)
         const int rows = min(G::ROWS, s.T * p.group - row0);
 
-        // queries
-        float rs[MT][2];
-        unsigned long long vis[MT][2];                                        // new tokens that each row sees
-        std::conditional_t<G::QREG, QRegs<MT, G::KS>, QShared<MT, G::KS>> qf;
-        if constexpr (G::QREG) {
-#pragma unroll
-            for (int m = 0; m < MT; m++) A::load_q(p, s, h, row0 + 16 * m, lane, qf.f[m], rs[m]);
-        } else {
-            qf.addr = sb + G::OFF_Q + lane * 16;
-            for (int m = warp; m < MT; m += kAttnWarps) {
-                uint32_t f[G::KS][4];
-                float r2[2];
-                A::load_q(p, s, h, row0 + 16 * m, lane, f, r2);
-#pragma unroll
-                for (int ks = 0; ks < G::KS; ks++)
-                    *reinterpret_cast<uint4 *>(smem + G::OFF_Q + (m * G::KS + ks) * 512 + lane * 16) =
-                        make_uint4(f[ks][0], f[ks][1], f[ks][2], f[ks][3]);
-                if (t == 0) { row_scale[16 * m + g] = r2[0]; row_scale[16 * m + g + 8] = r2[1]; }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int m = 0; m < MT; m++) { rs[m][0] = row_scale[16 * m + g]; rs[m][1] = row_scale[16 * m + g + 8]; }
-        }
-#pragma unroll
-        for (int m = 0; m < MT; m++)
-#pragma unroll
-            for (int r = 0; r < 2; r++) vis[m][r] = attn_sees(p, s, row0 + 16 * m + g + 8 * r);
-
-        float o[MT][NT][4], top[MT][2], sum[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; m++) {
-            top[m][0] = top[m][1] = NEG;
-            sum[m][0] = sum[m][1] = 0.f;
-#pragma unroll
-            for (int x = 0; x < NT; x++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) o[m][x][i] = 0.f;
-        }
-
         // strips of this warp: tokens 64 (tile0 + j) + 16 warp ..
         const uint32_t ring = sb + warp * S * G::STAGE;
         const int32_t *table = p.table + (int64_t)s.b * p.max_pages;
@@ -665,9 +638,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
         };
         unsigned valid = 0;                                                   // stages whose page is in the cache
         int page = page_of(0);
-        auto issue = [&](int j) {
+        auto issue = [&](int j, int st) {
             const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
-            const int st = j % S;
             valid &= ~(1u << st);
             if (j < n && tok0 < s.len) {
                 const bool ok = page >= 0 && page < p.cache.n_pages;
@@ -679,125 +651,160 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
             page = page_of(j + 1);
         };
 #pragma unroll 1
-        for (int j = 0; j < S - 1; j++) issue(j);
+        for (int j = 0; j < S - 1; j++) issue(j, j);
+
+        // queries, and what their rows see
+        std::conditional_t<G::QREG, QRegs<RT, G::KS>, QShared<RT, G::KS>> qf;
+        if constexpr (G::QREG) {
+#pragma unroll
+            for (int m = 0; m < RT; m++) {
+                float r;
+                A::load_q(p, s, h, row0 + 8 * m, lane, qf.f[m], r);
+                if (warp == 0 && t == 0) row_scale[8 * m + g] = r;
+            }
+        } else {
+            qf.addr = sb + G::OFF_Q + lane * 8;
+            for (int m = warp; m < RT; m += kAttnWarps) {
+                uint32_t f[G::KS][2];
+                float r;
+                A::load_q(p, s, h, row0 + 8 * m, lane, f, r);
+#pragma unroll
+                for (int ks = 0; ks < G::KS; ks++)
+                    *reinterpret_cast<uint2 *>(smem + G::OFF_Q + (m * G::KS + ks) * 256 + lane * 8) = make_uint2(f[ks][0], f[ks][1]);
+                if (t == 0) row_scale[8 * m + g] = r;
+            }
+        }
+        if (tid < G::ROWS) row_sees[tid] = attn_sees(p, s, row0 + tid);
+        __syncthreads();
+        float rs[RT][2];                                                      // rows 8 m + 2 t, + 1
+        float o[RT][MT][4], top[RT][2], sum[RT][2];
+#pragma unroll
+        for (int m = 0; m < RT; m++) {
+            rs[m][0] = row_scale[8 * m + 2 * t];
+            rs[m][1] = row_scale[8 * m + 2 * t + 1];
+            top[m][0] = top[m][1] = NEG;
+            sum[m][0] = sum[m][1] = 0.f;
+#pragma unroll
+            for (int x = 0; x < MT; x++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) o[m][x][i] = 0.f;
+        }
+
+        int stage = 0;                                                        // j % S
 #pragma unroll 1
         for (int j = 0; j < n; j++) {
             cp_async_wait<S - 2>();
             __syncwarp();
-            issue(j + S - 1);
+            issue(j + S - 1, stage ? stage - 1 : S - 1);
             const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
             if (tok0 >= s.len) break;
-            const uint32_t st = ring + (j % S) * G::STAGE;
-            const bool ok = (valid >> (j % S)) & 1;
+            const uint32_t st = ring + stage * G::STAGE;
+            const bool ok = (valid >> stage) & 1;
+            stage = stage + 1 == S ? 0 : stage + 1;
 
-            float sc[MT][2][4];
+            float sc[RT][4];
             A::scores(st, lane, qf, sc);
             const bool edge = tok0 + kStrip > s.ctx || !ok;                   // new tokens, the end, or no page
             if (edge) {
 #pragma unroll
-                for (int m = 0; m < MT; m++)
+                for (int m = 0; m < RT; m++)
 #pragma unroll
-                    for (int x = 0; x < 2; x++)
+                    for (int r = 0; r < 2; r++) {
+                        const unsigned long long sees = row_sees[8 * m + 2 * t + r];
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const int tok = tok0 + 8 * x + 2 * t + (i & 1);
-                            const bool see = ok && (tok < s.ctx || (tok < s.len && ((vis[m][i >> 1] >> (tok - s.ctx)) & 1)));
-                            if (!see) sc[m][x][i] = NEG;
+                        for (int x = 0; x < 2; x++) {
+                            const int tok = tok0 + 8 * x + g;
+                            const bool see = ok && (tok < s.ctx || (tok < s.len && ((sees >> (tok - s.ctx)) & 1)));
+                            if (!see) sc[m][2 * x + r] = NEG;
                         }
+                    }
             }
             // raise the running maximum where a score is well above it
             bool raise = false;
-            float lm[MT][2];
 #pragma unroll
-            for (int m = 0; m < MT; m++)
+            for (int m = 0; m < RT; m++)
 #pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    lm[m][r] = fmaxf(fmaxf(sc[m][0][2 * r], sc[m][0][2 * r + 1]), fmaxf(sc[m][1][2 * r], sc[m][1][2 * r + 1])) * rs[m][r];
-                    raise |= lm[m][r] > top[m][r] + kSlack;
-                }
+                for (int r = 0; r < 2; r++) raise |= fmaxf(sc[m][r], sc[m][2 + r]) * rs[m][r] > top[m][r] + kSlack;
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int m = 0; m < MT; m++)
+                for (int m = 0; m < RT; m++)
 #pragma unroll
                     for (int r = 0; r < 2; r++) {
-                        float v = fmaxf(lm[m][r], __shfl_xor_sync(0xffffffffu, lm[m][r], 1));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                        float v = fmaxf(sc[m][r], sc[m][2 + r]) * rs[m][r];
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                         v = fmaxf(v, top[m][r]);
                         const float c = (v == top[m][r]) ? 1.f : ex2(top[m][r] - v);
                         top[m][r] = v;
                         sum[m][r] *= c;
 #pragma unroll
-                        for (int x = 0; x < NT; x++) { o[m][x][2 * r] *= c; o[m][x][2 * r + 1] *= c; }
+                        for (int x = 0; x < MT; x++) { o[m][x][r] *= c; o[m][x][2 + r] *= c; }
                     }
             }
-            uint32_t pa[MT][4];
+            uint32_t pb[RT][2];
+            const bool exact = edge && A::any_nonfinite(st, lane);
+            float *const pw = reinterpret_cast<float *>(smem + G::OFF_P) + warp * 8 * kStrip;
 #pragma unroll
-            for (int m = 0; m < MT; m++)
+            for (int m = 0; m < RT; m++) {
+                float e[4];
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
                     const float off = A::kShift - (top[m][r] == NEG ? 0.f : top[m][r]);
-#pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        const float e0 = ex2(fmaf(sc[m][x][2 * r], rs[m][r], off)), e1 = ex2(fmaf(sc[m][x][2 * r + 1], rs[m][r], off));
-                        sum[m][r] += e0 + e1;
-                        pa[m][2 * x + r] = pack2<A::BF>(e0, e1);
-                        sc[m][x][2 * r] = sc[m][x][2 * r] == NEG ? -1.f : e0;        // for the exact path
-                        sc[m][x][2 * r + 1] = sc[m][x][2 * r + 1] == NEG ? -1.f : e1;
-                    }
+                    e[r] = ex2(fmaf(sc[m][r], rs[m][r], off));
+                    e[2 + r] = ex2(fmaf(sc[m][2 + r], rs[m][r], off));
+                    sum[m][r] += e[r] + e[2 + r];
                 }
-            if (edge && A::any_nonfinite(st, lane)) {
-                // an infinity or NaN among tokens that some rows do not see: 0 x inf must
-                // not reach them, so this strip's products are taken one by one in fp32
-                float *const pw = reinterpret_cast<float *>(smem + G::OFF_P) + warp * 16 * kStrip;
-#pragma unroll
-                for (int m = 0; m < MT; m++) {
+                pb[m][0] = transpose8x8(pack2<A::BF>(e[0], e[1]));
+                pb[m][1] = transpose8x8(pack2<A::BF>(e[2], e[3]));
+                if (exact) {
+                    // an infinity or NaN among tokens that some rows do not see: 0 x inf must
+                    // not reach them, so this strip's products are taken one by one in fp32
                     __syncwarp();
 #pragma unroll
-                    for (int x = 0; x < 2; x++)
-#pragma unroll
-                        for (int i = 0; i < 4; i++) pw[(g + 8 * (i >> 1)) * kStrip + 8 * x + 2 * t + (i & 1)] = sc[m][x][i];
+                    for (int i = 0; i < 4; i++) pw[(8 * (i >> 1) + g) * 8 + 2 * t + (i & 1)] = sc[m][i] == NEG ? -1.f : e[i];
                     __syncwarp();
 #pragma unroll 1
                     for (int k = 0; k < kStrip; k++) {
-                        const float p0 = pw[g * kStrip + k], p1 = pw[(g + 8) * kStrip + k];
+                        const float p0 = pw[k * 8 + 2 * t], p1 = pw[k * 8 + 2 * t + 1];
 #pragma unroll
-                        for (int x = 0; x < NT; x++)
+                        for (int x = 0; x < MT; x++)
 #pragma unroll
-                            for (int i = 0; i < 2; i++) {
-                                const float v = A::value_of(st, k, A::dim_of(x, i, t));
-                                if (!(p0 < 0.f)) o[m][x][i] = fmaf(p0, v, o[m][x][i]);
-                                if (!(p1 < 0.f)) o[m][x][2 + i] = fmaf(p1, v, o[m][x][2 + i]);
+                            for (int hi = 0; hi < 2; hi++) {
+                                const float v = A::value_of(st, k, A::dim_of(x, g, hi));
+                                if (!(p0 < 0.f)) o[m][x][2 * hi] = fmaf(p0, v, o[m][x][2 * hi]);
+                                if (!(p1 < 0.f)) o[m][x][2 * hi + 1] = fmaf(p1, v, o[m][x][2 * hi + 1]);
                             }
                     }
                 }
-            } else {
-                A::add_values(st, lane, pa, o);
             }
+            if (!exact) A::add_values(st, lane, pb, o);
         }
         cp_async_wait<0>();
         __syncthreads();                                                      // the ring's memory is free
 
         // the four warps' results of this piece, joined
 #pragma unroll
-        for (int m = 0; m < MT; m++)
+        for (int m = 0; m < RT; m++)
 #pragma unroll
             for (int r = 0; r < 2; r++) {
-                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 1);
-                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 2);
-                const int row = 16 * m + g + 8 * r;
-                if (t == 0) {
+                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 4);
+                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 8);
+                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 16);
+                const int row = 8 * m + 2 * t + r;
+                if (g == 0) {
                     ml[(warp * G::ROWS + row) * 2] = top[m][r];
                     ml[(warp * G::ROWS + row) * 2 + 1] = sum[m][r];
                 }
                 float *dst = merged + (warp * G::ROWS + row) * (D + G::PAD);
-                if constexpr (A::BF) {
 #pragma unroll
-                    for (int x = 0; x < NT; x++) *reinterpret_cast<float2 *>(dst + 8 * x + 2 * t) = make_float2(o[m][x][2 * r], o[m][x][2 * r + 1]);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < NT; x += 2)
-                        *reinterpret_cast<float4 *>(dst + 8 * x + 4 * t) =
-                            make_float4(o[m][x][2 * r], o[m][x + 1][2 * r], o[m][x][2 * r + 1], o[m][x + 1][2 * r + 1]);
+                for (int x = 0; x < MT; x++) {
+                    if constexpr (A::BF) {
+                        dst[16 * x + g] = o[m][x][r];
+                        dst[16 * x + 8 + g] = o[m][x][2 + r];
+                    } else {
+                        *reinterpret_cast<float2 *>(dst + 16 * x + 2 * g) = make_float2(o[m][x][r], o[m][x][2 + r]);
+                    }
                 }
             }
         __syncthreads();

@@ -90,12 +90,12 @@ inline double attn_most(const AttnParams &p, int tile, int rows)
 }
 
 // mma.sync kernel: plans the call (plan) or, plan null, launches it.
-template <int FMT, int D, int MT>
+template <int FMT, int D, int RT>
 cudaError_t attn_rows_call(AttnParams p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
-    using G = AttnGeom<FMT, D, MT>;
+    using G = AttnGeom<FMT, D, RT>;
     struct Kern {
-        void (*fn)(const AttnParams, int *) = attn_kernel<FMT, D, MT>;
+        void (*fn)(const AttnParams, int *) = attn_kernel<FMT, D, RT>;
         int most = kAttnMaxCtas;
     } kern;
     int ctas = 0;
@@ -156,8 +156,18 @@ template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, Att
     return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D, G::ROWS>, p, grid);
 }
 
-// rows: the most rows (new tokens x heads of a group) of any sequence.  Up
-// to 16 one mma.sync row tile; more on tcgen05 for head_dim 64 and 128 (at 256
+// The mma.sync kernel with enough row tiles of 8 for `rows` rows, up to 32
+// (16 at head_dim 256, whose accumulators would not fit in registers).
+template <int FMT, int D> cudaError_t attn_rows_pick(const AttnParams &p, int rows, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    if (rows <= 8) return attn_rows_call<FMT, D, 1>(p, error, plan, s, pdl);
+    if (rows <= 16 || D == 256) return attn_rows_call<FMT, D, 2>(p, error, plan, s, pdl);
+    if constexpr (D < 256) return attn_rows_call<FMT, D, 4>(p, error, plan, s, pdl);
+    return cudaErrorInvalidValue;
+}
+
+// rows: the most rows (new tokens x heads of a group) of any sequence.  Few
+// on mma.sync; more on tcgen05 for head_dim 64 and 128 (at 256
 // two streams' accumulators do not fit in tensor memory).
 template <int FMT>
 cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, AttnPlan *plan, cudaStream_t s, bool pdl)
@@ -167,13 +177,9 @@ cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, A
         if (cudaError_t e = cudaGetSymbolAddress(&word, error_word)) return e;
     int *error = static_cast<int *>(word);
     const bool tc = rows >= attn_tc_rows();
-    if (D == 64)
-        return tc ? attn_tc_call<FMT, 64>(p, error, plan, s, pdl)
-             : rows <= 16 ? attn_rows_call<FMT, 64, 1>(p, error, plan, s, pdl) : attn_rows_call<FMT, 64, 2>(p, error, plan, s, pdl);
-    if (D == 128)
-        return tc ? attn_tc_call<FMT, 128>(p, error, plan, s, pdl)
-             : rows <= 16 ? attn_rows_call<FMT, 128, 1>(p, error, plan, s, pdl) : attn_rows_call<FMT, 128, 2>(p, error, plan, s, pdl);
-    return attn_rows_call<FMT, 256, 1>(p, error, plan, s, pdl);
+    if (D == 64) return tc ? attn_tc_call<FMT, 64>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 64>(p, rows, error, plan, s, pdl);
+    if (D == 128) return tc ? attn_tc_call<FMT, 128>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 128>(p, rows, error, plan, s, pdl);
+    return attn_rows_pick<FMT, 256>(p, rows, error, plan, s, pdl);
 }
 
 }  // namespace bqg
