@@ -196,26 +196,38 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b)
     if ((uint64_t)(a | b) >> 32) return a / b;
     return (int64_t)((uint32_t)a / (uint32_t)b);
 }
-// The units (weight(sequence) of them) of all sequences, and BQG_DEVERR_LENGTH in `bad` of some lanes; `mine`: of
-// sequence `lane`.  Called by whole warps, as attn_find is.
+// The units (weight(sequence) of them) of all sequences, and BQG_DEVERR_LENGTH in `bad` of some lanes; s and `mine`:
+// sequence `lane` and its units.  Called by whole warps, as attn_find is, which takes them on.
 template <typename W>
-__device__ __forceinline__ int64_t attn_total(const AttnParams &p, int lane, W weight, int &bad, int64_t &mine)
+__device__ __forceinline__ int64_t attn_total(const AttnParams &p, int lane, W weight, int &bad, AttnSeq &s, int64_t &mine)
 {
-    mine = lane < p.n_seq ? weight(attn_seq(p, lane, bad)) : 0;
+    mine = 0;
+    s = AttnSeq{};
+    if (lane < p.n_seq) {
+        s = attn_seq(p, lane, bad);
+        mine = weight(s);
+    }
     int64_t total = mine;
     for (int b = lane + 32; b < p.n_seq; b += 32) total += weight(attn_seq(p, b, bad));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     return total;
 }
-// The sequence that holds number u of the line of all sequences' units; `base`: the number of its first.
+// The sequence that holds number u (below the total) of the line of all sequences' units; `base`: the number of its first.
 template <typename W>
-__device__ __forceinline__ int attn_find(const AttnParams &p, int64_t u, int lane, W weight, int64_t mine, int64_t &base)
+__device__ __forceinline__ AttnSeq attn_find(const AttnParams &p, int64_t u, int lane, W weight, AttnSeq s, int64_t mine,
+                                             int64_t &base)
 {
     base = 0;
     for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
         int bad = 0;
-        if (b0) mine = b0 + lane < p.n_seq ? weight(attn_seq(p, b0 + lane, bad)) : 0;
+        if (b0) {
+            mine = 0;
+            if (b0 + lane < p.n_seq) {
+                s = attn_seq(p, b0 + lane, bad);
+                mine = weight(s);
+            }
+        }
         int64_t sum = mine;                                                   // inclusive over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -226,11 +238,17 @@ __device__ __forceinline__ int attn_find(const AttnParams &p, int64_t u, int lan
         if (past) {
             const int first = __ffs(past) - 1;
             base += __shfl_sync(0xffffffffu, sum - mine, first);
-            return b0 + first;
+            AttnSeq r;
+            r.b = b0 + first;
+            r.q0 = __shfl_sync(0xffffffffu, s.q0, first);
+            r.T = __shfl_sync(0xffffffffu, s.T, first);
+            r.ctx = __shfl_sync(0xffffffffu, s.ctx, first);
+            r.len = __shfl_sync(0xffffffffu, s.len, first);
+            return r;
         }
         base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    return p.n_seq;      // not reached for u below the total
+    return s;            // not reached
 }
 
 // A finished row: E = D / 32 values per lane, divided by their sum of weights, in bf16.
@@ -250,35 +268,69 @@ template <int ROWS> __device__ __forceinline__ int64_t attn_slot_row(int c, int 
 {
     return (int64_t)(2 * c + (c == c0)) * ROWS + row;
 }
-// Row `row` of the pieces of CTAs c0 .. c1, joined in their order by one warp: E values per lane and the sum.
+// Rows of the pieces of CTAs c0 .. c1, joined: warp w of the CTA's takes pieces
+// w, w + kAttnWarps, ... in order, the warps' results are then joined in order
+// (`merged` and `ml` as in the piece itself: the caller's code behind it is the
+// same).  Four pieces x four rows are in flight: what bounds this is their latency.
 template <int E, int ROWS>
-__device__ __forceinline__ void attn_join_row(const float *part, const float *part_ml, int c0, int c1, int row, int lane,
-                                              float (&v)[E], float &l)
+__device__ __forceinline__ void attn_join(const float *part, const float *part_ml, int c0, int c1, int rows, int warp, int lane,
+                                          float *merged, int pitch, float *ml)
 {
-    constexpr int D = 32 * E;
-    auto ml_of = [&](int c) { return __ldcg(reinterpret_cast<const float2 *>(part_ml + attn_slot_row<ROWS>(c, c0, row) * 2)); };
-    float mt = -__builtin_huge_valf();
-    for (int c = c0 + lane; c <= c1; c += 32) mt = fmaxf(mt, ml_of(c).x);
-    mt = warp_max(mt);
-    l = 0.f;
+    constexpr int D = 32 * E, R = (E <= 4) ? 4 : 2;
+    for (int r0 = 0; r0 < rows; r0 += R) {
+        float v[R][E], top[R], sum[R];
 #pragma unroll
-    for (int e = 0; e < E; e++) v[e] = 0.f;
-#pragma unroll 4
-    for (int c = c0; c <= c1; c++) {
-        const float2 q = ml_of(c);
-        const float w = (q.x == mt) ? 1.f : ex2(q.x - mt);
-        const float *src = part + attn_slot_row<ROWS>(c, c0, row) * D + lane * E;
-        l += w * q.y;
-        if constexpr (E == 2) {
-            const float2 a = __ldcg(reinterpret_cast<const float2 *>(src));
-            v[0] += w * a.x; v[1] += w * a.y;
-        } else {
+        for (int r = 0; r < R; r++) {
+            top[r] = -__builtin_huge_valf();
+            sum[r] = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                const float4 a = __ldcg(reinterpret_cast<const float4 *>(src + e));
-                v[e] += w * a.x; v[e + 1] += w * a.y; v[e + 2] += w * a.z; v[e + 3] += w * a.w;
-            }
+            for (int e = 0; e < E; e++) v[r][e] = 0.f;
         }
+        for (int c = c0 + warp; c <= c1; c += 4 * kAttnWarps) {
+            float2 q[4][R];
+            float a[4][R][E];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    const int piece = c + i * kAttnWarps;
+                    q[i][r] = make_float2(-__builtin_huge_valf(), 0.f);
+#pragma unroll
+                    for (int e = 0; e < E; e++) a[i][r][e] = 0.f;
+                    if (piece <= c1 && r0 + r < rows) {
+                        const int64_t at = attn_slot_row<ROWS>(piece, c0, r0 + r);
+                        q[i][r] = __ldcg(reinterpret_cast<const float2 *>(part_ml + at * 2));
+                        const float *src = part + at * D + lane * E;
+#pragma unroll
+                        for (int e = 0; e < E; e += 2) {
+                            const float2 f = __ldcg(reinterpret_cast<const float2 *>(src + e));
+                            a[i][r][e] = f.x; a[i][r][e + 1] = f.y;
+                        }
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    const float up = fmaxf(top[r], q[i][r].x);
+                    const float old = up == top[r] ? 1.f : ex2(top[r] - up), now = up == q[i][r].x ? 1.f : ex2(q[i][r].x - up);
+                    top[r] = up;
+                    sum[r] = sum[r] * old + q[i][r].y * now;
+#pragma unroll
+                    for (int e = 0; e < E; e++) v[r][e] = v[r][e] * old + a[i][r][e] * now;
+                }
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++)
+            if (r0 + r < rows) {
+                float *dst = merged + (warp * ROWS + r0 + r) * pitch + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; e++) dst[e] = v[r][e];
+                if (lane == 0) {
+                    ml[(warp * ROWS + r0 + r) * 2] = top[r];
+                    ml[(warp * ROWS + r0 + r) * 2 + 1] = sum[r];
+                }
+            }
     }
 }
 
@@ -299,40 +351,43 @@ template <int FMT, int D, int RT> struct AttnKernel {
         return (int64_t)p.cache.n_kv * row_tiles_of(p, s) * tiles_of(s);
     }
 
-    // The query fragments of rows row0 .. row0 + 7 (KS steps x 2 registers: row
-    // lane / 4), and the softmax scale of this lane's row.
-    static __device__ __forceinline__ void load_q(const AttnParams &p, const AttnSeq &s, int h, int row0, int lane,
-                                                  uint32_t (&qf)[G::KS][2], float &rs)
+    // The queries of rows row0 .. row0 + 7 as they lie (this lane: row lane / 4).  The order of the
+    // values within a block follows the codes' words: q8_0 lane t = lane % 4 values
+    // 8t .. 8t + 7; q4_0 values 4t .. and 16 + 4t ..
+    struct RawQ { uint32_t w[D / 8]; };
+    static __device__ __forceinline__ void fetch_q(const AttnParams &p, const AttnSeq &s, int h, int row0, int lane, RawQ &q)
     {
         const int t = lane & 3;
         const uint16_t *src = attn_q_row(p, s, h, row0 + (lane >> 2), D);
+#pragma unroll
+        for (int i = 0; i < D / 8; i++) q.w[i] = 0;
+        if (!src) return;
+#pragma unroll
+        for (int b = 0; b < G::NB; b++) {
+            if constexpr (BF) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) q.w[4 * b + k] = *reinterpret_cast<const uint32_t *>(src + 32 * b + 8 * k + 2 * t);
+            } else if constexpr (FMT == BQG_Q8_0) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(src + 32 * b + 8 * t);
+                q.w[4 * b] = a.x; q.w[4 * b + 1] = a.y; q.w[4 * b + 2] = a.z; q.w[4 * b + 3] = a.w;
+            } else {
+                const uint2 a = *reinterpret_cast<const uint2 *>(src + 32 * b + 4 * t);
+                const uint2 c = *reinterpret_cast<const uint2 *>(src + 32 * b + 16 + 4 * t);
+                q.w[4 * b] = a.x; q.w[4 * b + 1] = a.y; q.w[4 * b + 2] = c.x; q.w[4 * b + 3] = c.y;
+            }
+        }
+    }
+    // Their fragments (KS steps x 2 registers), and the softmax scale of this lane's row.
+    static __device__ __forceinline__ void make_q(const AttnParams &p, const RawQ &q, uint32_t (&qf)[G::KS][2], float &rs)
+    {
         rs = p.scale_log2;
         if constexpr (BF) {
 #pragma unroll
-            for (int ks = 0; ks < G::KS; ks++) {
-                qf[ks][0] = src ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 2 * t) : 0u;
-                qf[ks][1] = src ? *reinterpret_cast<const uint32_t *>(src + 16 * ks + 8 + 2 * t) : 0u;
-            }
+            for (int i = 0; i < D / 8; i++) qf[i >> 1][i & 1] = q.w[i];
         } else {
-            // the order of the values within a block follows the codes' words:
-            // q8_0 lane t values 8t .. 8t + 7; q4_0 values 4t .. and 16 + 4t ..,
-            // even ones first
-            uint32_t w[G::NB][4];
             float top = 0.f;
 #pragma unroll
-            for (int b = 0; b < G::NB; b++) {
-                if constexpr (FMT == BQG_Q8_0) {
-                    const uint4 a = src ? *reinterpret_cast<const uint4 *>(src + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
-                    w[b][0] = a.x; w[b][1] = a.y; w[b][2] = a.z; w[b][3] = a.w;
-                } else {
-                    const uint2 a = src ? *reinterpret_cast<const uint2 *>(src + 32 * b + 4 * t) : make_uint2(0, 0);
-                    const uint2 c = src ? *reinterpret_cast<const uint2 *>(src + 32 * b + 16 + 4 * t) : make_uint2(0, 0);
-                    w[b][0] = __byte_perm(a.x, a.y, 0x5410); w[b][1] = __byte_perm(a.x, a.y, 0x7632);
-                    w[b][2] = __byte_perm(c.x, c.y, 0x5410); w[b][3] = __byte_perm(c.x, c.y, 0x7632);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; j++) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[b][j])), fabsf(bf16_hi(w[b][j]))));
-            }
+            for (int i = 0; i < D / 8; i++) top = fmaxf(top, fmaxf(fabsf(bf16_lo(q.w[i])), fabsf(bf16_hi(q.w[i]))));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             float inv = 1.f;
@@ -342,10 +397,17 @@ template <int FMT, int D, int RT> struct AttnKernel {
                 rs = fmaxf(p.scale_log2 * (1.0f / inv), 1.17549435e-38f);       // 1 / inv: a power of two
             }
 #pragma unroll
-            for (int b = 0; b < G::NB; b++)
+            for (int b = 0; b < G::NB; b++) {
+                uint32_t w[4] = {q.w[4 * b], q.w[4 * b + 1], q.w[4 * b + 2], q.w[4 * b + 3]};
+                if constexpr (FMT == BQG_Q4_0) {                                // even values first
+                    const uint32_t a = w[0], c = w[2];
+                    w[0] = __byte_perm(a, w[1], 0x5410); w[1] = __byte_perm(a, w[1], 0x7632);
+                    w[2] = __byte_perm(c, w[3], 0x5410); w[3] = __byte_perm(c, w[3], 0x7632);
+                }
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    qf[2 * b + (j >> 1)][j & 1] = pack2<false>(bf16_lo(w[b][j]) * inv, bf16_hi(w[b][j]) * inv);
+                    qf[2 * b + (j >> 1)][j & 1] = pack2<false>(bf16_lo(w[j]) * inv, bf16_hi(w[j]) * inv);
+            }
         }
     }
 
@@ -605,21 +667,21 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
     int bad = 0;
     auto weight = [&](const AttnSeq &q) { return A::units(p, q); };
     int64_t mine;
-    const int64_t total = attn_total(p, lane, weight, bad, mine);
+    AttnSeq s;
+    const int64_t total = attn_total(p, lane, weight, bad, s, mine);
     if (bad && blockIdx.x == 0 && warp == 0) atomicOr(error, bad);
     const int64_t per = div_pos(total + gridDim.x - 1, gridDim.x);
     int64_t u = per * blockIdx.x;
     const int64_t u_end = min(u + per, total);
     if (u >= u_end) return;
     int64_t base;
-    int b = attn_find(p, u, lane, weight, mine, base);
-    AttnSeq s = attn_seq(p, b, bad);
+    s = attn_find(p, u, lane, weight, s, mine, base);
     int pages_bad = 0;
 
     while (u < u_end) {
         while (u - base >= A::units(p, s)) {                                  // next sequence with work
             base += A::units(p, s);
-            s = attn_seq(p, ++b, bad);
+            s = attn_seq(p, s.b + 1, bad);
         }
         const int64_t off = u - base;
         const int tiles = A::tiles_of(s), row_tiles = A::row_tiles_of(p, s);
@@ -632,14 +694,25 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
         // strips of this warp: tokens 64 (tile0 + j) + 16 warp ..
         const uint32_t ring = sb + warp * S * G::STAGE;
         const int32_t *table = p.table + (int64_t)s.b * p.max_pages;
-        auto page_of = [&](int j) {
-            const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
-            return (j < n && tok0 < s.len) ? table[tok0 >> p.cache.lp] : -1;
+        // pages of the warp's strips j0 .. j0 + 31, one per lane
+        auto pages_from = [&](int j0) {
+            const int tok0 = (tile0 + j0 + lane) * kUnit + warp * kStrip;
+            return (j0 + lane < n && tok0 < s.len) ? table[tok0 >> p.cache.lp] : -1;
         };
+        int pages = pages_from(0);
+        // queries (their loads are under way when the first strips are requested)
+        std::conditional_t<G::QREG, QRegs<RT, G::KS>, QShared<RT, G::KS>> qf;
+        typename A::RawQ raw[G::QREG ? RT : 1];
+        if constexpr (G::QREG) {
+#pragma unroll
+            for (int m = 0; m < RT; m++) A::fetch_q(p, s, h, row0 + 8 * m, lane, raw[m]);
+        } else if (warp < RT) {
+            A::fetch_q(p, s, h, row0 + 8 * warp, lane, raw[0]);
+        }
         unsigned valid = 0;                                                   // stages whose page is in the cache
-        int page = page_of(0);
         auto issue = [&](int j, int st) {
             const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
+            const int page = __shfl_sync(0xffffffffu, pages, j & 31);
             valid &= ~(1u << st);
             if (j < n && tok0 < s.len) {
                 const bool ok = page >= 0 && page < p.cache.n_pages;
@@ -648,30 +721,30 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                 A::issue(p, s, h, tok0, page, ok, ring + st * G::STAGE, lane);
             }
             cp_async_commit();
-            page = page_of(j + 1);
+            if ((j & 31) == 31) pages = pages_from(j + 1);
         };
 #pragma unroll 1
         for (int j = 0; j < S - 1; j++) issue(j, j);
 
-        // queries, and what their rows see
-        std::conditional_t<G::QREG, QRegs<RT, G::KS>, QShared<RT, G::KS>> qf;
+        // the queries' fragments, and what their rows see
         if constexpr (G::QREG) {
 #pragma unroll
             for (int m = 0; m < RT; m++) {
                 float r;
-                A::load_q(p, s, h, row0 + 8 * m, lane, qf.f[m], r);
+                A::make_q(p, raw[m], qf.f[m], r);
                 if (warp == 0 && t == 0) row_scale[8 * m + g] = r;
             }
         } else {
+            static_assert(G::QREG || RT <= kAttnWarps, "a row tile per warp");
             qf.addr = sb + G::OFF_Q + lane * 8;
-            for (int m = warp; m < RT; m += kAttnWarps) {
+            if (warp < RT) {
                 uint32_t f[G::KS][2];
                 float r;
-                A::load_q(p, s, h, row0 + 8 * m, lane, f, r);
+                A::make_q(p, raw[0], f, r);
 #pragma unroll
                 for (int ks = 0; ks < G::KS; ks++)
-                    *reinterpret_cast<uint2 *>(smem + G::OFF_Q + (m * G::KS + ks) * 256 + lane * 8) = make_uint2(f[ks][0], f[ks][1]);
-                if (t == 0) row_scale[8 * m + g] = r;
+                    *reinterpret_cast<uint2 *>(smem + G::OFF_Q + (warp * G::KS + ks) * 256 + lane * 8) = make_uint2(f[ks][0], f[ks][1]);
+                if (t == 0) row_scale[8 * warp + g] = r;
             }
         }
         if (tid < G::ROWS) row_sees[tid] = attn_sees(p, s, row0 + tid);
@@ -816,32 +889,36 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
             const int i = (row0 + row) / p.group, hh = row0 + row - i * p.group;
             return p.out + ((int64_t)(s.q0 + i) * p.n_q + h * p.group + hh) * D + lane * E;
         };
-        for (int row = warp; row < rows; row += kAttnWarps) {
-            float mt = NEG;
+        // rows of `merged`, the warps' results joined: into the output, or the workspace
+        auto finish = [&](bool last) {
+            for (int row = warp; row < rows; row += kAttnWarps) {
+                float mt = NEG;
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; w++) mt = fmaxf(mt, ml[(w * G::ROWS + row) * 2]);
-            float v[E], l = 0.f;
+                for (int w = 0; w < kAttnWarps; w++) mt = fmaxf(mt, ml[(w * G::ROWS + row) * 2]);
+                float v[E], l = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; e++) v[e] = 0.f;
+                for (int e = 0; e < E; e++) v[e] = 0.f;
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; w++) {
-                const float mw = ml[(w * G::ROWS + row) * 2];
-                const float c = (mw == mt) ? 1.f : ex2(mw - mt);
-                l += c * ml[(w * G::ROWS + row) * 2 + 1];
-                const float *src = merged + (w * G::ROWS + row) * (D + G::PAD) + lane * E;
+                for (int w = 0; w < kAttnWarps; w++) {
+                    const float mw = ml[(w * G::ROWS + row) * 2];
+                    const float c = (mw == mt) ? 1.f : ex2(mw - mt);
+                    l += c * ml[(w * G::ROWS + row) * 2 + 1];
+                    const float *src = merged + (w * G::ROWS + row) * (D + G::PAD) + lane * E;
 #pragma unroll
-                for (int e = 0; e < E; e++) v[e] += c * src[e];
+                    for (int e = 0; e < E; e++) v[e] += c * src[e];
+                }
+                if (last) {
+                    attn_store_row<E>(out_row(row), v, l);
+                } else {
+                    const int64_t at = attn_slot_row<G::ROWS>(cta, c0, row);
+                    float *dst = p.part + at * D + lane * E;
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(dst + e) = make_float2(v[e], v[e + 1]);
+                    if (lane == 0) *reinterpret_cast<float2 *>(part_ml + at * 2) = make_float2(mt, l);
+                }
             }
-            if (c0 == c1) {
-                attn_store_row<E>(out_row(row), v, l);
-            } else {
-                const int64_t at = attn_slot_row<G::ROWS>(cta, c0, row);
-                float *dst = p.part + at * D + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; e++) dst[e] = v[e];
-                if (lane == 0) *reinterpret_cast<float2 *>(part_ml + at * 2) = make_float2(mt, l);
-            }
-        }
+        };
+        finish(c0 == c1);
         if (c0 != c1) {
             int *flag = reinterpret_cast<int *>(smem + G::OFF_FLAG);
             __threadfence();
@@ -851,11 +928,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
             if (*flag) {                                                      // every piece is in the workspace
                 __threadfence();
                 if (tid == 0) p.counters[c0] = 0;
-                for (int row = warp; row < rows; row += kAttnWarps) {
-                    float v[E], l;
-                    attn_join_row<E, G::ROWS>(p.part, part_ml, c0, c1, row, lane, v, l);
-                    attn_store_row<E>(out_row(row), v, l);
-                }
+                attn_join<E, G::ROWS>(p.part, part_ml, c0, c1, rows, warp, lane, merged, D + G::PAD, ml);
+                __syncthreads();
+                finish(true);
             }
         }
         __syncthreads();                                                      // before the ring is filled again

@@ -124,17 +124,13 @@ template <int NQ> struct TcWork {
     {
         auto weight = [&](const AttnSeq &q) { return cost(p, q); };
         int64_t mine;
-        const int64_t total = attn_total(p, lane, weight, bad, mine);
+        const int64_t total = attn_total(p, lane, weight, bad, s, mine);
         // at least NQ, so that every range between a set's first and last holds the beginning of a tile
         per = max(div_pos(total + gridDim.x - 1, gridDim.x), (int64_t)NQ);
         cur = per * blockIdx.x;
         end = min(cur + per, total);
         base = 0;
-        s = AttnSeq{};
-        if (cur < end) {
-            int ignored = 0;
-            s = attn_seq(p, attn_find(p, cur, lane, weight, mine, base), ignored);
-        }
+        if (cur < end) s = attn_find(p, cur, lane, weight, s, mine, base);
     }
     __device__ __forceinline__ bool next(const AttnParams &p, TcPiece &o)
     {
