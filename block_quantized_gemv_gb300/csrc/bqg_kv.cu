@@ -1,15 +1,23 @@
 // bqg_kv.cu -- per-head norm and rotation of queries and keys, the cache's
 // encoder and decoder.
 //
-// norm_rope_kernel: one warp per head row of one token (queries, keys and
-// values of a token are consecutive rows).  Lane l holds the E = D / 32
-// values from E l on, so a row is one load of 4 to 32 bytes per lane, its
-// sum of squares one warp reduction, and a 32-value block sits in 32 / E
-// neighbouring lanes.  A pair (i, i + R/2) is R/2/E lanes apart (R is a
-// multiple of 16, E divides 8): one exchange; an adjacent pair is in one lane.
-// Everything is fp32 with the roundings of include/bqgemv.h; the sum of
-// squares is kept as error-free fp32 pairs (SumSq), so r matches the fp64
-// definition up to a rare tie.
+// norm_rope_kernel: a head row of one token is held by a warp, lane l the
+// E = D / 32 values from E l on, so a row is one load of 4 to 32 bytes per lane,
+// and a 32-value block sits in 32 / E neighbouring lanes.  A pair
+// (i, i + R/2) is R/2/E lanes apart (R is a multiple of 16, E divides 8): one
+// exchange; an adjacent pair is in one lane.  Everything is fp32 with the
+// roundings of include/bqgemv.h; the sum of squares is kept as error-free fp32
+// pairs, so r matches the fp64 definition up to a rare tie.
+//
+// It is a stream (bytes: rows in, queries out, cached rows out), but one row at a
+// time per warp left it at 1.0 TB/s, bound by the instructions of the exact sum and
+// their latency.  So a warp takes four rows of a token and one kind (queries, keys or
+// values) together: their loads are in flight at once, and the next four's behind them; the
+// arithmetic works on two rows per instruction (packed fp32, each half with
+// its own rounding); the four sums are reduced together, each step halving the rows
+// a lane still holds, and the reciprocal roots are taken once, each
+// in the lanes that ended up with its row; the rotation's cos and sin are loaded once
+// for the four rows.
 #include <algorithm>
 
 #include "bqg_kv.cuh"
@@ -31,31 +39,7 @@ cudaError_t kv_take_error(int *out)
 
 namespace {
 
-constexpr int kWarps = 8;      // warps per CTA
-
-template <int E> __device__ __forceinline__ void load_row(const void *x, int x_f32, int64_t first, float (&v)[E])
-{
-    if (x_f32) {
-        const float *p = reinterpret_cast<const float *>(x) + first;
-        if constexpr (E == 2) {
-            const float2 a = *reinterpret_cast<const float2 *>(p);
-            v[0] = a.x; v[1] = a.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; i += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(p + i);
-                v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
-            }
-        }
-    } else {
-        const uint16_t *p = reinterpret_cast<const uint16_t *>(x) + first;
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(p + i);
-            v[i] = bf16_lo(w); v[i + 1] = bf16_hi(w);
-        }
-    }
-}
+constexpr int kWarps = 4;      // warps per CTA
 
 __device__ __forceinline__ uint32_t pack_bf16x2_rn(float lo, float hi)
 {
@@ -76,23 +60,114 @@ template <int E> __device__ __forceinline__ void store_bf16(uint16_t *p, const f
     }
 }
 
-// r = fp32(1 / sqrt(sum x^2 / D + eps)) of the row held by the warp.
-template <int E> __device__ __forceinline__ float row_rms_recip(const float (&x)[E], float eps)
+// Two fp32 values, one per row, in one register pair: each operation rounds each of them once.
+struct F2 { uint64_t v; };
+__device__ __forceinline__ F2 f2(float a, float b) { F2 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b)); return r; }
+__device__ __forceinline__ float f2a(F2 x) { return __uint_as_float((uint32_t)x.v); }
+__device__ __forceinline__ float f2b(F2 x) { return __uint_as_float((uint32_t)(x.v >> 32)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { F2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { F2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { F2 r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v)); return r; }
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return fma2(b, f2(-1.f, -1.f), a); }
+// a + b where b may be a product: a packed product and the sum behind it would be
+// fused into one rounding (measured: ptxas contracts mul.rn.f32x2 and add.rn.f32x2), so the
+// sum is a 1 + b with a one that the compiler does not know.
+__device__ __forceinline__ F2 add2_apart(F2 a, F2 b, F2 one) { return fma2(a, one, b); }
+__device__ __forceinline__ void two_sum2(F2 a, F2 b, F2 &s, F2 &e, F2 one)
 {
-    SumSq acc;
+    s = add2_apart(a, b, one);
+    const F2 bb = sub2(s, a);
+    e = add2(sub2(a, sub2(s, bb)), sub2(b, bb));
+}
+
+// r = fp32(1 / sqrt(sum x^2 / D + eps)) of one row of the warp in fp64, for
+// rows that leave the range of the pair arithmetic.
+template <int E> __device__ __noinline__ float row_rms_recip_wide(const float (&x)[E], float eps)
+{
+    double t = 0.0;
 #pragma unroll
-    for (int i = 0; i < E; i++) acc.add(x[i]);
+    for (int i = 0; i < E; i++) t = fma((double)x[i], (double)x[i], t);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        acc.merge(__shfl_xor_sync(0xffffffffu, acc.hi, o), __shfl_xor_sync(0xffffffffu, acc.lo, o));
-    const bool wide = __any_sync(0xffffffffu, acc.wide != 0.0);
-    // every lane holds the same pair up to the order of the sums: take lane 0's
-    const float hi = __shfl_sync(0xffffffffu, acc.hi, 0), lo = __shfl_sync(0xffffffffu, acc.lo, 0);
-    if (!wide && hi >= 0x1p-60f && hi <= 0x1p100f) return rms_recip_pair(hi, lo, (float)(E * 32), eps);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc.wide += __shfl_xor_sync(0xffffffffu, acc.wide, o);
-    const double t = ((double)hi + (double)lo) + __shfl_sync(0xffffffffu, acc.wide, 0);
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return (float)(1.0 / sqrt(t / (double)(E * 32) + (double)eps));
+}
+
+// r of the warp's four rows (x[pair][value]: rows 2 pair and 2 pair + 1), as pairs.
+template <int E> __device__ __forceinline__ void rms_recip4(const F2 (&x)[2][E], bool f32, float eps, int lane, F2 one, F2 (&r)[2])
+{
+    F2 hi[2], lo[2];
+#pragma unroll
+    for (int p = 0; p < 2; p++) {
+        hi[p] = mul2(x[p][0], x[p][0]);
+        lo[p] = f32 ? fma2(x[p][0], x[p][0], mul2(hi[p], f2(-1.f, -1.f))) : f2(0.f, 0.f);   // the square's rounding (none: bf16)
+#pragma unroll
+        for (int i = 1; i < E; i++) {
+            const F2 q = mul2(x[p][i], x[p][i]);
+            F2 e;
+            if (f32) lo[p] = add2(lo[p], fma2(x[p][i], x[p][i], mul2(q, f2(-1.f, -1.f))));
+            two_sum2(hi[p], q, hi[p], e, one);
+            lo[p] = add2(lo[p], e);
+        }
+    }
+    // rows 0, 1 stay in lanes 0..15, rows 2, 3 in 16..31
+    const bool up = lane & 16;
+    auto xchg = [&](F2 v, int o) { F2 r; r.v = __shfl_xor_sync(0xffffffffu, (unsigned long long)v.v, o); return r; };
+    F2 h = up ? hi[1] : hi[0], l = up ? lo[1] : lo[0], e;
+    const F2 oh = xchg(up ? hi[0] : hi[1], 16), ol = xchg(up ? lo[0] : lo[1], 16);
+    two_sum2(h, oh, h, e, one);
+    l = add2(l, add2(ol, e));
+    // the even row of the two in lanes with bit 3 clear, the odd one in the others
+    const bool odd = lane & 8;
+    SumSq t;
+    t.hi = odd ? f2b(h) : f2a(h);
+    t.lo = odd ? f2b(l) : f2a(l);
+    t.merge(__shfl_xor_sync(0xffffffffu, odd ? f2a(h) : f2b(h), 8), __shfl_xor_sync(0xffffffffu, odd ? f2a(l) : f2b(l), 8));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) t.merge(__shfl_xor_sync(0xffffffffu, t.hi, o), __shfl_xor_sync(0xffffffffu, t.lo, o));
+    // (the eight lanes of a row differ at most in the order of their sums: the lowest one's counts)
+    float mine = 0.f;
+    const bool pair_ok = t.hi >= 0x1p-60f && t.hi <= 0x1p100f;
+    if (pair_ok) mine = rms_recip_pair(t.hi, t.lo, (float)(E * 32), eps);
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = __shfl_sync(0xffffffffu, mine, 8 * j);
+    const unsigned bad = __ballot_sync(0xffffffffu, !pair_ok);
+    if (bad & 0x01010101u) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if ((bad >> (8 * j)) & 1) {
+                float row[E];
+#pragma unroll
+                for (int i = 0; i < E; i++) row[i] = (j & 1) ? f2b(x[j >> 1][i]) : f2a(x[j >> 1][i]);
+                v[j] = row_rms_recip_wide<E>(row, eps);
+            }
+    }
+    r[0] = f2(v[0], v[1]);
+    r[1] = f2(v[2], v[3]);
+}
+
+// Codes of E values under the stored scale d: round(x / d), halves away from zero, x / d rounded once to fp32 as the format
+// has it.  x times the approximate 1 / d is within 2^-15 of that (|x / d| is at most about 128), so unless it lies within
+// 2^-12 of a half both round alike; the rest divide.
+template <int E> __device__ __forceinline__ void block_codes(const float (&y)[E], float d, int (&q)[E])
+{
+    float rd;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(d));
+    bool near = !(d > -65536.f && d < 65536.f && d != 0.f);
+#pragma unroll
+    for (int i = 0; i < E; i++) {
+        const float t = __fmul_rn(y[i], rd);
+        q[i] = __float2int_rn(t);
+        const float f = fabsf(t - (float)q[i]);
+        near |= !(f < 0.5f - 0x1p-12f) || !(fabsf(t) < 1024.f);
+    }
+    if (near) {
+#pragma unroll
+        for (int i = 0; i < E; i++) {
+            const float t = d == 0.f ? 0.f : roundf(__fdiv_rn(y[i], d));
+            q[i] = t != t ? -1024 : (int)fminf(fmaxf(t, -1024.f), 1024.f);      // NaN: the lowest code, as the encoders have it
+        }
+    }
 }
 
 // The warp's row (E values per lane) into cache row `row`.
@@ -110,12 +185,14 @@ __device__ __forceinline__ void encode_row(const float (&y)[D / 32], int lane, u
 #pragma unroll
         for (int o = LB / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const __half dh = __float2half_rn(__fdiv_rn(amax, 127.0f));
-        const float d = __half2float(dh);
+        int q[E];
+        block_codes<E>(y, __half2float(dh), q);
+        uint32_t w[(E + 3) / 4] = {};
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            const uint32_t a = (uint8_t)(int8_t)q8_code(y[i], d), b = (uint8_t)(int8_t)q8_code(y[i + 1], d);
-            *reinterpret_cast<uint16_t *>(dst + lane * E + i) = (uint16_t)(a | (b << 8));
-        }
+        for (int i = 0; i < E; i++) w[i / 4] |= ((uint32_t)max(min(q[i], 127), -127) & 0xffu) << (8 * (i % 4));
+        if constexpr (E == 2) *reinterpret_cast<uint16_t *>(dst + 2 * lane) = (uint16_t)w[0];
+        else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst + 4 * lane) = w[0];
+        else *reinterpret_cast<uint2 *>(dst + 8 * lane) = make_uint2(w[0], w[1]);
         if (lane % LB == 0) scales[row * KvRow<FMT, D>::NB + lane / LB] = __half_as_ushort(dh);
     } else {
         // signed value of largest magnitude, the first one on ties
@@ -126,107 +203,211 @@ __device__ __forceinline__ void encode_row(const float (&y)[D / 32], int lane, u
         int bl = lane;
 #pragma unroll
         for (int o = LB / 2; o > 0; o >>= 1) {
-            const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-            const float oa = __shfl_xor_sync(0xffffffffu, ba, o);
+            const float ov = __shfl_xor_sync(0xffffffffu, bv, o), oa = fabsf(ov);
             const int ol = __shfl_xor_sync(0xffffffffu, bl, o);
             if (oa > ba || (oa == ba && ol < bl)) { bv = ov; ba = oa; bl = ol; }
         }
         const __half dh = __float2half_rn(__fdiv_rn(bv, -8.0f));
-        const float d = __half2float(dh);
-        uint32_t q[E];
+        int q[E];
+        block_codes<E>(y, __half2float(dh), q);
+        uint32_t w[(E + 3) / 4] = {};
 #pragma unroll
-        for (int i = 0; i < E; i++) {
-            q[i] = 8;
-            if (d != 0.0f) q[i] = (uint32_t)fminf(fmaxf(roundf(__fdiv_rn(y[i], d)) + 8.0f, 0.0f), 15.0f);
-            q[i] |= __shfl_xor_sync(0xffffffffu, q[i], LB / 2) << 4;      // lower half: the value 16 further on
-        }
+        for (int i = 0; i < E; i++) w[i / 4] |= (uint32_t)max(min(q[i] + 8, 15), 0) << (8 * (i % 4));
+#pragma unroll
+        for (int i = 0; i < (E + 3) / 4; i++) w[i] |= __shfl_xor_sync(0xffffffffu, w[i], LB / 2) << 4;   // the values 16 further on
         if (lane % LB < LB / 2) {
-            const int at = (lane / LB) * 16 + (lane % LB) * E;
-#pragma unroll
-            for (int i = 0; i < E; i += 2)
-                *reinterpret_cast<uint16_t *>(dst + at + i) = (uint16_t)((q[i] & 0xffu) | ((q[i + 1] & 0xffu) << 8));
+            uint8_t *at = dst + (lane / LB) * 16 + (lane % LB) * E;
+            if constexpr (E == 2) *reinterpret_cast<uint16_t *>(at) = (uint16_t)w[0];
+            else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(at) = w[0];
+            else *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
         }
         if (lane % LB == 0) scales[row * KvRow<FMT, D>::NB + lane / LB] = __half_as_ushort(dh);
     }
 }
 
-template <int FMT, int D> __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeParams p)
+// Four rows of one token and kind, as loaded.
+template <int E> struct RawRows { uint32_t w[4][E]; };       // fp32: E words a row; bf16: the first E / 2
+
+template <int FMT, int D, bool F32> __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeParams p)
 {
     constexpr int E = D / 32;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int rows = p.n_q + (p.k ? p.n_kv : 0) + (p.v ? p.n_kv : 0);       // rows of one token
-    for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < p.T * rows;
-         i += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = i / rows;
-        int h = (int)(i - t * rows);
-        const int what = h < p.n_q ? 0 : (p.k && h < p.n_q + p.n_kv) ? 1 : 2;       // query, key, value
-        h -= what == 0 ? 0 : what == 1 ? p.n_q : rows - p.n_kv;
-        int64_t slot = -1;
-        if (what && p.slots) {
-            slot = p.slots[t];
-            if (slot >= 0 && !kv_slot_ok(p.cache, slot)) {
-                if (lane == 0) atomicOr(&g_kv_error, BQG_DEVERR_SLOT);
-                slot = -1;
-            }
-            if (slot < 0) continue;
-        }
-        float y[E];
-        const void *x = what == 0 ? p.q : what == 1 ? p.k : p.v;
-        const int64_t stride = what == 0 ? p.q_stride : what == 1 ? p.k_stride : p.v_stride;
-        load_row<E>(x, p.x_f32, t * stride + (int64_t)h * D + lane * E, y);
-        if (what < 2 && p.norm) {
-            const float r = row_rms_recip<E>(y, p.eps);
-            const float *g = what ? p.gamma_k : p.gamma_q;
+    // groups of four rows of a token: queries, then keys, then values
+    const int gq = (p.n_q + 3) / 4, gk = p.k ? (p.n_kv + 3) / 4 : 0, gv = p.v ? (p.n_kv + 3) / 4 : 0, groups = gq + gk + gv;
+    struct Item { int64_t t; int what, h, rows; };                            // what: 0 queries, 1 keys, 2 values
+    auto item_of = [&](int64_t i) {
+        Item m;
+        m.t = (i >> 32) ? i / groups : (int64_t)((uint32_t)i / (uint32_t)groups);
+        const int g = (int)(i - m.t * groups);
+        m.what = g < gq ? 0 : g < gq + gk ? 1 : 2;
+        m.h = 4 * (g - (m.what == 0 ? 0 : m.what == 1 ? gq : gq + gk));
+        m.rows = min(4, (m.what ? p.n_kv : p.n_q) - m.h);
+        return m;
+    };
+    auto load = [&](const Item &m, RawRows<E> &x) {
+        const void *src = m.what == 0 ? p.q : m.what == 1 ? p.k : p.v;
+        const int64_t first = m.t * (m.what == 0 ? p.q_stride : m.what == 1 ? p.k_stride : p.v_stride) + (int64_t)m.h * D + lane * E;
 #pragma unroll
-            for (int j = 0; j < E; j++) {
-                y[j] = __fmul_rn(y[j], r);
-                if (g) y[j] = __fmul_rn(y[j], g[lane * E + j]);
+        for (int j = 0; j < 4; j++) {
+#pragma unroll
+            for (int i = 0; i < E; i++) x.w[j][i] = F32 ? 0x3f800000u : 0x3f803f80u;    // no row: ones, whose root is quick
+            if (j < m.rows) {
+                if constexpr (F32) {
+                    const uint32_t *s = reinterpret_cast<const uint32_t *>(src) + first + j * D;
+                    if constexpr (E == 2) {
+                        const uint2 a = *reinterpret_cast<const uint2 *>(s);
+                        x.w[j][0] = a.x; x.w[j][1] = a.y;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < E; i += 4) {
+                            const uint4 a = *reinterpret_cast<const uint4 *>(s + i);
+                            x.w[j][i] = a.x; x.w[j][i + 1] = a.y; x.w[j][i + 2] = a.z; x.w[j][i + 3] = a.w;
+                        }
+                    }
+                } else {
+                    const uint16_t *s = reinterpret_cast<const uint16_t *>(src) + first + j * D;
+                    if constexpr (E == 2) {
+                        x.w[j][0] = *reinterpret_cast<const uint32_t *>(s);
+                    } else if constexpr (E == 4) {
+                        const uint2 a = *reinterpret_cast<const uint2 *>(s);
+                        x.w[j][0] = a.x; x.w[j][1] = a.y;
+                    } else {
+                        const uint4 a = *reinterpret_cast<const uint4 *>(s);
+                        x.w[j][0] = a.x; x.w[j][1] = a.y; x.w[j][2] = a.z; x.w[j][3] = a.w;
+                    }
+                }
             }
         }
+    };
+    const float one_f = __int_as_float(0x3f800000 | (int)(p.T < 0));          // 1: the host lets no T < 0 through
+    const F2 one = f2(one_f, one_f);
+    const int64_t items = p.T * groups, step = (int64_t)gridDim.x * kWarps;
+    int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (i >= items) return;
+    Item m = item_of(i);
+    RawRows<E> raw;
+    load(m, raw);
+    for (;;) {
+        // the position and slot of this token, the rows of the next item
+        int64_t slot = -1;
+        if (m.what && p.slots) slot = p.slots[m.t];
+        int64_t pos = 0;
+        const bool turn = m.what < 2 && p.rot;
+        if (turn) pos = p.pos[m.t];
+        F2 y[2][E];
+#pragma unroll
+        for (int a = 0; a < 2; a++)
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                if constexpr (F32) {
+                    y[a][e] = f2(__uint_as_float(raw.w[2 * a][e]), __uint_as_float(raw.w[2 * a + 1][e]));
+                } else {
+                    const uint32_t u = raw.w[2 * a][e / 2], w = raw.w[2 * a + 1][e / 2];
+                    y[a][e] = (e & 1) ? f2(bf16_hi(u), bf16_hi(w)) : f2(bf16_lo(u), bf16_lo(w));
+                }
+            }
+        const Item now = m;
+        const int64_t next = i + step;
+        if (next < items) {
+            m = item_of(next);
+            load(m, raw);
+        }
+
+        // cos and sin of this lane's values (sin negated where the value is the first of its pair)
+        float cs[E], sn[E];
         bool lost = false;
-        if (what < 2 && p.rot) {
-            const int64_t pos = p.pos[t];
+        const int half = p.rot / 2;
+        const bool in = turn && lane * E < p.rot;
+        int other = lane;
+        if (turn) {
             lost = pos < 0 || pos >= p.n_pos;
             if (lost && lane == 0) atomicOr(&g_kv_error, BQG_DEVERR_POSITION);
             const float *row = p.table + (lost ? 0 : pos) * p.rot;
-            const int half = p.rot / 2;
-            if (p.interleaved) {
-                if (lane * E < p.rot) {
+            if (in) {
+                if (p.interleaved) {
 #pragma unroll
-                    for (int j = 0; j < E; j += 2) {
-                        const int pair = (lane * E + j) / 2;
-                        const float c = row[pair], s = row[half + pair], a = y[j], b = y[j + 1];
-                        y[j] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-                        y[j + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+                    for (int e = 0; e < E; e += 2) {
+                        const int pair = (lane * E + e) / 2;
+                        cs[e] = cs[e + 1] = row[pair];
+                        sn[e + 1] = row[half + pair];
+                        sn[e] = -sn[e + 1];
                     }
-                }
-            } else {
-                const bool low = lane * E < half, in = lane * E < p.rot;
-                const int other = !in ? lane : low ? lane + half / E : lane - half / E;
+                } else {
+                    const bool low = lane * E < half;
+                    const int first = lane * E - (low ? 0 : half);
+                    other = low ? lane + half / E : lane - half / E;
 #pragma unroll
-                for (int j = 0; j < E; j++) {
-                    const float o = __shfl_sync(0xffffffffu, y[j], other);
-                    if (in) {
-                        const int pair = lane * E + j - (low ? 0 : half);
-                        const float c = row[pair], s = row[half + pair];
-                        y[j] = low ? __fsub_rn(__fmul_rn(y[j], c), __fmul_rn(o, s))
-                                   : __fadd_rn(__fmul_rn(o, s), __fmul_rn(y[j], c));
+                    for (int e = 0; e < E; e += 2) {
+                        const float2 c = *reinterpret_cast<const float2 *>(row + first + e);
+                        const float2 s = *reinterpret_cast<const float2 *>(row + half + first + e);
+                        cs[e] = c.x; cs[e + 1] = c.y;
+                        sn[e] = low ? -s.x : s.x; sn[e + 1] = low ? -s.y : s.y;
                     }
                 }
             }
         }
-        if (what && p.slots) {
-            if (!lost)
-                encode_row<FMT, D>(y, lane, what == 1 ? p.cache.k : p.cache.v,
-                                   what == 1 ? p.cache.k_scale : p.cache.v_scale, kv_row(p.cache, slot, h));
-        } else {
+        if (now.what < 2 && p.norm) {
+            F2 r[2];
+            rms_recip4<E>(y, F32, p.eps, lane, one, r);
+            const float *g = now.what ? p.gamma_k : p.gamma_q;
+            float gain[E];
+            if (g) {
 #pragma unroll
-            for (int j = 0; j < E; j++) y[j] = lost ? 0.f : y[j];
-            uint16_t *out = what ? p.k_out : p.q_out;
-            store_bf16<E>(out + (t * (what ? p.n_kv : p.n_q) + h) * D + lane * E, y);
+                for (int e = 0; e < E; e += 2) {
+                    const float2 a = *reinterpret_cast<const float2 *>(g + lane * E + e);
+                    gain[e] = a.x; gain[e + 1] = a.y;
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < 2; a++)
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    y[a][e] = mul2(y[a][e], r[a]);
+                    if (g) y[a][e] = mul2(y[a][e], f2(gain[e], gain[e]));
+                }
         }
+        if (turn) {
+#pragma unroll
+            for (int a = 0; a < 2; a++) {
+                F2 o[E];                                                      // the pairs' other values
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    if (p.interleaved) o[e] = y[a][e ^ 1];
+                    else o[e].v = __shfl_sync(0xffffffffu, (unsigned long long)y[a][e].v, other);
+                }
+                if (in) {
+                    // a c - b s = a c + b (-s) and a s + b c: each product rounded, then their sum
+#pragma unroll
+                    for (int e = 0; e < E; e++)
+                        y[a][e] = add2_apart(mul2(y[a][e], f2(cs[e], cs[e])), mul2(o[e], f2(sn[e], sn[e])), one);
+                }
+            }
+        }
+        if (slot >= 0 && !kv_slot_ok(p.cache, slot)) {
+            if (lane == 0) atomicOr(&g_kv_error, BQG_DEVERR_SLOT);
+            slot = -1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            if (j >= now.rows) break;
+            float row[E];
+#pragma unroll
+            for (int e = 0; e < E; e++) row[e] = (j & 1) ? f2b(y[j >> 1][e]) : f2a(y[j >> 1][e]);
+            if (now.what && p.slots) {
+                if (!lost && slot >= 0)
+                    encode_row<FMT, D>(row, lane, now.what == 1 ? p.cache.k : p.cache.v,
+                                       now.what == 1 ? p.cache.k_scale : p.cache.v_scale, kv_row(p.cache, slot, now.h + j));
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; e++) row[e] = lost ? 0.f : row[e];
+                uint16_t *out = now.what ? p.k_out : p.q_out;
+                store_bf16<E>(out + (now.t * (now.what ? p.n_kv : p.n_q) + now.h + j) * D + lane * E, row);
+            }
+        }
+        if (next >= items) break;
+        i = next;
     }
 }
 
@@ -317,9 +498,9 @@ template <typename P> cudaError_t launch(void (*kern)(P), const P &p, int64_t ct
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int FMT> void (*norm_rope_fn(int D))(NormRopeParams)
+template <int FMT, bool F32> void (*norm_rope_fn(int D))(NormRopeParams)
 {
-    return D == 64 ? norm_rope_kernel<FMT, 64> : D == 128 ? norm_rope_kernel<FMT, 128> : norm_rope_kernel<FMT, 256>;
+    return D == 64 ? norm_rope_kernel<FMT, 64, F32> : D == 128 ? norm_rope_kernel<FMT, 128, F32> : norm_rope_kernel<FMT, 256, F32>;
 }
 template <int FMT, bool F32> void (*kv_read_fn(int D))(KvReadParams)
 {
@@ -330,10 +511,12 @@ template <int FMT, bool F32> void (*kv_read_fn(int D))(KvReadParams)
 
 cudaError_t launch_norm_rope(const NormRopeParams &p, int fmt, int D, int sms, cudaStream_t s, bool pdl)
 {
-    const int64_t rows = p.T * (p.n_q + (p.k ? p.n_kv : 0) + (p.v ? p.n_kv : 0));
-    if (rows == 0) return cudaSuccess;
-    auto fn = fmt == BQG_Q8_0 ? norm_rope_fn<BQG_Q8_0>(D) : fmt == BQG_Q4_0 ? norm_rope_fn<BQG_Q4_0>(D) : norm_rope_fn<BQG_BF16>(D);
-    return launch(fn, p, std::min<int64_t>((rows + kWarps - 1) / kWarps, (int64_t)sms * 8), 32 * kWarps, s, pdl);
+    const int64_t groups = (p.n_q + 3) / 4 + ((p.k ? 1 : 0) + (p.v ? 1 : 0)) * ((p.n_kv + 3) / 4);
+    const int64_t items = p.T * groups;
+    if (items == 0) return cudaSuccess;
+    auto fn = p.x_f32 ? (fmt == BQG_Q8_0 ? norm_rope_fn<BQG_Q8_0, true>(D) : fmt == BQG_Q4_0 ? norm_rope_fn<BQG_Q4_0, true>(D) : norm_rope_fn<BQG_BF16, true>(D))
+                      : (fmt == BQG_Q8_0 ? norm_rope_fn<BQG_Q8_0, false>(D) : fmt == BQG_Q4_0 ? norm_rope_fn<BQG_Q4_0, false>(D) : norm_rope_fn<BQG_BF16, false>(D));
+    return launch(fn, p, std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)sms * 5), 32 * kWarps, s, pdl);
 }
 
 cudaError_t launch_kv_read(const KvReadParams &p, int fmt, int D, int out_f32, int sms, cudaStream_t s, bool pdl)
