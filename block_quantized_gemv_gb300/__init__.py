@@ -482,8 +482,9 @@ class KVCache:
         self._ptr = ctypes.addressof(self._struct)
         self.device_index = k.device.index
 
-    def _handle(self) -> int:
-        check_device(self.device_index, _current_device(), "cache")
+    def _handle(self, cur: int) -> int:
+        if self.device_index != cur:
+            check_device(self.device_index, cur, "cache")
         return self._ptr
 
 
@@ -502,55 +503,88 @@ def kv_cache(fmt: int, n_pages: int, n_kv: int, page_size: int, head_dim: int, d
 _X_DTYPE = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _tokens(t: torch.Tensor, name: str, heads: int | None = None, dim: int | None = None, T: int | None = None,
-            dtype=None):
-    """(pointer, token stride) of [tokens, heads, head_dim] rows whose tokens
-    may lie apart (a part of a fused projection's rows)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    check_device(t.device.index, _current_device(), name)
-    return t.data_ptr(), _token_stride(t, name, heads, dim, T, dtype)
+# These calls take up to nine tensors and their kernels a few microseconds, so the
+# checks that hold are made inline; what does not pass goes through the full check,
+# which raises with the reason.
+def _ptr(t, cur: int, name: str, dtype, nbytes: int):
+    """Pointer of a contiguous tensor on the current device `cur` with at least nbytes."""
+    if type(t) is torch.Tensor and t.get_device() == cur and t.dtype is dtype and t.is_contiguous() and t.nbytes >= nbytes:
+        return t.data_ptr()
+    return _dev(t, name, dtype, nbytes)
 
 
-def _token_stride(t, name, heads, dim, T, dtype):
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    n, h, d = t.shape
-    if (heads is not None and h != heads) or (dim is not None and d != dim) or (T is not None and n != T):
-        raise ValueError(f"{name} is {list(t.shape)}, needs [{'T' if T is None else T}, "
-                         f"{'heads' if heads is None else heads}, {'head_dim' if dim is None else dim}]")
-    s = t.stride()
-    if t.numel() and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
-        raise ValueError(f"each token's heads of {name} must be contiguous")
-    return s[0] if n > 1 else h * d
-
-
-def _rotation(pos, table, T):
-    if table is None:
-        if pos is not None:
-            raise ValueError("pos without table")
-        return None, None, 0, 0
-    if table.dim() != 2:
-        raise ValueError("table must be [n_pos, rot_dim]")
-    return (_vector(pos, "pos", torch.int32, T), _dev(table, "table", torch.float32), table.shape[0], table.shape[1])
-
-
-def _vector(t, name, dtype, n):
+def _vector(t, cur, name, dtype, n):
+    """_ptr of exactly n values."""
+    if type(t) is torch.Tensor and t.get_device() == cur and t.dtype is dtype and t.is_contiguous() and t.numel() == n:
+        return t.data_ptr()
     p = _dev(t, name, dtype)
     if t.numel() != n:
         raise ValueError(f"{name} holds {t.numel()} values, needs {n}")
     return p
 
 
-def _gains(gamma_q, gamma_k, eps, dim):
+def _tokens(t, cur, name, shape, dtype):
+    """(pointer, token stride) of [tokens, heads, head_dim] rows whose tokens
+    may lie apart (a part of a fused projection's rows)."""
+    if type(t) is torch.Tensor and t.get_device() == cur and t.dtype is dtype and t.shape == shape:
+        s = t.stride()
+        if s[2] == 1 and s[1] == shape[2]:
+            return t.data_ptr(), s[0] if shape[0] > 1 else shape[1] * shape[2]
+    return _tokens_checked(t, name, shape, dtype)
+
+
+def _tokens_checked(t, name, shape, dtype):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    check_device(t.device.index, _current_device(), name)
+    return t.data_ptr(), _token_stride(t, name, shape, dtype)
+
+
+def _token_stride(t, name, shape, dtype):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {list(t.shape)}, needs {list(shape)}")
+    n, h, d = shape
+    s = t.stride()
+    if t.numel() and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+        raise ValueError(f"each token's heads of {name} must be contiguous")
+    return s[0] if n > 1 else h * d
+
+
+def _shape3(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [tokens, heads, head_dim] tensor")
+    return t.shape
+
+
+def _rotation(pos, table, T, cur):
+    if table is None:
+        if pos is not None:
+            raise ValueError("pos without table")
+        return None, None, 0, 0
+    if table.dim() != 2:
+        raise ValueError("table must be [n_pos, rot_dim]")
+    n_pos, rot = table.shape
+    return _vector(pos, cur, "pos", torch.int32, T), _ptr(table, cur, "table", torch.float32, 0), n_pos, rot
+
+
+def _gains(gamma_q, gamma_k, eps, dim, cur):
     if eps is None:
         if gamma_q is not None or gamma_k is not None:
             raise ValueError("gamma without eps (no norm)")
         return 0, None, None, 0.0
-    return (1, None if gamma_q is None else _vector(gamma_q, "gamma_q", torch.float32, dim),
-            None if gamma_k is None else _vector(gamma_k, "gamma_k", torch.float32, dim), float(eps))
+    return (1, None if gamma_q is None else _vector(gamma_q, cur, "gamma_q", torch.float32, dim),
+            None if gamma_k is None else _vector(gamma_k, cur, "gamma_k", torch.float32, dim), eps)
+
+
+def _x_dtype(t, name):
+    dt = _X_DTYPE.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be bf16 or fp32")
+    return dt
 
 
 def qk_norm_rope(q, k, pos=None, table=None, gamma_q=None, gamma_k=None, eps=None, interleaved=False, out=None,
@@ -559,21 +593,20 @@ def qk_norm_rope(q, k, pos=None, table=None, gamma_q=None, gamma_k=None, eps=Non
     queries [T, n_q, head_dim] and keys [T, n_kv, head_dim], bf16 or fp32,
     tokens possibly apart.  table: fp32 [n_pos, rot_dim], cos of the pair
     angles then their sines; pos: int32 [T].  Returns (q, k) in bf16."""
-    T, n_q, dim = q.shape
-    n_kv = k.shape[1]
-    dt = _X_DTYPE.get(q.dtype)
-    if dt is None:
-        raise TypeError("q must be bf16 or fp32")
-    qp, qs = _tokens(q, "q")
-    kp, ks = _tokens(k, "k", dim=dim, T=T, dtype=q.dtype)
-    norm, gq, gk, eps = _gains(gamma_q, gamma_k, eps, dim)
-    pp, tp, n_pos, rot = _rotation(pos, table, T)
+    cur = _current_device()
+    shape = T, n_q, dim = _shape3(q, "q")
+    n_kv = _shape3(k, "k")[1]
+    dt = _x_dtype(q, "q")
+    qp, qs = _tokens(q, cur, "q", shape, q.dtype)
+    kp, ks = _tokens(k, cur, "k", (T, n_kv, dim), q.dtype)
+    norm, gq, gk, eps = _gains(gamma_q, gamma_k, eps, dim, cur)
+    pp, tp, n_pos, rot = _rotation(pos, table, T, cur)
     if out is None:
         out = (torch.empty((T, n_q, dim), dtype=torch.bfloat16, device=q.device),
                torch.empty((T, n_kv, dim), dtype=torch.bfloat16, device=q.device))
     _check(load().bqg_qk_norm_rope(qp, kp, dt, qs, ks, T, n_q, n_kv, dim, norm, gq, gk, eps, pp, tp, n_pos, rot,
-                                   1 if interleaved else 0, _dev(out[0], "out[0]", torch.bfloat16, T * n_q * dim * 2),
-                                   _dev(out[1], "out[1]", torch.bfloat16, T * n_kv * dim * 2), _stream(stream)),
+                                   1 if interleaved else 0, _ptr(out[0], cur, "out[0]", torch.bfloat16, T * n_q * dim * 2),
+                                   _ptr(out[1], cur, "out[1]", torch.bfloat16, T * n_kv * dim * 2), _stream(stream)),
            "bqg_qk_norm_rope")
     return out
 
@@ -583,56 +616,64 @@ def qk_norm_rope_kv_write(q, k, v, slots, cache: KVCache, pos=None, table=None, 
     """qk_norm_rope with the keys, and the values v, going into `cache` at
     int64 `slots` (page * page_size + place; negative: not stored) in the same
     launch.  Returns the queries in bf16."""
-    T, n_q, dim = q.shape
-    dt = _X_DTYPE.get(q.dtype)
-    if dt is None:
-        raise TypeError("q must be bf16 or fp32")
-    qp, qs = _tokens(q, "q", dim=cache.head_dim)
-    kp, ks = _tokens(k, "k", cache.n_kv, dim, T, q.dtype)
-    vp, vs = _tokens(v, "v", cache.n_kv, dim, T, q.dtype)
-    norm, gq, gk, eps = _gains(gamma_q, gamma_k, eps, dim)
-    pp, tp, n_pos, rot = _rotation(pos, table, T)
+    cur = _current_device()
+    T, n_q, _ = _shape3(q, "q")
+    dim, dtype = cache.head_dim, q.dtype
+    dt = _x_dtype(q, "q")
+    qp, qs = _tokens(q, cur, "q", (T, n_q, dim), dtype)
+    kv = (T, cache.n_kv, dim)
+    kp, ks = _tokens(k, cur, "k", kv, dtype)
+    vp, vs = _tokens(v, cur, "v", kv, dtype)
+    norm, gq, gk, eps = _gains(gamma_q, gamma_k, eps, dim, cur)
+    pp, tp, n_pos, rot = _rotation(pos, table, T, cur)
     if out is None:
         out = torch.empty((T, n_q, dim), dtype=torch.bfloat16, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, cur, "out", torch.bfloat16, T * n_q * dim * 2)
     _check(load().bqg_qk_norm_rope_kv_write(qp, kp, vp, dt, qs, ks, vs, T, n_q, norm, gq, gk, eps, pp, tp, n_pos, rot,
-                                            1 if interleaved else 0,
-                                            _dev(out, "out", torch.bfloat16, T * n_q * dim * 2),
-                                            _vector(slots, "slots", torch.int64, T), cache._handle(), _stream(stream)),
+                                            1 if interleaved else 0, op,
+                                            _vector(slots, cur, "slots", torch.int64, T), cache._handle(cur),
+                                            _stream(stream)),
            "bqg_qk_norm_rope_kv_write")
     return out
 
 
 def kv_write(k, v, slots, cache: KVCache, stream=None) -> None:
     """Keys and values [T, n_kv, head_dim] (bf16 or fp32) into `cache` at `slots`."""
-    dt = _X_DTYPE.get(k.dtype)
-    if dt is None:
-        raise TypeError("k must be bf16 or fp32")
-    T = k.shape[0]
-    kp, ks = _tokens(k, "k", cache.n_kv, cache.head_dim)
-    vp, vs = _tokens(v, "v", cache.n_kv, cache.head_dim, T, k.dtype)
-    _check(load().bqg_kv_write(kp, vp, dt, ks, vs, T, _vector(slots, "slots", torch.int64, T), cache._handle(),
+    cur = _current_device()
+    T = _shape3(k, "k")[0]
+    dt = _x_dtype(k, "k")
+    kv = (T, cache.n_kv, cache.head_dim)
+    kp, ks = _tokens(k, cur, "k", kv, k.dtype)
+    vp, vs = _tokens(v, cur, "v", kv, k.dtype)
+    _check(load().bqg_kv_write(kp, vp, dt, ks, vs, T, _vector(slots, cur, "slots", torch.int64, T), cache._handle(cur),
                                _stream(stream)), "bqg_kv_write")
 
 
 def kv_read(cache: KVCache, slots, dtype=torch.bfloat16, out=None, stream=None):
     """The cache's keys and values at `slots`, each [T, n_kv, head_dim] bf16
     or fp32; a negative slot reads as zeros."""
+    cur = _current_device()
     T = slots.numel()
     dt = _X_DTYPE.get(dtype)
     if dt is None:
         raise TypeError("dtype must be bf16 or fp32")
     if out is None:
-        out = tuple(torch.empty((T, cache.n_kv, cache.head_dim), dtype=dtype, device=slots.device) for _ in range(2))
-    n = T * cache.n_kv * cache.head_dim * dtype.itemsize
-    _check(load().bqg_kv_read(cache._handle(), _vector(slots, "slots", torch.int64, T), T, dt,
-                              _dev(out[0], "out[0]", dtype, n), _dev(out[1], "out[1]", dtype, n), _stream(stream)),
-           "bqg_kv_read")
+        shape, device = (T, cache.n_kv, cache.head_dim), slots.device
+        out = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
+        kp, vp = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        n = T * cache.n_kv * cache.head_dim * dtype.itemsize
+        kp, vp = _ptr(out[0], cur, "out[0]", dtype, n), _ptr(out[1], cur, "out[1]", dtype, n)
+    _check(load().bqg_kv_read(cache._handle(cur), _vector(slots, cur, "slots", torch.int64, T), T, dt, kp, vp,
+                              _stream(stream)), "bqg_kv_read")
     return out
 
 
 def tree_attention_workspace(cache: KVCache, n_q: int, n_seq: int, max_q: int) -> torch.Tensor:
     """A zero-filled workspace for tree_attention calls of these sizes."""
-    n = int(load().bqg_tree_attention_workspace_size(cache._handle(), n_q, n_seq, max_q))
+    n = int(load().bqg_tree_attention_workspace_size(cache._handle(_current_device()), n_q, n_seq, max_q))
     if n == 0:
         raise ValueError("not a tree_attention call on this device")
     return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
@@ -648,20 +689,29 @@ def tree_attention(q, cache: KVCache, block_table, ctx_len, q_start, max_q: int,
     ctx_len int32 [n_seq]; mask int64 [n_tokens], bit j set where new token j
     of the sequence is seen (a tree of drafted tokens), or None for causal;
     scale defaults to head_dim ** -0.5.  Returns bf16 [n_tokens, n_q, head_dim]."""
-    n, n_q, dim = q.shape
-    qp, qs = _tokens(q, "q", dim=cache.head_dim, dtype=torch.bfloat16)
+    cur = _current_device()
+    n, n_q, _ = _shape3(q, "q")
+    dim = cache.head_dim
+    qp, qs = _tokens(q, cur, "q", (n, n_q, dim), torch.bfloat16)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [n_seq, max_pages]")
     n_seq, max_pages = block_table.shape
     if out is None:
         out = torch.empty((n, n_q, dim), dtype=torch.bfloat16, device=q.device)
-    wsp, wsb = _ws(ws)
-    _check(load().bqg_tree_attention(qp, qs, cache._handle(), _dev(block_table, "block_table", torch.int32), max_pages,
-                                     _vector(ctx_len, "ctx_len", torch.int32, n_seq),
-                                     _vector(q_start, "q_start", torch.int32, n_seq + 1), n_seq, n, max_q, n_q,
-                                     None if mask is None else _vector(mask, "mask", torch.int64, n),
-                                     dim ** -0.5 if scale is None else float(scale),
-                                     _dev(out, "out", torch.bfloat16, n * n_q * dim * 2), wsp, wsb, _stream(stream)),
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, cur, "out", torch.bfloat16, n * n_q * dim * 2)
+    if ws is None:
+        wsp, wsb = None, 0
+    else:
+        wsb = ws.nbytes
+        wsp = _ptr(ws, cur, "ws", ws.dtype, wsb)
+    _check(load().bqg_tree_attention(qp, qs, cache._handle(cur), _ptr(block_table, cur, "block_table", torch.int32, 0),
+                                     max_pages, _vector(ctx_len, cur, "ctx_len", torch.int32, n_seq),
+                                     _vector(q_start, cur, "q_start", torch.int32, n_seq + 1), n_seq, n, max_q, n_q,
+                                     None if mask is None else _vector(mask, cur, "mask", torch.int64, n),
+                                     dim ** -0.5 if scale is None else scale,
+                                     op, wsp, wsb, _stream(stream)),
            "bqg_tree_attention")
     return out
 

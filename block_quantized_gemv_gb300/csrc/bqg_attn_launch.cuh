@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cstdlib>
 #include <mutex>
 
@@ -172,10 +173,20 @@ template <int FMT, int D> cudaError_t attn_rows_pick(const AttnParams &p, int ro
 template <int FMT>
 cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
-    void *word = nullptr;
-    if (!plan)
-        if (cudaError_t e = cudaGetSymbolAddress(&word, error_word)) return e;
-    int *error = static_cast<int *>(word);
+    int *error = nullptr;
+    if (!plan) {
+        // the error word's address: looked up once per device
+        static std::atomic<void *> known[64];
+        int dev = 0;
+        if (cudaError_t e = cudaGetDevice(&dev)) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        void *word = known[dev].load(std::memory_order_relaxed);
+        if (!word) {
+            if (cudaError_t e = cudaGetSymbolAddress(&word, error_word)) return e;
+            known[dev].store(word, std::memory_order_relaxed);
+        }
+        error = static_cast<int *>(word);
+    }
     const bool tc = rows >= attn_tc_rows();
     if (D == 64) return tc ? attn_tc_call<FMT, 64>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 64>(p, rows, error, plan, s, pdl);
     if (D == 128) return tc ? attn_tc_call<FMT, 128>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 128>(p, rows, error, plan, s, pdl);

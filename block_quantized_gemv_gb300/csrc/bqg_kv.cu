@@ -146,82 +146,167 @@ template <int E> __device__ __forceinline__ void rms_recip4(const F2 (&x)[2][E],
     r[1] = f2(v[2], v[3]);
 }
 
-// Codes of E values under the stored scale d: round(x / d), halves away from zero, x / d rounded once to fp32 as the format
-// has it.  x times the approximate 1 / d is within 2^-15 of that (|x / d| is at most about 128), so unless it lies within
-// 2^-12 of a half both round alike; the rest divide.
-template <int E> __device__ __forceinline__ void block_codes(const float (&y)[E], float d, int (&q)[E])
+// Larger of two magnitudes; a NaN stays.
+__device__ __forceinline__ float max_abs_nan(float a, float b)
 {
-    float rd;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(d));
-    bool near = !(d > -65536.f && d < 65536.f && d != 0.f);
-#pragma unroll
-    for (int i = 0; i < E; i++) {
-        const float t = __fmul_rn(y[i], rd);
-        q[i] = __float2int_rn(t);
-        const float f = fabsf(t - (float)q[i]);
-        near |= !(f < 0.5f - 0x1p-12f) || !(fabsf(t) < 1024.f);
-    }
-    if (near) {
-#pragma unroll
-        for (int i = 0; i < E; i++) {
-            const float t = d == 0.f ? 0.f : roundf(__fdiv_rn(y[i], d));
-            q[i] = t != t ? -1024 : (int)fminf(fmaxf(t, -1024.f), 1024.f);      // NaN: the lowest code, as the encoders have it
-        }
-    }
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
 }
 
-// The warp's row (E values per lane) into cache row `row`.
+// One row's codes as the format defines them, for what the quick path below leaves: lane's E values, d the
+// scale of their block.
+template <int FMT, int E> __device__ __noinline__ uint64_t codes_exact(const float (&y)[E], float d)
+{
+    uint64_t w = 0;
+#pragma unroll
+    for (int i = 0; i < E; i++) {
+        uint32_t c;
+        if constexpr (FMT == BQG_Q8_0) c = (uint32_t)q8_code(y[i], d) & 0xffu;
+        else c = d != 0.0f ? (uint32_t)fminf(fmaxf(roundf(__fdiv_rn(y[i], d)) + 8.0f, 0.0f), 15.0f) : 8u;
+        w |= (uint64_t)c << (8 * i);
+    }
+    return w;
+}
+
+// The warp's four rows (y[pair][value]: rows 2 pair and 2 pair + 1) into cache rows row, row + pitch, ...
+//
+// The four rows' block maxima are reduced together: each of the first two exchanges
+// halves the rows a lane holds, so a row's scale is worked out in LB / 4 lanes of
+// its block and handed to the others.  A code is round(x / d), halves away
+// from zero, x / d rounded once to fp32.  The quick way is x times the approximate 1 / d (within 2^-15 of
+// that, as |x / d| is at most about 128) rounded by adding and taking off 1.5 x 2^23, two values per
+// instruction; where that lies within 2^-12 of a half, or the scale or a value is not an ordinary number, the row's
+// codes are divided out.
 template <int FMT, int D>
-__device__ __forceinline__ void encode_row(const float (&y)[D / 32], int lane, uint8_t *codes, uint16_t *scales, int64_t row)
+__device__ __forceinline__ void encode_rows(const F2 (&y)[2][D / 32], int rows, int lane, uint8_t *codes, uint16_t *scales,
+                                            int64_t row, int64_t pitch)
 {
     constexpr int E = D / 32, LB = 32 / E;            // lanes per block
-    uint8_t *dst = codes + row * KvRow<FMT, D>::BYTES;
+    constexpr int RB = KvRow<FMT, D>::BYTES, NB = KvRow<FMT, D>::NB;
+    auto value = [&](int j, int e) { return (j & 1) ? f2b(y[j >> 1][e]) : f2a(y[j >> 1][e]); };
     if constexpr (FMT == BQG_BF16) {
-        store_bf16<E>(reinterpret_cast<uint16_t *>(dst) + lane * E, y);
-    } else if constexpr (FMT == BQG_Q8_0) {
-        float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; i++) amax = fmaxf(amax, fabsf(y[i]));
+        for (int j = 0; j < 4; j++) {
+            float one[E];
 #pragma unroll
-        for (int o = LB / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const __half dh = __float2half_rn(__fdiv_rn(amax, 127.0f));
-        int q[E];
-        block_codes<E>(y, __half2float(dh), q);
-        uint32_t w[(E + 3) / 4] = {};
-#pragma unroll
-        for (int i = 0; i < E; i++) w[i / 4] |= ((uint32_t)max(min(q[i], 127), -127) & 0xffu) << (8 * (i % 4));
-        if constexpr (E == 2) *reinterpret_cast<uint16_t *>(dst + 2 * lane) = (uint16_t)w[0];
-        else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst + 4 * lane) = w[0];
-        else *reinterpret_cast<uint2 *>(dst + 8 * lane) = make_uint2(w[0], w[1]);
-        if (lane % LB == 0) scales[row * KvRow<FMT, D>::NB + lane / LB] = __half_as_ushort(dh);
+            for (int e = 0; e < E; e++) one[e] = value(j, e);
+            if (j < rows) store_bf16<E>(reinterpret_cast<uint16_t *>(codes + (row + j * pitch) * RB) + lane * E, one);
+        }
     } else {
-        // signed value of largest magnitude, the first one on ties
-        float bv = y[0], ba = fabsf(y[0]);
+        constexpr bool Q8 = (FMT == BQG_Q8_0);
+        constexpr int S = Q8 ? 1 : 2;                 // largest magnitude; or largest value and largest negated value
+        float a[4][S];
 #pragma unroll
-        for (int i = 1; i < E; i++)
-            if (fabsf(y[i]) > ba) { bv = y[i]; ba = fabsf(y[i]); }
-        int bl = lane;
+        for (int j = 0; j < 4; j++) {
+            a[j][0] = Q8 ? fabsf(value(j, 0)) : value(j, 0);
+            if constexpr (!Q8) a[j][1] = -value(j, 0);
 #pragma unroll
-        for (int o = LB / 2; o > 0; o >>= 1) {
-            const float ov = __shfl_xor_sync(0xffffffffu, bv, o), oa = fabsf(ov);
-            const int ol = __shfl_xor_sync(0xffffffffu, bl, o);
-            if (oa > ba || (oa == ba && ol < bl)) { bv = ov; ba = oa; bl = ol; }
+            for (int e = 1; e < E; e++) {
+                a[j][0] = fmaxf(a[j][0], Q8 ? fabsf(value(j, e)) : value(j, e));
+                if constexpr (!Q8) a[j][1] = fmaxf(a[j][1], -value(j, e));
+            }
         }
-        const __half dh = __float2half_rn(__fdiv_rn(bv, -8.0f));
-        int q[E];
-        block_codes<E>(y, __half2float(dh), q);
-        uint32_t w[(E + 3) / 4] = {};
+        const bool up = lane & (LB / 2), up2 = lane & (LB / 4);
+        float k[S];
 #pragma unroll
-        for (int i = 0; i < E; i++) w[i / 4] |= (uint32_t)max(min(q[i] + 8, 15), 0) << (8 * (i % 4));
+        for (int i = 0; i < S; i++) {
+            const float k0 = fmaxf(up ? a[2][i] : a[0][i], __shfl_xor_sync(0xffffffffu, up ? a[0][i] : a[2][i], LB / 2));
+            const float k1 = fmaxf(up ? a[3][i] : a[1][i], __shfl_xor_sync(0xffffffffu, up ? a[1][i] : a[3][i], LB / 2));
+            k[i] = fmaxf(up2 ? k1 : k0, __shfl_xor_sync(0xffffffffu, up2 ? k0 : k1, LB / 4));
 #pragma unroll
-        for (int i = 0; i < (E + 3) / 4; i++) w[i] |= __shfl_xor_sync(0xffffffffu, w[i], LB / 2) << 4;   // the values 16 further on
-        if (lane % LB < LB / 2) {
-            uint8_t *at = dst + (lane / LB) * 16 + (lane % LB) * E;
-            if constexpr (E == 2) *reinterpret_cast<uint16_t *>(at) = (uint16_t)w[0];
-            else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(at) = w[0];
-            else *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+            for (int o = LB / 8; o > 0; o >>= 1) k[i] = fmaxf(k[i], __shfl_xor_sync(0xffffffffu, k[i], o));
         }
-        if (lane % LB == 0) scales[row * KvRow<FMT, D>::NB + lane / LB] = __half_as_ushort(dh);
+        // this lane's row: 2 up + up2
+        __half dh;
+        bool odd;                                     // to be divided out
+        if constexpr (Q8) {
+            dh = __float2half_rn(__fdiv_rn(k[0], 127.0f));
+        } else {
+            dh = __float2half_rn(__fdiv_rn(k[0] > k[1] ? k[0] : -k[1], -8.0f));
+        }
+        float d = __half2float(dh), rd;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rd) : "f"(d));
+        if constexpr (Q8) odd = !(k[0] * rd < 127.45f);
+        else odd = k[0] == k[1] || !(fmaxf(k[0], k[1]) * fabsf(rd) < 8.05f);      // both signs of the largest: the first decides
+        float near = odd ? 1.f : 0.f;
+        uint32_t w[4][(E + 3) / 4];
+        const float magic = Q8 ? 12582912.f : 12582920.f;                         // 1.5 x 2^23; q4_0: codes are round(x / d) + 8
+#pragma unroll
+        for (int p = 0; p < 2; p++) {
+            const int from = (lane & ~(LB - 1)) + p * (LB / 2);
+            const F2 rd2 = f2(__shfl_sync(0xffffffffu, rd, from), __shfl_sync(0xffffffffu, rd, from + LB / 4));
+            F2 m[E];
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                F2 t = mul2(y[p][e], rd2);
+                if constexpr (!Q8) t = f2(fminf(f2a(t), 7.0f), fminf(f2b(t), 7.0f));  // 15 is the last code (NaN: seen below)
+                m[e] = add2(t, f2(magic, magic));
+                const F2 f = sub2(mul2(y[p][e], rd2), sub2(m[e], f2(magic, magic)));
+                const bool ca = !Q8 && f2a(t) == 7.0f, cb = !Q8 && f2b(t) == 7.0f;    // clipped: its own remainder says nothing
+                near = max_abs_nan(near, ca && f2a(f) > 0.f ? 0.f : f2a(f));
+                near = max_abs_nan(near, cb && f2b(f) > 0.f ? 0.f : f2b(f));
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int e = 0; e < E; e += 4) {
+                    auto bits = [&](int i) { return __float_as_uint(h ? f2b(m[i]) : f2a(m[i])); };
+                    uint32_t u = __byte_perm(bits(e), bits(e + 1), 0x0040);
+                    if constexpr (E >= 4) u = __byte_perm(u, __byte_perm(bits(e + 2), bits(e + 3), 0x0040), 0x5410);
+                    w[2 * p + h][e / 4] = u;
+                }
+        }
+        if (__any_sync(0xffffffffu, !(near < 0.5f - 0x1p-12f))) {
+            if constexpr (!Q8) {
+                // the first value of largest magnitude of each row, in order
+                float first = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    float bv = value(j, 0), ba = fabsf(bv);
+#pragma unroll
+                    for (int e = 1; e < E; e++)
+                        if (fabsf(value(j, e)) > ba) { bv = value(j, e); ba = fabsf(bv); }
+                    int bl = lane;
+#pragma unroll
+                    for (int o = LB / 2; o > 0; o >>= 1) {
+                        const float ov = __shfl_xor_sync(0xffffffffu, bv, o), oa = fabsf(ov);
+                        const int ol = __shfl_xor_sync(0xffffffffu, bl, o);
+                        if (oa > ba || (oa == ba && ol < bl)) { bv = ov; ba = oa; bl = ol; }
+                    }
+                    if (j == 2 * up + up2) first = bv;
+                }
+                dh = __float2half_rn(__fdiv_rn(first, -8.0f));
+                d = __half2float(dh);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float dj = __shfl_sync(0xffffffffu, d, (lane & ~(LB - 1)) + (j >> 1) * (LB / 2) + (j & 1) * (LB / 4));
+                float one[E];
+#pragma unroll
+                for (int e = 0; e < E; e++) one[e] = value(j, e);
+                const uint64_t c = codes_exact<FMT, E>(one, dj);
+                w[j][0] = (uint32_t)c;
+                if constexpr (E == 8) w[j][1] = (uint32_t)(c >> 32);
+            }
+        }
+        // scales: by the first lane of those that worked a row's out
+        const int mine = 2 * up + up2;
+        if ((lane & (LB / 4 - 1)) == 0 && mine < rows) scales[(row + mine * pitch) * NB + lane / LB] = __half_as_ushort(dh);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            uint8_t *dst = codes + (row + j * pitch) * RB;
+            if constexpr (!Q8) {
+#pragma unroll
+                for (int i = 0; i < (E + 3) / 4; i++) w[j][i] |= __shfl_xor_sync(0xffffffffu, w[j][i], LB / 2) << 4;   // the values 16 further on
+            }
+            if (j < rows && (Q8 || !up)) {
+                uint8_t *at = Q8 ? dst + lane * E : dst + (lane / LB) * 16 + (lane % LB) * E;
+                if constexpr (E == 2) *reinterpret_cast<uint16_t *>(at) = (uint16_t)w[j][0];
+                else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(at) = w[j][0];
+                else *reinterpret_cast<uint2 *>(at) = make_uint2(w[j][0], w[j][1]);
+            }
+        }
     }
 }
 
@@ -389,21 +474,20 @@ template <int FMT, int D, bool F32> __global__ void __launch_bounds__(32 * kWarp
             if (lane == 0) atomicOr(&g_kv_error, BQG_DEVERR_SLOT);
             slot = -1;
         }
+        if (now.what && p.slots) {
+            if (!lost && slot >= 0)
+                encode_rows<FMT, D>(y, now.rows, lane, now.what == 1 ? p.cache.k : p.cache.v,
+                                    now.what == 1 ? p.cache.k_scale : p.cache.v_scale, kv_row(p.cache, slot, now.h),
+                                    (int64_t)1 << p.cache.lp);
+        } else {
+            uint16_t *out = now.what ? p.k_out : p.q_out;
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            if (j >= now.rows) break;
-            float row[E];
+            for (int j = 0; j < 4; j++) {
+                float row[E];
 #pragma unroll
-            for (int e = 0; e < E; e++) row[e] = (j & 1) ? f2b(y[j >> 1][e]) : f2a(y[j >> 1][e]);
-            if (now.what && p.slots) {
-                if (!lost && slot >= 0)
-                    encode_row<FMT, D>(row, lane, now.what == 1 ? p.cache.k : p.cache.v,
-                                       now.what == 1 ? p.cache.k_scale : p.cache.v_scale, kv_row(p.cache, slot, now.h + j));
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; e++) row[e] = lost ? 0.f : row[e];
-                uint16_t *out = now.what ? p.k_out : p.q_out;
-                store_bf16<E>(out + (now.t * (now.what ? p.n_kv : p.n_q) + now.h + j) * D + lane * E, row);
+                for (int e = 0; e < E; e++) row[e] = lost ? 0.f : (j & 1) ? f2b(y[j >> 1][e]) : f2a(y[j >> 1][e]);
+                if (j < now.rows)
+                    store_bf16<E>(out + (now.t * (now.what ? p.n_kv : p.n_q) + now.h + j) * D + lane * E, row);
             }
         }
         if (next >= items) break;

@@ -140,8 +140,7 @@ def stub(monkeypatch):
 
     monkeypatch.setattr(bqg, "load", lambda path=None: Lib())
     monkeypatch.setattr(bqg, "_dev", dev)
-    monkeypatch.setattr(bqg, "_tokens", lambda t, name, heads=None, dim=None, T=None, dtype=None:
-                        (16, bqg._token_stride(t, name, heads, dim, T, dtype)))
+    monkeypatch.setattr(bqg, "_tokens_checked", lambda t, name, shape, dtype: (16, bqg._token_stride(t, name, shape, dtype)))
     monkeypatch.setattr(bqg, "_stream", lambda stream=None: 0)
     monkeypatch.setattr(bqg, "check_device", lambda *a: None)
     monkeypatch.setattr(bqg, "_current_device", lambda: 0)
