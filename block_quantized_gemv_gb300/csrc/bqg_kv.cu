@@ -174,10 +174,12 @@ template <int FMT, int E> __device__ __noinline__ uint64_t codes_exact(const flo
 // The four rows' block maxima are reduced together: each of the first two exchanges
 // halves the rows a lane holds, so a row's scale is worked out in LB / 4 lanes of
 // its block and handed to the others.  A code is round(x / d), halves away
-// from zero, x / d rounded once to fp32.  The quick way is x times the approximate 1 / d (within 2^-15 of
-// that, as |x / d| is at most about 128) rounded by adding and taking off 1.5 x 2^23, two values per
-// instruction; where that lies within 2^-12 of a half, or the scale or a value is not an ordinary number, the row's
-// codes are divided out.
+// from zero, x / d rounded once to fp32.  The quick way is x times the approximate 1 / d, rounded by adding
+// and taking off 1.5 x 2^23, two values per instruction.  It is off by at most 2^-22.4 of |x / d| (1 / d:
+// 2^-23, the product and the quotient 2^-24 each), which is under 2^-14 for q8_0 (127.5) and under 2^-18 for
+// q4_0 (8.05); where a value lies within that of a half, or it or the scale is not an ordinary number, the
+// rows' codes are divided out (one group of four rows in 16, and in 256; with 2^-12 for both it was one
+// in four, and 8192 tokens of 8 heads took 39 us instead of 27).
 template <int FMT, int D>
 __device__ __forceinline__ void encode_rows(const F2 (&y)[2][D / 32], int rows, int lane, uint8_t *codes, uint16_t *scales,
                                             int64_t row, int64_t pitch)
@@ -257,7 +259,7 @@ __device__ __forceinline__ void encode_rows(const F2 (&y)[2][D / 32], int rows, 
                     w[2 * p + h][e / 4] = u;
                 }
         }
-        if (__any_sync(0xffffffffu, !(near < 0.5f - 0x1p-12f))) {
+        if (__any_sync(0xffffffffu, !(near < 0.5f - (Q8 ? 0x1p-14f : 0x1p-18f)))) {
             if constexpr (!Q8) {
                 // the first value of largest magnitude of each row, in order
                 float first = 0.f;
@@ -310,10 +312,13 @@ __device__ __forceinline__ void encode_rows(const F2 (&y)[2][D / 32], int rows, 
     }
 }
 
+// CTAs per SM: registers allow so many, and a grid of that many has no second wave.
+template <int D> constexpr int resident() { return D == 256 ? 3 : D == 128 ? 6 : 8; }
+
 // Four rows of one token and kind, as loaded.
 template <int E> struct RawRows { uint32_t w[4][E]; };       // fp32: E words a row; bf16: the first E / 2
 
-template <int FMT, int D, bool F32> __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeParams p)
+template <int FMT, int D, bool F32> __global__ void __launch_bounds__(32 * kWarps, resident<D>()) norm_rope_kernel(const NormRopeParams p)
 {
     constexpr int E = D / 32;
     pdl_wait();
@@ -600,7 +605,8 @@ cudaError_t launch_norm_rope(const NormRopeParams &p, int fmt, int D, int sms, c
     if (items == 0) return cudaSuccess;
     auto fn = p.x_f32 ? (fmt == BQG_Q8_0 ? norm_rope_fn<BQG_Q8_0, true>(D) : fmt == BQG_Q4_0 ? norm_rope_fn<BQG_Q4_0, true>(D) : norm_rope_fn<BQG_BF16, true>(D))
                       : (fmt == BQG_Q8_0 ? norm_rope_fn<BQG_Q8_0, false>(D) : fmt == BQG_Q4_0 ? norm_rope_fn<BQG_Q4_0, false>(D) : norm_rope_fn<BQG_BF16, false>(D));
-    return launch(fn, p, std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)sms * 5), 32 * kWarps, s, pdl);
+    const int per_sm = D == 256 ? resident<256>() : D == 128 ? resident<128>() : resident<64>();
+    return launch(fn, p, std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)sms * per_sm), 32 * kWarps, s, pdl);
 }
 
 cudaError_t launch_kv_read(const KvReadParams &p, int fmt, int D, int out_f32, int sms, cudaStream_t s, bool pdl)
