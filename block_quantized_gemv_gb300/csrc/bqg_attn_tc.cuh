@@ -53,7 +53,7 @@ namespace bqg {
 constexpr int kTcTile = 128;             // tokens of a tile
 constexpr int kTcHalf = 128;             // rows of a stream
 constexpr int kTcSoftmaxWarps = 8;
-constexpr int kTcMmaWarp = 8, kTcCopyWarp = 9, kTcBuildWarp = 12;
+constexpr int kTcMmaWarp = 8, kTcCopyWarp = 9, kTcPlanWarp = 10, kTcBuildWarp = 12;
 constexpr int kTcAhead = 2;              // tiles whose scores may be issued before the first values are needed
 constexpr int kTcMarks = 32;             // tiles or pieces that the copying warp may be ahead of the softmax
 
@@ -89,10 +89,12 @@ template <int FMT, int D> struct TcGeom {
     static constexpr int OFF_RAW = OFF_RING + NS * TILE;
     static constexpr int OFF_ML = OFF_RAW + NR * RAW;                   // (maximum, sum) per stream and row
     static constexpr int OFF_SIDES = OFF_ML + 2 * kTcHalf * 8;          // what a raw side holds, 16 bytes each
-    static constexpr int OFF_BARS = OFF_SIDES + 16 * NR;
+    static constexpr int OFF_RS = OFF_SIDES + 16 * NR;                  // softmax scale per row
+    static constexpr int OFF_PIECES = OFF_RS + (QUANT ? kTcHalf * 4 : 0);   // two pieces
+    static constexpr int OFF_BARS = OFF_PIECES + 2 * 64;
     // full, empty per slot; raw full, empty; products done, probabilities (two each);
-    // queries; the softmax warps' meeting point; values landed
-    static constexpr int NBARS = 2 * NS + 2 * NR + 4 + 3;
+    // queries; the softmax warps' meeting point; values landed; piece there, taken (two each)
+    static constexpr int NBARS = 2 * NS + 2 * NR + 4 + 3 + 4;
     static constexpr int OFF_WORDS = OFF_BARS + NBARS * 8;              // tensor memory base, NaN marks, page marks
     static constexpr int SMEM = OFF_WORDS + 8 + 4 * kTcMarks + kTcMarks + 1024;   // + slack for 1024-byte alignment
     static constexpr int S0 = 0, O0 = 256;                              // tensor memory columns, + 128 per stream
@@ -101,24 +103,45 @@ template <int FMT, int D> struct TcGeom {
 
 // Positions of tile g's keys and values in the rings' order K0 K1 V0 K2 V1 K3 V2 ..., the order in which the
 // products take them (g counts all tiles of the CTA; the last values leave the position before them unused).
+// At the end of a piece the values do not wait for the next piece's first keys, which come one position before them.
 __device__ __forceinline__ int tc_k_pos(int g) { return g < kTcAhead ? g : 2 * g - 1; }
 __device__ __forceinline__ int tc_v_pos(int g) { return 2 * g + 2; }
 
 // The pieces of one CTA: consecutive tiles of one (sequence, KV head, row group).
-struct TcPiece {
+struct alignas(16) TcPiece {
     AttnSeq s;
     int h, row0, rows;          // first row of the group, its rows
     int nq;                     // 2: the streams are two halves of the rows; 1: of each tile's tokens
     int tile0, n;               // tiles of the piece
     int c0, c1;                 // CTAs that share the (sequence, KV head, row group)
 };
+// Units: tiles x streams.  Where it costs at most kTcSecond units more than an even share, no CTA
+// takes more than one piece: a second one waits for its queries, its first keys and an
+// idle tensor core, 8 to 9 us, the time of 5 quantized units or 10 of bf16.  Otherwise (more (sequence, KV head, row group)
+// than CTAs, or few of unlike lengths) each takes an equal range of the line of all units.
+// 8 x 5000 tokens q8_0, 64 such groups on 152 CTAs: 46 us with one piece each, 50 with ranges.
+template <int NQ> constexpr int kTcSecond = NQ == 2 ? 10 : 5;
+static_assert(sizeof(TcPiece) == 64, "two pieces in shared memory");
 template <int NQ> struct TcWork {
     int64_t per, cur, end, base;
+    int most;                   // units of a piece where each CTA has one; 0: ranges of `per` units
     AttnSeq s;
     __device__ static __forceinline__ int64_t cost(const AttnParams &p, const AttnSeq &q)
     {
         const int tiles = (q.len + kTcTile - 1) / kTcTile, halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
         return (int64_t)p.cache.n_kv * tiles * halves;
+    }
+    // pieces of at most `most` units (a multiple of NQ) of a KV head: of a row group with NQ halves, of one with fewer, of all
+    struct Pieces { int groups, full, rest, head; };
+    __device__ static __forceinline__ Pieces pieces(const AttnParams &p, const AttnSeq &q, int most)
+    {
+        const unsigned tiles = (q.len + kTcTile - 1) / kTcTile, halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
+        Pieces r;
+        r.groups = halves / NQ;
+        r.full = (tiles * NQ + most - 1) / (unsigned)most;
+        r.rest = halves % NQ ? (tiles + most - 1) / (unsigned)most : 0;
+        r.head = r.groups * r.full + r.rest;
+        return r;
     }
     __device__ __forceinline__ void init(const AttnParams &p, int lane, int &bad)
     {
@@ -127,6 +150,32 @@ template <int NQ> struct TcWork {
         const int64_t total = attn_total(p, lane, weight, bad, s, mine);
         // at least NQ, so that every range between a set's first and last holds the beginning of a tile
         per = max(div_pos(total + gridDim.x - 1, gridDim.x), (int64_t)NQ);
+        most = 0;
+        auto count = [&](int m) {
+            int ignored = 0;
+            unsigned n = lane < p.n_seq ? p.cache.n_kv * pieces(p, s, m).head : 0;
+            for (int b = lane + 32; b < p.n_seq; b += 32) n += p.cache.n_kv * pieces(p, attn_seq(p, b, ignored), m).head;
+            return __reduce_add_sync(0xffffffffu, n);
+        };
+        if (total < (1 << 28)) {
+            int lo = ((int)per + NQ - 1) / NQ - 1, hi = ((int)per + kTcSecond<NQ>) / NQ;      // too small; enough, if any is
+            if (count(hi * NQ) <= gridDim.x) {
+                while (hi - lo > 1) {
+                    const int m = (lo + hi) >> 1;
+                    (count(m * NQ) <= gridDim.x ? hi : lo) = m;
+                }
+                most = hi * NQ;
+            }
+        }
+        if (most) {
+            auto number = [&](const AttnSeq &q) { return (int64_t)p.cache.n_kv * pieces(p, q, most).head; };
+            mine = lane < p.n_seq ? number(s) : 0;
+            cur = blockIdx.x;
+            end = min(cur + 1, (int64_t)count(most));
+            base = 0;
+            if (cur < end) s = attn_find(p, cur, lane, number, s, mine, base);
+            return;
+        }
         cur = per * blockIdx.x;
         end = min(cur + per, total);
         base = 0;
@@ -134,6 +183,25 @@ template <int NQ> struct TcWork {
     }
     __device__ __forceinline__ bool next(const AttnParams &p, TcPiece &o)
     {
+        if (most) {
+            if (cur >= end) return false;
+            const Pieces n = pieces(p, s, most);
+            const unsigned off = (unsigned)(cur - base), rem = off % (unsigned)n.head;
+            const unsigned tiles = (s.len + kTcTile - 1) / kTcTile;
+            o.h = off / (unsigned)n.head;
+            const int g = min((int)(rem / (unsigned)n.full), n.groups);
+            const unsigned j = rem - g * n.full, k = g < n.groups ? n.full : n.rest;               // piece j of k
+            o.row0 = g * NQ * kTcHalf;
+            o.rows = min(NQ * kTcHalf, s.T * p.group - o.row0);
+            o.nq = g < n.groups ? NQ : 1;
+            o.tile0 = j * (tiles / k) + min(j, tiles % k);
+            o.n = tiles / k + (j < tiles % k);
+            o.c0 = blockIdx.x - j;
+            o.c1 = o.c0 + k - 1;
+            o.s = s;
+            cur = end;
+            return true;
+        }
         int ignored = 0;
         while (cur < end) {
             while (cur - base >= cost(p, s)) {
@@ -291,9 +359,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
     auto bar_s = [&](int c) { return bars2 + 8 * (c & 1); };
     auto bar_p = [&](int n) { return bars2 + 16 + 8 * (n & 1); };
     const uint32_t bar_q = bars2 + 32, bar_meet = bars2 + 40, bar_land = bars2 + 48;
+    auto bar_pf = [&](int n) { return bars2 + 56 + 8 * (n & 1); };
+    auto bar_pe = [&](int n) { return bars2 + 72 + 8 * (n & 1); };
     volatile uint32_t *const base_word = reinterpret_cast<volatile uint32_t *>(smem + G::OFF_WORDS);
     volatile uint32_t *const nan_mark = base_word + 2;                                                   // [piece % kTcMarks]
     volatile uint8_t *const dead_strips = reinterpret_cast<volatile uint8_t *>(base_word + 2 + kTcMarks); // [tile % kTcMarks]
+
+    volatile float *const row_scale = reinterpret_cast<volatile float *>(smem + G::OFF_RS);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -308,6 +380,8 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
         for (int i = 0; i < 2; i++) {
             mbar_init(bar_s(i), 1);                    // tcgen05.commit
             mbar_init(bar_p(i), kTcSoftmaxWarps);
+            mbar_init(bar_pf(i), 1);
+            mbar_init(bar_pe(i), kTcSoftmaxWarps + 2 + G::BUILD_WARPS);
         }
         mbar_init(bar_q, kTcSoftmaxWarps);
         mbar_init(bar_meet, kTcSoftmaxWarps);
@@ -332,18 +406,22 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
         if (!ok && lane == 0) atomicOr(error, 2);
         return ok;
     };
-    int bad = 0;
-    TcWork<G::NQ> work;
+    // the next piece from the planning warp into w (whose fields that a role does not use cost it nothing); false: the last was
     TcPiece w;
-    auto begin = [&]() {
-        work.init(p, lane, bad);
-        if (bad && blockIdx.x == 0 && warp == 0) atomicOr(error, bad);
+    int taken = 0;
+    bool ok = true;
+    auto next = [&]() {
+        if (!(ok = wait(bar_pf(taken), (taken >> 1) & 1))) return false;
+        w = *reinterpret_cast<const TcPiece *>(smem + G::OFF_PIECES + (taken & 1) * sizeof(TcPiece));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_pe(taken));
+        taken++;
+        return w.n > 0;
     };
 
     if (warp < kTcSoftmaxWarps) {
         // ---------------- softmax and results ----------------
         if constexpr (G::QUANT) regs_more<G::REGS_SOFTMAX>();
-        begin();
         const int st = warp >> 2, r = (warp & 3) * 32 + lane;                // stream, row of its half
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t to = lanes + G::O0 + 128 * st;
@@ -351,50 +429,60 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
         float *const part_ml = p.part + (int64_t)2 * gridDim.x * G::ROWS * D;
         TcSet set{};                                                         // begun here, ended elsewhere
         int pieces = 0, tiles = 0, commits = 0, steps = 0;                   // before this piece
-        bool ok = true;
-        while (ok && work.next(p, w)) {
+        while (ok && next()) {
             const int np = w.n * w.nq;                                       // steps
             const int grow = w.nq == 2 ? st * kTcHalf + r : r;               // row of the group
             const bool row_ok = grow < w.rows;
             const bool warp_ok = __any_sync(0xffffffffu, row_ok);
             const int row = w.row0 + grow, qi = row / p.group, qh = row - qi * p.group;
             const unsigned long long sees = row_ok ? attn_sees(p, w.s, row) : 0;
-            // the warp's 32 queries into shared memory, a row per CPR lanes, and each lane's row's softmax scale
-            float rs = p.scale_log2;
+            // queries into shared memory, a row per CPR lanes
             {
                 constexpr int CPR = D / 8, RPI = 32 / CPR;                   // chunks per row, rows per step
-                const int64_t mine = row_ok ? (int64_t)(w.s.q0 + qi) * p.q_stride + (int64_t)(w.h * p.group + qh) * D : -1;
+                // bf16: the warp's 32 rows as they are; else 16 rows, which serve both streams
+                constexpr int QROWS = BF ? 32 : 16, N = QROWS * CPR / 32;
+                const int first = BF ? (warp & 3) * 32 : warp * 16;
+                const int qrow = w.row0 + (BF ? grow : first + (lane & 15)), i0 = qrow / p.group;
+                const int64_t mine = qrow < w.row0 + w.rows ? (int64_t)(w.s.q0 + i0) * p.q_stride
+                                                              + (int64_t)(w.h * p.group + qrow - i0 * p.group) * D : -1;
                 const uint32_t dst = sb + G::OFF_Q + (w.nq == 2 ? st : 0) * G::TILE;
                 const int c = lane % CPR;
+                uint4 v[N];
 #pragma unroll
-                for (int i0 = 0; i0 < CPR; i0 += 8) {
-                    uint4 v[8];
+                for (int i = 0; i < N; i++) {
+                    const int64_t from = __shfl_sync(0xffffffffu, mine, i * RPI + lane / CPR);
+                    v[i] = from >= 0 ? *reinterpret_cast<const uint4 *>(p.q + from + 8 * c) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const int64_t from = __shfl_sync(0xffffffffu, mine, (i0 + i) * RPI + lane / CPR);
-                        v[i] = from >= 0 ? *reinterpret_cast<const uint4 *>(p.q + from + 8 * c) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < N; i++)
+                    if (!BF || st == 0 || w.nq == 2) sts128(dst + tc_chunk(first + i * RPI + lane / CPR, c), v[i]);
+                if constexpr (!BF) {
+                    // two lanes per row: its largest value, the power of two, fp16
+                    __syncwarp();
+                    const int r2 = first + (lane >> 1);
+                    auto at = [&](int k) { return dst + tc_chunk(r2, (lane & 1) * 4 + (k & 3) + (k >> 2) * 8); };
+                    uint32_t hi = 0;                                         // bf16 without sign order as integers
+#pragma unroll
+                    for (int k = 0; k < CPR / 2; k++) {
+                        const uint4 x = lds128(at(k));
+                        hi = __vmaxu2(hi, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        if constexpr (!BF) {
-                            float f[8], top = 0.f, inv = 1.f, scale = p.scale_log2;
-                            bf16x8_to_f32(v[i], f);
-#pragma unroll
-                            for (int k = 0; k < 8; k++) top = fmaxf(top, fabsf(f[k]));
-#pragma unroll
-                            for (int o = CPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            if (top > 0.f && top < __int_as_float(0x7f800000)) {
-                                const uint32_t ex = min(__float_as_uint(top) >> 23, 253u);
-                                inv = __uint_as_float((254u - ex) << 23);
-                                scale = fmaxf(p.scale_log2 * (1.0f / inv), 1.17549435e-38f);
-                            }
-                            v[i] = make_uint4(pack2<false>(f[0] * inv, f[1] * inv), pack2<false>(f[2] * inv, f[3] * inv),
-                                              pack2<false>(f[4] * inv, f[5] * inv), pack2<false>(f[6] * inv, f[7] * inv));
-                            const float theirs = __shfl_sync(0xffffffffu, scale, (lane % RPI) * CPR);
-                            if (lane / RPI == i0 + i) rs = theirs;
-                        }
-                        const int to_row = (warp & 3) * 32 + (i0 + i) * RPI + lane / CPR;
-                        if (st == 0 || w.nq == 2) sts128(dst + tc_chunk(to_row, c), v[i]);
+                    hi = max(hi >> 16, hi & 0xffffu);
+                    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+                    float inv = 1.f, scale = p.scale_log2;
+                    if (hi > 0 && hi < 0x7f80u) {
+                        const uint32_t ex = min(hi >> 7, 253u);
+                        inv = __uint_as_float((254u - ex) << 23);
+                        scale = fmaxf(p.scale_log2 * (1.0f / inv), 1.17549435e-38f);
+                    }
+                    if ((lane & 1) == 0) row_scale[r2] = scale;
+#pragma unroll 2
+                    for (int k = 0; k < CPR / 2; k++) {
+                        float f[8];
+                        bf16x8_to_f32(lds128(at(k)), f);
+                        sts128(at(k), make_uint4(pack2<false>(f[0] * inv, f[1] * inv), pack2<false>(f[2] * inv, f[3] * inv),
+                                                 pack2<false>(f[4] * inv, f[5] * inv), pack2<false>(f[6] * inv, f[7] * inv)));
                     }
                 }
             }
@@ -402,11 +490,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_q);
 
-            float top = NEG, sum = 0.f;
+            float top = NEG, sum = 0.f, rs = p.scale_log2;                   // softmax scale of the row
             for (int m = 0; m < np; m++) {
                 const int c = commits + m, i = w.nq == 2 ? m >> 1 : m, half = w.nq == 2 ? m & 1 : st;   // of the tile's tokens
                 if (!(ok = wait(bar_s(c), (c >> 1) & 1))) break;
                 tc_fence_after();
+                // (the products that were waited for were issued after all warps had brought their queries)
+                if (!BF && m == 0) rs = row_scale[r];
                 const uint32_t ts = lanes + G::S0 + 128 * (c & 1) + 64 * st;
                 const int tok0 = (w.tile0 + i) * kTcTile + 64 * half;
                 const unsigned dead = dead_strips[(tiles + i) % kTcMarks] >> (4 * half) & 15;
@@ -565,7 +655,6 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
         if (warp == kTcMmaWarp) {
             // ---------------- products ----------------
             // the whole warp walks the steps, so that operands stay in uniform registers; one lane issues
-            begin();
             constexpr uint32_t TYPE = BF ? 1u : 0u;
             constexpr uint32_t IDESC = (1u << 4) | (TYPE << 7) | (TYPE << 10) | ((uint32_t)(kTcHalf >> 4) << 24);
             constexpr uint32_t IDESC_S = IDESC | ((uint32_t)(kTcTile >> 3) << 17), IDESC_S64 = IDESC | (64u >> 3 << 17);
@@ -573,8 +662,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             const uint64_t k_desc = sw128_desc(sb), v_desc = sw128_desc_mn(sb, G::HALF);
             const bool one = elect_one();
             int tiles = 0, pieces = 0, commits = 0, steps = 0;
-            bool ok = true;
-            while (ok && work.next(p, w)) {
+            while (ok && next()) {
                 if (!(ok = wait(bar_q, pieces & 1))) break;
                 tc_fence_after();
                 pieces++;
@@ -663,7 +751,6 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
         } else if (warp == kTcCopyWarp) {
             // ---------------- keys and values from the cache ----------------
             // a page's tokens (at most 128 of them, a box) at a time: lane i copies the tile's i-th box
-            begin();
             const int box = min(1 << p.cache.lp, kTcTile), boxes = kTcTile / box;
             struct Tile {
                 int64_t row;            // this lane's box: its first cached row
@@ -673,12 +760,11 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             };
             constexpr int RING = G::QUANT ? NR : NS;
             int pieces = 0, tiles = 0, lands = 0, copied = 0;                // copied: positions up to here
-            bool ok = true;
             // keys (side 0) or values (side 1) of a tile into position x
             auto copy = [&](const Tile &q, int side, int x) {
                 const int slot = x % RING, turn = x / RING;
                 if (turn && !(ok = wait(G::QUANT ? bar_rawe(slot) : bar_empty(slot), (turn - 1) & 1))) return;
-                copied = x + 1;
+                copied = max(copied, x + 1);
                 if constexpr (G::QUANT) {
                     const uint32_t dst = sb + G::OFF_RAW + slot * G::RAW;
                     if (lane == 0) {
@@ -707,22 +793,27 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                         // zeros behind the end and where there is no page; new tokens' infinities and NaN out, and marked
                         if (!(ok = wait(bar_land, lands++ & 1))) return;
                         bool hit = false;
+                        constexpr int N = 4;                                 // chunks at a time (kTcTile * D / 8 is a multiple of 32 N)
 #pragma unroll 1
-                        for (int i = (q.dead ? 0 : q.ctx) * (D / 8) + lane; i < kTcTile * (D / 8); i += 32) {
-                            const int r = i / (D / 8), c = i % (D / 8);
-                            const uint32_t at = dst + tc_chunk(r, c);
-                            if (r >= q.len || ((q.dead >> (r >> 4)) & 1)) {
-                                sts128(at, make_uint4(0, 0, 0, 0));
-                            } else if (r >= q.ctx) {
-                                const uint4 v = lds128(at);
-                                uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                                bool any = false;
+                        for (int i0 = (q.dead ? 0 : q.ctx) * (D / 8) / (32 * N) * (32 * N) + lane; i0 < kTcTile * (D / 8); i0 += 32 * N) {
+                            uint4 v[N];
 #pragma unroll
-                                for (int y = 0; y < 4; y++) {
-                                    if ((u[y] & 0x7f80u) == 0x7f80u) { u[y] &= 0xffff0000u; any = true; }
-                                    if ((u[y] & 0x7f800000u) == 0x7f800000u) { u[y] &= 0xffffu; any = true; }
+                            for (int n = 0; n < N; n++) v[n] = lds128(dst + tc_chunk((i0 + 32 * n) / (D / 8), (i0 + 32 * n) % (D / 8)));
+#pragma unroll
+                            for (int n = 0; n < N; n++) {
+                                const int r = (i0 + 32 * n) / (D / 8), c = (i0 + 32 * n) % (D / 8);
+                                uint32_t u[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
+                                bool any = r >= q.len || ((q.dead >> (r >> 4)) & 1);
+                                if (any) {
+                                    u[0] = u[1] = u[2] = u[3] = 0;
+                                } else if (r >= q.ctx) {
+#pragma unroll
+                                    for (int y = 0; y < 4; y++) {
+                                        if ((u[y] & 0x7f80u) == 0x7f80u) { u[y] &= 0xffff0000u; any = hit = true; }
+                                        if ((u[y] & 0x7f800000u) == 0x7f800000u) { u[y] &= 0xffffu; any = hit = true; }
+                                    }
                                 }
-                                if (any) { sts128(at, make_uint4(u[0], u[1], u[2], u[3])); hit = true; }
+                                if (any) sts128(dst + tc_chunk(r, c), make_uint4(u[0], u[1], u[2], u[3]));
                             }
                         }
                         if (hit) nan_mark[(q.mark - 1) % kTcMarks] = (uint32_t)q.mark;
@@ -733,7 +824,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 }
             };
             Tile last{};                                                     // whose values are still to come
-            while (ok && work.next(p, w)) {
+            while (ok && next()) {
                 const int32_t *table = p.table + (int64_t)w.s.b * p.max_pages;
                 auto page_of = [&](int t) {
                     const int tok = t * kTcTile + lane * box;
@@ -758,27 +849,42 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                         if (q.dead) atomicOr(error, BQG_DEVERR_PAGE);
                     }
                     copy(q, 0, tc_k_pos(tiles));
-                    if (ok && tiles) copy(last, 1, tc_v_pos(tiles - 1));
+                    if (ok && t > w.tile0) copy(last, 1, tc_v_pos(tiles - 1));
                     last = q;
                     tiles++;
                 }
+                if (ok) copy(last, 1, tc_v_pos(tiles - 1));
                 pieces++;
             }
-            if (ok && tiles) copy(last, 1, tc_v_pos(tiles - 1));
             // do not leave while copies into shared memory are in flight (position 2 tiles - 1 is not used)
             for (int x = max(0, copied - RING); x < copied; x++)
                 if (x != 2 * tiles - 1) mbar_wait_spin(G::QUANT ? bar_rawf(x % RING) : bar_full(x % RING), (x / RING) & 1);
+        } else if (warp == kTcPlanWarp) {
+            // ---------------- the pieces, for all roles ----------------
+            // one copy of this code: a CTA's first microseconds are mostly spent on fetching instructions
+            int bad = 0;
+            TcWork<G::NQ> work;
+            work.init(p, lane, bad);
+            if (bad && blockIdx.x == 0) atomicOr(error, bad);
+            for (int i = 0; ok; i++) {
+                if (!work.next(p, w)) w.n = 0;
+                if (i >= 2 && !(ok = wait(bar_pe(i), ((i >> 1) - 1) & 1))) break;
+                if (lane == 0) {
+                    *reinterpret_cast<TcPiece *>(smem + G::OFF_PIECES + (i & 1) * sizeof(TcPiece)) = w;
+                    mbar_arrive(bar_pf(i));
+                }
+                __syncwarp();
+                if (w.n == 0) break;
+            }
         }
     } else {
         // ---------------- fp16 tiles from codes and scales ----------------
         if constexpr (G::QUANT) {
             regs_less<G::REGS_OTHER>();
-            begin();
             const int lt = tid - 32 * kTcBuildWarp;                          // 0 .. 255
             constexpr int STEP = 256 / G::CPT;
             const int c = lt % G::CPT, r0 = lt / G::CPT;                     // chunk c of rows r0 + i STEP
             int tiles = 0;
-            bool ok = true;
             auto build = [&](int x) {
                 const int rs = x % NR, slot = x % NS;
                 // lane 0 waits for the side, lane 1 for the slot's last products
@@ -854,12 +960,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     mbar_arrive(bar_full(slot));
                 }
             };
-            while (ok && work.next(p, w))
+            while (ok && next()) {
                 for (int t = 0; t < w.n && ok; t++, tiles++) {
                     build(tc_k_pos(tiles));
-                    if (ok && tiles) build(tc_v_pos(tiles - 1));
+                    if (ok && t) build(tc_v_pos(tiles - 1));
                 }
-            if (ok && tiles) build(tc_v_pos(tiles - 1));
+                if (ok) build(tc_v_pos(tiles - 1));
+            }
         }
     }
     tc_fence_before();
