@@ -902,54 +902,64 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 const int4 side = *reinterpret_cast<const int4 *>(smem + G::OFF_SIDES + 16 * rs);
                 const uint32_t dst = sb + G::OFF_RING + slot * G::TILE;
                 const uint8_t *src = smem + G::OFF_RAW + rs * G::RAW;
-                constexpr int N = G::CHUNKS / 256;
-                uint4 codes[N];
-                uint32_t scale[N];
-#pragma unroll
-                for (int i = 0; i < N; i++) {
-                    codes[i] = *reinterpret_cast<const uint4 *>(src + (i * 256 + lt) * 16);
-                    scale[i] = *reinterpret_cast<const uint16_t *>(src + kTcTile * G::RB + ((r0 + i * STEP) * G::NB + (FMT == BQG_Q8_0 ? c >> 1 : c)) * 2);
-                }
+                constexpr int M = G::CHUNKS / 256;
+                const bool plain = side.x >= kTcTile && side.y >= kTcTile && side.z == 0;
                 bool hit = false;
+                // STEP is a multiple of 8: a thread's chunks have the same place in their rows' swizzle.  Chunks of a row's
+                // second 64 values are stored in the other order: distinct banks
+                static_assert(STEP % 8 == 0, "swizzle");
+                constexpr int OUT = FMT == BQG_Q8_0 ? 2 : 4;                 // chunks of fp16 from one of codes
+                const int f = FMT == BQG_Q8_0 ? (c >> 2) & 1 : (c >> 1) & 1;
+                uint32_t at[OUT];
 #pragma unroll
-                for (int i = 0; i < N; i++) {
-                    const int r = r0 + i * STEP;
-                    const uint4 q = codes[i];
-                    uint32_t d = scale[i];
+                for (int k = 0; k < OUT; k++) at[k] = dst + tc_chunk(r0, OUT * c + (k ^ (f * (OUT / 2))));
+                uint4 codes[M];
+                uint32_t scale[M];
+#pragma unroll
+                for (int i = 0; i < M; i++) {
+                    codes[i] = *reinterpret_cast<const uint4 *>(src + (i * 256 + lt) * 16);
+                    scale[i] = *reinterpret_cast<const uint16_t *>(src + kTcTile * G::RB + ((r0 + i * STEP) * G::NB
+                                                                                           + (FMT == BQG_Q8_0 ? c >> 1 : c)) * 2);
+                }
+                if (!plain) {
                     // no token: zeros; a new token's infinite or NaN scale: zeros, and marked
-                    if (r >= side.x || ((side.z >> (r >> 4)) & 1)) d = 0;
-                    if (r >= side.y && (d & 0x7c00u) == 0x7c00u) { d = 0; hit = true; }
-                    d |= d << 16;
-                    const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int i = 0; i < M; i++) {
+                        const int r = r0 + i * STEP;
+                        if (r >= side.x || ((side.z >> (r >> 4)) & 1)) scale[i] = 0;
+                        if (r >= side.y && (scale[i] & 0x7c00u) == 0x7c00u) { scale[i] = 0; hit = true; }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < M; i++) {
+                    const uint4 q = codes[i];
+                    const uint32_t d = __byte_perm(scale[i], 0, 0x1010), o = i * STEP * 128;
                     if constexpr (FMT == BQG_Q8_0) {
-                        uint32_t u[8];
+                        const uint32_t wd[4] = {f ? q.z : q.x, f ? q.w : q.y, f ? q.x : q.z, f ? q.y : q.w};
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const uint32_t b = wd[k] ^ 0x80808080u;
-                            u[2 * k] = hmul2(hsub2(__byte_perm(b, 0x64646464u, 0x4140), 0x64806480u), d);
-                            u[2 * k + 1] = hmul2(hsub2(__byte_perm(b, 0x64646464u, 0x4342), 0x64806480u), d);
+                        for (int k = 0; k < 2; k++) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int n = 0; n < 2; n++) {
+                                const uint32_t b = wd[2 * k + n] ^ 0x80808080u;
+                                u[2 * n] = hmul2(hsub2(__byte_perm(b, 0x64646464u, 0x4140), 0x64806480u), d);
+                                u[2 * n + 1] = hmul2(hsub2(__byte_perm(b, 0x64646464u, 0x4342), 0x64806480u), d);
+                            }
+                            sts128(at[k] + o, make_uint4(u[0], u[1], u[2], u[3]));
                         }
-                        // a row's second half of chunks stores in the other order: distinct banks
-                        const uint4 lo = make_uint4(u[0], u[1], u[2], u[3]), hi = make_uint4(u[4], u[5], u[6], u[7]);
-                        const int f = (c >> 2) & 1;
-                        sts128(dst + tc_chunk(r, 2 * c + f), f ? hi : lo);
-                        sts128(dst + tc_chunk(r, 2 * c + 1 - f), f ? lo : hi);
                     } else {
-                        uint32_t u[16];                                       // value pairs of the block in order
+                        const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const uint32_t b = wd[k] & 0x0f0f0f0fu, e = (wd[k] >> 4) & 0x0f0f0f0fu;
-                            u[2 * k] = hmul2(hsub2(__byte_perm(b, 0x64646464u, 0x4140), 0x64086408u), d);
-                            u[2 * k + 1] = hmul2(hsub2(__byte_perm(b, 0x64646464u, 0x4342), 0x64086408u), d);
-                            u[8 + 2 * k] = hmul2(hsub2(__byte_perm(e, 0x64646464u, 0x4140), 0x64086408u), d);
-                            u[8 + 2 * k + 1] = hmul2(hsub2(__byte_perm(e, 0x64646464u, 0x4342), 0x64086408u), d);
+                        for (int k = 0; k < 4; k++) {                     // low nibbles of words 0, 1, of 2, 3, high ones
+                            uint32_t u[4];
+#pragma unroll
+                            for (int n = 0; n < 2; n++) {
+                                const uint32_t b = (wd[2 * (k & 1) + n] >> (((k >> 1) ^ f) * 4)) & 0x0f0f0f0fu;
+                                u[2 * n] = hmul2(hsub2(__byte_perm(b, 0x64646464u, 0x4140), 0x64086408u), d);
+                                u[2 * n + 1] = hmul2(hsub2(__byte_perm(b, 0x64646464u, 0x4342), 0x64086408u), d);
+                            }
+                            sts128(at[k] + o, make_uint4(u[0], u[1], u[2], u[3]));
                         }
-                        const bool f = c >> 1;                                // the second 64 values: pairs of chunks swapped
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            sts128(dst + tc_chunk(r, 4 * c + (k ^ (f ? 2 : 0))),
-                                   f ? make_uint4(u[4 * (k ^ 2)], u[4 * (k ^ 2) + 1], u[4 * (k ^ 2) + 2], u[4 * (k ^ 2) + 3])
-                                     : make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]));
                     }
                 }
                 if (hit) nan_mark[(side.w - 1) % kTcMarks] = (uint32_t)side.w;
