@@ -24,7 +24,7 @@
 //    scores of the step after next, behind one wait for all they need and with
 //    one commit.  (A wait that is already over costs this warp 100 to 200 cycles and a commit 30 to
 //    120, so a step per stream with three waits took 1230 cycles for 640 of products.)
-//  * Warp 9 brings keys and values.  bf16: straight into the ring of tiles, in TMA boxes
+//  * Warp 10 plans the CTA's pieces; warp 9 brings keys, warp 11 values.  bf16: straight into the ring of tiles, in TMA boxes
 //    of 64 values x the tokens of a page.  q8_0 / q4_0: codes and scales as they
 //    lie, one bulk copy each per page, into a ring of their own, from which warps
 //    12-19 build the tile: codes as fp16 integers (bqg_attn.cuh), times the
@@ -53,9 +53,9 @@ namespace bqg {
 constexpr int kTcTile = 128;             // tokens of a tile
 constexpr int kTcHalf = 128;             // rows of a stream
 constexpr int kTcSoftmaxWarps = 8;
-constexpr int kTcMmaWarp = 8, kTcCopyWarp = 9, kTcPlanWarp = 10, kTcBuildWarp = 12;
+constexpr int kTcMmaWarp = 8, kTcKeyWarp = 9, kTcPlanWarp = 10, kTcValueWarp = 11, kTcBuildWarp = 12;
 constexpr int kTcAhead = 2;              // tiles whose scores may be issued before the first values are needed
-constexpr int kTcMarks = 32;             // tiles or pieces that the copying warp may be ahead of the softmax
+constexpr int kTcMarks = 32;             // tiles or pieces that the copying warps may be ahead of the softmax
 
 // A set of tiles shared by several CTAs, as its first CTA describes it for the join (rows 0: none).
 struct TcSet {
@@ -101,11 +101,27 @@ template <int FMT, int D> struct TcGeom {
     static_assert(SMEM <= 232448, "shared memory");
 };
 
-// Positions of tile g's keys and values in the rings' order K0 K1 V0 K2 V1 K3 V2 ..., the order in which the
-// products take them (g counts all tiles of the CTA; the last values leave the position before them unused).
-// At the end of a piece the values do not wait for the next piece's first keys, which come one position before them.
-__device__ __forceinline__ int tc_k_pos(int g) { return g < kTcAhead ? g : 2 * g - 1; }
-__device__ __forceinline__ int tc_v_pos(int g) { return 2 * g + 2; }
+// Ring positions of the keys and values of tile t of a piece of n tiles, in the order in which the products
+// take them: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1); `before`: tiles of the CTA's earlier pieces.  Position x lies
+// in slot x % slots, in the slot's phase x / slots.  A phase's parity tells nothing to who may be two
+// phases off, so whoever waits for a slot's phase has to know that the one before is complete.
+//  * Quantized: a CTA's positions are numbered through.  The build warps take them in this order, so who has seen position
+//    x - 3 of the raw ring emptied knows it of all before; consecutive positions of keys (or
+//    values) are at most 3 apart, no more than the ring has slots.  (With the numbers of bf16 a key warp
+//    that saw a piece's last values emptied knew nothing of the next one's first keys.)
+//  * bf16: a slot serves keys or values only (but for the very first keys), so each copying warp has
+//    waited for every phase of its slots; numbered through all pieces, the last values before the next piece's
+//    first keys leave the position before theirs to them.
+template <bool QUANT> __device__ __forceinline__ int tc_k_pos(int before, int t)
+{
+    if constexpr (QUANT) return 2 * before + (t < kTcAhead ? t : 2 * t - 1);
+    return before + t < kTcAhead ? before + t : 2 * (before + t) - 1;
+}
+template <bool QUANT> __device__ __forceinline__ int tc_v_pos(int before, int t, int n)
+{
+    if constexpr (QUANT) return 2 * before + (t == n - 1 ? 2 * n - 1 : 2 * t + 2);
+    return 2 * (before + t) + 2;
+}
 
 // The pieces of one CTA: consecutive tiles of one (sequence, KV head, row group).
 struct alignas(16) TcPiece {
@@ -381,7 +397,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             mbar_init(bar_s(i), 1);                    // tcgen05.commit
             mbar_init(bar_p(i), kTcSoftmaxWarps);
             mbar_init(bar_pf(i), 1);
-            mbar_init(bar_pe(i), kTcSoftmaxWarps + 2 + G::BUILD_WARPS);
+            mbar_init(bar_pe(i), kTcSoftmaxWarps + 3 + G::BUILD_WARPS);
         }
         mbar_init(bar_q, kTcSoftmaxWarps);
         mbar_init(bar_meet, kTcSoftmaxWarps);
@@ -709,7 +725,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     return true;
                 };
                 for (int m = 0; m < 2 && ok; m++) {
-                    const int x = tc_k_pos(tiles + (two ? 0 : m)), slot = (m < np) ? x % NS : -1;
+                    const int x = tc_k_pos<G::QUANT>(tiles, two ? 0 : m), slot = (m < np) ? x % NS : -1;
                     if (!(ok = wait_for(m, false, 0, 0, slot, x / NS))) break;
                     if (one) {
                         if (slot >= 0) scores(m, commits + m, slot);
@@ -720,7 +736,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 }
                 for (int m = 0; m < np && ok; m++) {
                     const int tv = two ? m >> 1 : m, tk = two ? (m + 2) >> 1 : m + 2;
-                    const int xv = tc_v_pos(tiles + tv), xk = tc_k_pos(tiles + tk);
+                    const int xv = tc_v_pos<G::QUANT>(tiles, tv, w.n), xk = tc_k_pos<G::QUANT>(tiles, tk);
                     const int slot_v = xv % NS, slot_k = m + 2 < np ? xk % NS : -1;
                     if (!(ok = wait_for(m, true, slot_v, xv / NS, slot_k, xk / NS))) break;
                     const int c = commits + m;                               // (c + 2 has the same parity)
@@ -748,9 +764,12 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 tiles += w.n;
             }
             // (every piece's last products were waited for by its softmax warps before they left)
-        } else if (warp == kTcCopyWarp) {
+        } else if (warp == kTcKeyWarp || warp == kTcValueWarp) {
             // ---------------- keys and values from the cache ----------------
-            // a page's tokens (at most 128 of them, a box) at a time: lane i copies the tile's i-th box
+            // a page's tokens (at most 128 of them, a box) at a time: lane i copies the tile's i-th box.  A warp for keys, one for
+            // values: a box costs its warp about 100 cycles (16 of them, codes and scales of 16-token pages, 2000 per side).
+            // Who waits for a slot's phase has seen the one before, as slots are emptied in the order of the positions.
+            const int side = warp == kTcValueWarp;
             const int box = min(1 << p.cache.lp, kTcTile), boxes = kTcTile / box;
             struct Tile {
                 int64_t row;            // this lane's box: its first cached row
@@ -759,12 +778,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 int ctx, len, mark;     // first new token and end within the tile; mark of the piece
             };
             constexpr int RING = G::QUANT ? NR : NS;
-            int pieces = 0, tiles = 0, lands = 0, copied = 0;                // copied: positions up to here
-            // keys (side 0) or values (side 1) of a tile into position x
-            auto copy = [&](const Tile &q, int side, int x) {
+            int pieces = 0, tiles = 0, lands = 0;
+            int last[4] = {-1, -1, -1, -1};                                  // own positions, newest first: all that a ring can hold
+            // keys or values of a tile into position x
+            auto copy = [&](const Tile &q, int x) {
                 const int slot = x % RING, turn = x / RING;
                 if (turn && !(ok = wait(G::QUANT ? bar_rawe(slot) : bar_empty(slot), (turn - 1) & 1))) return;
-                copied = max(copied, x + 1);
+                last[3] = last[2]; last[2] = last[1]; last[1] = last[0]; last[0] = x;
                 if constexpr (G::QUANT) {
                     const uint32_t dst = sb + G::OFF_RAW + slot * G::RAW;
                     if (lane == 0) {
@@ -823,7 +843,6 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     }
                 }
             };
-            Tile last{};                                                     // whose values are still to come
             while (ok && next()) {
                 const int32_t *table = p.table + (int64_t)w.s.b * p.max_pages;
                 auto page_of = [&](int t) {
@@ -844,21 +863,20 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     q.ctx = min(max(0, w.s.ctx - t * kTcTile), kTcTile);
                     q.len = min(w.s.len - t * kTcTile, kTcTile);
                     q.mark = pieces + 1;
-                    if (lane == 0) {
-                        dead_strips[tiles % kTcMarks] = (uint8_t)q.dead;
+                    if (side == 0 && lane == 0) {
+                        dead_strips[(tiles + t - w.tile0) % kTcMarks] = (uint8_t)q.dead;
                         if (q.dead) atomicOr(error, BQG_DEVERR_PAGE);
                     }
-                    copy(q, 0, tc_k_pos(tiles));
-                    if (ok && t > w.tile0) copy(last, 1, tc_v_pos(tiles - 1));
-                    last = q;
-                    tiles++;
+                    copy(q, side ? tc_v_pos<G::QUANT>(tiles, t - w.tile0, w.n) : tc_k_pos<G::QUANT>(tiles, t - w.tile0));
                 }
-                if (ok) copy(last, 1, tc_v_pos(tiles - 1));
+                tiles += w.n;
                 pieces++;
             }
-            // do not leave while copies into shared memory are in flight (position 2 tiles - 1 is not used)
-            for (int x = max(0, copied - RING); x < copied; x++)
-                if (x != 2 * tiles - 1) mbar_wait_spin(G::QUANT ? bar_rawf(x % RING) : bar_full(x % RING), (x / RING) & 1);
+            // do not leave while own copies into shared memory are in flight
+            const int past = 2 * tiles + (G::QUANT ? 0 : 1);                 // the positions' end
+            for (int i = 0; i < 4; i++)
+                if (last[i] >= max(0, past - RING))
+                    mbar_wait_spin(G::QUANT ? bar_rawf(last[i] % RING) : bar_full(last[i] % RING), (last[i] / RING) & 1);
         } else if (warp == kTcPlanWarp) {
             // ---------------- the pieces, for all roles ----------------
             // one copy of this code: a CTA's first microseconds are mostly spent on fetching instructions
@@ -971,11 +989,12 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 }
             };
             while (ok && next()) {
-                for (int t = 0; t < w.n && ok; t++, tiles++) {
-                    build(tc_k_pos(tiles));
-                    if (ok && t) build(tc_v_pos(tiles - 1));
+                for (int t = 0; t < w.n && ok; t++) {
+                    build(tc_k_pos<true>(tiles, t));
+                    if (ok && t) build(tc_v_pos<true>(tiles, t - 1, w.n));
                 }
-                if (ok) build(tc_v_pos(tiles - 1));
+                if (ok) build(tc_v_pos<true>(tiles, w.n - 1, w.n));
+                tiles += w.n;
             }
         }
     }
