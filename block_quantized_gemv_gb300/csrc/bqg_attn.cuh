@@ -25,10 +25,9 @@
 //    as M, 16 at least, half the products, scores, exponentials and
 //    accumulators of 8 rows were padding: 637 instructions per strip).  P^T
 //    goes from accumulators to operand with one movmatrix per 8 x 8.
-//    bf16: as stored.  q8_0 / q4_0: the codes are built as exact fp16 integers
-//    (a byte under 0x64 is 1024 + byte); a key block's two products give an
-//    exact block sum that is scaled by its fp16 scale in fp32; a value is
-//    q d rounded once to fp16 (relative 2^-12).  The queries then are fp16
+//    bf16: as stored.  q8_0 / q4_0: a key's codes are fp16 numbers as they lie (make_q), their block sum
+//    is scaled by its fp16 scale in fp32; a value's code becomes an fp16 integer (a byte under 0x64
+//    is 1024 + byte) and is multiplied by the scale, rounded once to fp16 (relative 2^-12).  The queries then are fp16
 //    too: each row is scaled by a power of two (exact) so that its largest
 //    value lies in [1, 2), which keeps a bf16 value's eight bits down to 2^-16
 //    of the largest; the power goes into the row's softmax scale.
@@ -85,7 +84,8 @@ template <int FMT, int D, int RT> struct AttnGeom {
     static constexpr int OFF_ML = OFF_P + kAttnWarps * 8 * kStrip * 4;  // (maximum, sum) per warp and row
     static constexpr int OFF_VIS = OFF_ML + kAttnWarps * ROWS * 8;      // new tokens that each row sees
     static constexpr int OFF_RS = OFF_VIS + ROWS * 8;                   // softmax scale per row
-    static constexpr int OFF_FLAG = OFF_RS + ROWS * 4;
+    static constexpr int OFF_BIAS = OFF_RS + ROWS * 4;                  // quantized keys: [row tile][block][row], see make_q
+    static constexpr int OFF_FLAG = OFF_BIAS + (FMT == BQG_BF16 ? 0 : ROWS * NB * 4);
     static constexpr int SMEM = OFF_FLAG + 16;
 };
 
@@ -377,8 +377,13 @@ template <int FMT, int D, int RT> struct AttnKernel {
             }
         }
     }
-    // Their fragments (KS steps x 2 registers), and the softmax scale of this lane's row.
-    static __device__ __forceinline__ void make_q(const AttnParams &p, const RawQ &q, uint32_t (&qf)[G::KS][2], float &rs)
+    // Their fragments (KS steps x 2 registers), the softmax scale of this lane's row, and bias[b]:
+    // a code's bits are taken as an fp16 number as they lie, u 2^-24 exactly for the unsigned code u = q + B, so
+    //     sum q_k = 2^24 (sum u 2^-24 q_k  -  B 2^-24 sum q_k),
+    // whose second term is what the products of block b begin with.  (q4_0's nibbles 2, 3 of a half word are 16 u 2^-24: their
+    // queries are smaller by 16.)
+    static __device__ __forceinline__ void make_q(const AttnParams &p, const RawQ &q, uint32_t (&qf)[G::KS][2], float &rs,
+                                                  float (&bias)[G::NB])
     {
         rs = p.scale_log2;
         if constexpr (BF) {
@@ -405,8 +410,20 @@ template <int FMT, int D, int RT> struct AttnKernel {
                     w[2] = __byte_perm(c, w[3], 0x5410); w[3] = __byte_perm(c, w[3], 0x7632);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    qf[2 * b + (j >> 1)][j & 1] = pack2<false>(bf16_lo(w[j]) * inv, bf16_hi(w[j]) * inv);
+                for (int j = 0; j < 4; j++) {
+                    const float by = (j >> 1) || FMT == BQG_Q8_0 ? 1.0f : 16.0f;     // (16 inv may be infinite)
+                    qf[2 * b + (j >> 1)][j & 1] = pack2<false>(bf16_lo(w[j]) * inv * by, bf16_hi(w[j]) * inv * by);
+                }
+                float part[2] = {0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&qf[2 * b + (j >> 1)][j & 1]));
+                    part[j >> 1] += f.x + f.y;
+                }
+                float sum = FMT == BQG_Q8_0 ? part[0] + part[1] : fmaf(16.0f, part[1], part[0]);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                bias[b] = sum * (FMT == BQG_Q8_0 ? -0x1p-17f : -0x1p-21f);      // 128 2^-24, 8 2^-24
             }
         }
     }
@@ -451,7 +468,9 @@ template <int FMT, int D, int RT> struct AttnKernel {
 
     // Scores of the strip in stage `st`: s[row tile] = tokens lane / 4 (elements 0, 1) and 8 on (2, 3) x
     // rows 2 (lane % 4) and the next.
-    template <typename QF> static __device__ __forceinline__ void scores(uint32_t st, int lane, const QF &qf, float (&s)[RT][4])
+    // bias: this lane's part of the row tiles' OFF_BIAS.
+    template <typename QF>
+    static __device__ __forceinline__ void scores(uint32_t st, int lane, const QF &qf, uint32_t bias, float (&s)[RT][4])
     {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -495,17 +514,16 @@ template <int FMT, int D, int RT> struct AttnKernel {
                     if constexpr (FMT == BQG_Q8_0) {
                         uint2 w = lds64(st + chunk_at<G::CPT>(8 * x + g, 2 * b + (t >> 1)) + (t & 1) * 8);
                         w.x ^= 0x80808080u; w.y ^= 0x80808080u;              // q + 128
-                        e[x][0] = hsub2(__byte_perm(w.x, 0x64646464u, 0x4140), 0x64806480u);
-                        e[x][1] = hsub2(__byte_perm(w.x, 0x64646464u, 0x4342), 0x64806480u);
-                        e[x][2] = hsub2(__byte_perm(w.y, 0x64646464u, 0x4140), 0x64806480u);
-                        e[x][3] = hsub2(__byte_perm(w.y, 0x64646464u, 0x4342), 0x64806480u);
+                        e[x][0] = __byte_perm(w.x, 0, 0x4140);
+                        e[x][1] = __byte_perm(w.x, 0, 0x4342);
+                        e[x][2] = __byte_perm(w.y, 0, 0x4140);
+                        e[x][3] = __byte_perm(w.y, 0, 0x4342);
                     } else {
-                        // a nibble at bits 0..3 under 0x64 is 1024 + n, at bits 4..7 under 0x54 it is 64 + n
                         const uint32_t w = lds32(st + chunk_at<G::CPT>(8 * x + g, b) + t * 4), w8 = w >> 8;
-                        e[x][0] = hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                        e[x][1] = hsub2((w8 & 0x000f000fu) | 0x64006400u, 0x64086408u);
-                        e[x][2] = hsub2((w & 0x00f000f0u) | 0x54005400u, 0x54805480u);
-                        e[x][3] = hsub2((w8 & 0x00f000f0u) | 0x54005400u, 0x54805480u);
+                        e[x][0] = w & 0x000f000fu;
+                        e[x][1] = w8 & 0x000f000fu;
+                        e[x][2] = w & 0x00f000f0u;
+                        e[x][3] = w8 & 0x00f000f0u;
                     }
                 }
                 const uint32_t h0 = dw[0][b >> 1], h1 = dw[1][b >> 1];
@@ -514,7 +532,8 @@ template <int FMT, int D, int RT> struct AttnKernel {
                 const uint32_t a0[4] = {e[0][0], e[1][0], e[0][1], e[1][1]}, a1[4] = {e[0][2], e[1][2], e[0][3], e[1][3]};
 #pragma unroll
                 for (int m = 0; m < RT; m++) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint2 c = lds64(bias + (m * G::NB + b) * 32);
+                    float acc[4] = {__uint_as_float(c.x), __uint_as_float(c.y), __uint_as_float(c.x), __uint_as_float(c.y)};
                     uint32_t q[2];
                     qf.get(m, 2 * b, q);
                     mma16816<false>(acc, a0, q[0], q[1]);
@@ -526,6 +545,10 @@ template <int FMT, int D, int RT> struct AttnKernel {
                     s[m][3] = fmaf(acc[3], d1, s[m][3]);
                 }
             }
+#pragma unroll
+            for (int m = 0; m < RT; m++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) s[m][i] *= FMT == BQG_Q8_0 ? 0x1p24f : 0x1p20f;
         }
     }
 
@@ -658,6 +681,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     float *const ml = reinterpret_cast<float *>(smem + G::OFF_ML);            // [warp][row][2]
     float *const row_scale = reinterpret_cast<float *>(smem + G::OFF_RS);
+    float *const row_bias = reinterpret_cast<float *>(smem + G::OFF_BIAS);
     unsigned long long *const row_sees = reinterpret_cast<unsigned long long *>(smem + G::OFF_VIS);
     float *const merged = reinterpret_cast<float *>(smem);                    // [warp][row][D + PAD]
     pdl_wait();
@@ -731,8 +755,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
 #pragma unroll
             for (int m = 0; m < RT; m++) {
                 float r;
-                A::make_q(p, raw[m], qf.f[m], r);
-                if (warp == 0 && t == 0) row_scale[8 * m + g] = r;
+                float bias[G::NB];
+                A::make_q(p, raw[m], qf.f[m], r, bias);
+                if (warp == 0 && t == 0) {
+                    row_scale[8 * m + g] = r;
+                    if constexpr (!A::BF)
+#pragma unroll
+                        for (int b = 0; b < G::NB; b++) row_bias[(m * G::NB + b) * 8 + g] = bias[b];
+                }
             }
         } else {
             static_assert(G::QREG || RT <= kAttnWarps, "a row tile per warp");
@@ -740,23 +770,30 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
             if (warp < RT) {
                 uint32_t f[G::KS][2];
                 float r;
-                A::make_q(p, raw[0], f, r);
+                float bias[G::NB];
+                A::make_q(p, raw[0], f, r, bias);
 #pragma unroll
                 for (int ks = 0; ks < G::KS; ks++)
                     *reinterpret_cast<uint2 *>(smem + G::OFF_Q + (warp * G::KS + ks) * 256 + lane * 8) = make_uint2(f[ks][0], f[ks][1]);
-                if (t == 0) row_scale[8 * warp + g] = r;
+                if (t == 0) {
+                    row_scale[8 * warp + g] = r;
+                    if constexpr (!A::BF)
+#pragma unroll
+                        for (int b = 0; b < G::NB; b++) row_bias[(warp * G::NB + b) * 8 + g] = bias[b];
+                }
             }
         }
         if (tid < G::ROWS) row_sees[tid] = attn_sees(p, s, row0 + tid);
         __syncthreads();
         float rs[RT][2];                                                      // rows 8 m + 2 t, + 1
-        float o[RT][MT][4], top[RT][2], sum[RT][2];
+        float o[RT][MT][4], top[RT][2], sum[RT][2], from[RT][2];              // from: what the exponents are relative to
 #pragma unroll
         for (int m = 0; m < RT; m++) {
             rs[m][0] = row_scale[8 * m + 2 * t];
             rs[m][1] = row_scale[8 * m + 2 * t + 1];
             top[m][0] = top[m][1] = NEG;
             sum[m][0] = sum[m][1] = 0.f;
+            from[m][0] = from[m][1] = A::kShift;
 #pragma unroll
             for (int x = 0; x < MT; x++)
 #pragma unroll
@@ -776,7 +813,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
             stage = stage + 1 == S ? 0 : stage + 1;
 
             float sc[RT][4];
-            A::scores(st, lane, qf, sc);
+            A::scores(st, lane, qf, sb + G::OFF_BIAS + t * 8, sc);
             const bool edge = tok0 + kStrip > s.ctx || !ok;                   // new tokens, the end, or no page
             if (edge) {
 #pragma unroll
@@ -810,6 +847,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                         v = fmaxf(v, top[m][r]);
                         const float c = (v == top[m][r]) ? 1.f : ex2(top[m][r] - v);
                         top[m][r] = v;
+                        from[m][r] = A::kShift - (v == NEG ? 0.f : v);
                         sum[m][r] *= c;
 #pragma unroll
                         for (int x = 0; x < MT; x++) { o[m][x][r] *= c; o[m][x][2 + r] *= c; }
@@ -823,9 +861,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                 float e[4];
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
-                    const float off = A::kShift - (top[m][r] == NEG ? 0.f : top[m][r]);
-                    e[r] = ex2(fmaf(sc[m][r], rs[m][r], off));
-                    e[2 + r] = ex2(fmaf(sc[m][2 + r], rs[m][r], off));
+                    e[r] = ex2(fmaf(sc[m][r], rs[m][r], from[m][r]));
+                    e[2 + r] = ex2(fmaf(sc[m][2 + r], rs[m][r], from[m][r]));
                     sum[m][r] += e[r] + e[2 + r];
                 }
                 pb[m][0] = transpose8x8(pack2<A::BF>(e[0], e[1]));

@@ -3,7 +3,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstdlib>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -37,15 +36,12 @@ inline cudaError_t take_error(int &word, int *out)
     return cudaSuccess;
 }
 
-// Rows from which the tcgen05 kernel serves a call (BQG_ATTN_TC_ROWS; read once).
-inline int attn_tc_rows()
-{
-    static const int n = [] {
-        const char *v = getenv("BQG_ATTN_TC_ROWS");
-        return (v && *v) ? std::max(1, atoi(v)) : 17;
-    }();
-    return n;
-}
+// Rows from which the tcgen05 kernel serves a call of head_dim 64 or 128.  Measured with 4 heads on each of 8 KV heads
+// of 128 values, 1 to 64 sequences of 200 to 40,000 tokens, each kernel's time over the mma.sync kernel's:
+// 12 and 16 rows (two of its row tiles) 0.6 to 1.4 for bf16, but 0.9 to 2.1 for q8_0 and q4_0; 24 and 32 rows (with
+// four row tiles) 0.4 to 1.1 for bf16 and 0.6 to 1.3 for the quantized formats, above 1.05 only for 64
+// sequences of up to 1500 tokens.
+constexpr int kAttnTcRows = 17;
 
 inline void attn_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int threads, int smem, cudaStream_t s,
                         bool pdl)
@@ -157,14 +153,11 @@ template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, Att
     return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D, G::ROWS>, p, grid);
 }
 
-// The mma.sync kernel with enough row tiles of 8 for `rows` rows, up to 32
-// (16 at head_dim 256, whose accumulators would not fit in registers).
+// The mma.sync kernel with one or two row tiles of 8 (more rows are taken in turn: head_dim 256 only).
 template <int FMT, int D> cudaError_t attn_rows_pick(const AttnParams &p, int rows, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
     if (rows <= 8) return attn_rows_call<FMT, D, 1>(p, error, plan, s, pdl);
-    if (rows <= 16 || D == 256) return attn_rows_call<FMT, D, 2>(p, error, plan, s, pdl);
-    if constexpr (D < 256) return attn_rows_call<FMT, D, 4>(p, error, plan, s, pdl);
-    return cudaErrorInvalidValue;
+    return attn_rows_call<FMT, D, 2>(p, error, plan, s, pdl);
 }
 
 // rows: the most rows (new tokens x heads of a group) of any sequence.  Few
@@ -187,7 +180,7 @@ cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, A
         }
         error = static_cast<int *>(word);
     }
-    const bool tc = rows >= attn_tc_rows();
+    const bool tc = rows >= kAttnTcRows;
     if (D == 64) return tc ? attn_tc_call<FMT, 64>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 64>(p, rows, error, plan, s, pdl);
     if (D == 128) return tc ? attn_tc_call<FMT, 128>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 128>(p, rows, error, plan, s, pdl);
     return attn_rows_pick<FMT, 256>(p, rows, error, plan, s, pdl);

@@ -1019,21 +1019,33 @@ template <int D, int ROWS> __global__ void __launch_bounds__(256) attn_tc_join_k
     const float2 *ml = reinterpret_cast<const float2 *>(p.part + (int64_t)2 * ctas * ROWS * D);
     const float4 *part = reinterpret_cast<const float4 *>(p.part);
     auto slot = [&](int c) { return attn_slot_row<1>(c, set.c0, 0); };
-    float mt = -__builtin_huge_valf();
-#pragma unroll 4
-    for (int c = set.c0; c <= set.c1; c++) mt = fmaxf(mt, ml[slot(c) * ROWS + row].x);
-    float l = 0.f, v[4 * V];
+    // in one pass, relative to the largest maximum so far, four pieces' loads at a time
+    float mt = -__builtin_huge_valf(), l = 0.f, v[4 * V];
 #pragma unroll
     for (int i = 0; i < 4 * V; i++) v[i] = 0.f;
-#pragma unroll 2
-    for (int c = set.c0; c <= set.c1; c++) {
-        const float2 q = ml[slot(c) * ROWS + row];
-        const float w = (q.x == mt) ? 1.f : ex2(q.x - mt);
-        l += w * q.y;
+    constexpr int N = 4;
+    for (int c = set.c0; c <= set.c1; c += N) {
+        float2 q[N];
+        float4 a[N][V];
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-            const float4 a = part[(slot(c) * (D / 4) + warp * V + i) * ROWS + row];
-            v[4 * i] += w * a.x; v[4 * i + 1] += w * a.y; v[4 * i + 2] += w * a.z; v[4 * i + 3] += w * a.w;
+        for (int n = 0; n < N; n++) {
+            if (c + n > set.c1) break;
+            q[n] = ml[slot(c + n) * ROWS + row];
+#pragma unroll
+            for (int i = 0; i < V; i++) a[n][i] = part[(slot(c + n) * (D / 4) + warp * V + i) * ROWS + row];
+        }
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            if (c + n > set.c1) break;
+            const float up = fmaxf(mt, q[n].x);
+            const float w0 = mt == up ? 1.f : ex2(mt - up), w = q[n].x == up ? 1.f : ex2(q[n].x - up);
+            mt = up;
+            l = l * w0 + w * q[n].y;
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                v[4 * i] = v[4 * i] * w0 + w * a[n][i].x; v[4 * i + 1] = v[4 * i + 1] * w0 + w * a[n][i].y;
+                v[4 * i + 2] = v[4 * i + 2] * w0 + w * a[n][i].z; v[4 * i + 3] = v[4 * i + 3] * w0 + w * a[n][i].w;
+            }
         }
     }
     const float inv = l == 0.f ? 0.f : 1.0f / l;
