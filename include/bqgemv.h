@@ -366,17 +366,18 @@ int bqg_kv_read(const bqg_kv_cache *cache, const int64_t *slots, int64_t T, int 
  * bf16, contiguous.  q_start: n_seq + 1 int32, ascending from 0, the last
  * one n_tokens.  ctx_len: n_seq int32.  block_table: n_seq rows of max_pages int32.
  * 1 <= max_q <= 64.  scale > 0 and finite.
- * Keys enter the products exactly (bf16, or integer codes whose block sums
- * are scaled in fp32).  Values enter as they are (bf16) or as q d rounded
- * once to fp16 (quantized), so quantized values beyond fp16's range (65504)
- * are out of range here.
+ * Keys and values enter the products as they are (bf16), or (quantized) values as q d rounded
+ * once to fp16 (relative 2^-12), and keys as their integer codes, whose block sums are scaled in fp32, where
+ * max_q * n_q / n_kv is at most 16 or head_dim 256, as q d rounded once to fp16 otherwise.  So
+ * quantized keys and values beyond fp16's range (65504) are out of range here.  A quantized call's queries
+ * are scaled per row by a power of two and rounded to fp16: a value below 2^-16 of its row's largest loses bits.
  * Scores, softmax sums and outputs accumulate in fp32; the probabilities are
  * rounded to the values' type (bf16 or fp16) for the second product; in fp16
  * (quantized) one below 2^-22 of its row's largest loses bits, and below 2^-33
  * it counts as zero.
  * ws: bqg_tree_attention_workspace_size(...) bytes, 16-byte aligned, ZERO
  * before the first call on it (every call leaves its counters zero).  Calls
- * that share a workspace must not overlap.  Results do not depend on timing:
+ * that share a workspace must not overlap.  One or two launches.  Results do not depend on timing:
  * two calls on the same data give the same bits. */
 int bqg_tree_attention(const void *q, int64_t q_stride, const bqg_kv_cache *cache, const int32_t *block_table,
                        int64_t max_pages, const int32_t *ctx_len, const int32_t *q_start, int n_seq, int64_t n_tokens,
