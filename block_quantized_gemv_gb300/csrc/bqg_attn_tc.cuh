@@ -36,6 +36,11 @@
 //    them, the CTA that came last took longer for it than the whole GPU does.
 //  * Every wait is bounded; one that gives up sets the error word, and the
 //    rest of the CTA's work is skipped.
+//  * Measured (head_dim 128, back to back): bf16, 4 x 16,384 tokens, 64 new, 8 heads on each of 8: 128 us, 1080 TFLOP/s; a step of
+//    64 tokens x 256 rows takes 2000 cycles, 1400 of them products (N = 64: each MMA reads its 128 x 16 of Q, 56 cycles
+//    instead of 32).  q8_0, 8 x 5000, 13 new, 4 heads on each of 8: 34.5 us: 7 until the first scores, 1.4 per tile of
+//    128 tokens (building its two sides, 1100 to 1300 cycles each), 2 for the results, 3 for the join.  Two
+//    teams of builders, one per side, took 34 % longer.
 //
 // A drafted token's infinite or NaN value must not reach rows that do not see
 // it, and 0 x NaN in the product would.  In tiles that hold new tokens zeros

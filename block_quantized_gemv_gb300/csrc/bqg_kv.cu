@@ -18,6 +18,10 @@
 // a lane still holds, and the reciprocal roots are taken once, each
 // in the lanes that ended up with its row; the rotation's cos and sin are loaded once
 // for the four rows.
+//
+// Measured (back to back): 7001 tokens of 64 + 8 + 8 heads of 128 values, bf16, norm and rotation: 96 us, bound by issue
+// (148 instructions per row, 71 % of the slots); 8192 tokens of 8 + 8 heads, f32 into q4_0: 28 us, read back as bf16: 10.4 us,
+// 0.6 of the copy rate; one token: 3.6 and 2.2 us, a launch's latency.
 #include <algorithm>
 
 #include "bqg_kv.cuh"
@@ -312,7 +316,8 @@ __device__ __forceinline__ void encode_rows(const F2 (&y)[2][D / 32], int rows, 
     }
 }
 
-// CTAs per SM: registers allow so many, and a grid of that many has no second wave.
+// CTAs per SM: registers allow so many, and a grid of that many has no second wave.  (D = 128, 7001 tokens: 95.8 us with six,
+// 98.4 with seven, 104.3 with eight, whose registers spill.)
 template <int D> constexpr int resident() { return D == 256 ? 3 : D == 128 ? 6 : 8; }
 
 // Four rows of one token and kind, as loaded.
