@@ -131,7 +131,7 @@ template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, Att
         const int64_t rows = (p.cache.n_pages * p.cache.n_kv) << p.cache.lp;
         if (rows > 0x7fffffff) return cudaErrorInvalidValue;        // beyond any GPU's memory at 128 bytes a row
         const cuuint64_t dim[2] = {(cuuint64_t)D, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)D * 2};
-        const cuuint32_t box[2] = {64, (cuuint32_t)std::min(1 << p.cache.lp, kTcTile)}, one[2] = {1, 1};
+        const cuuint32_t box[2] = {64, (cuuint32_t)std::min(1 << p.cache.lp, G::TT)}, one[2] = {1, 1};
         for (int i = 0; i < 2; i++)
             if (enc(i ? &vmap : &kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, i ? p.cache.v : p.cache.k, dim, stride, box, one,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -141,7 +141,7 @@ template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, Att
     uint8_t *ws = reinterpret_cast<uint8_t *>(p.counters);
     p.counters = reinterpret_cast<int *>(ws + kAttnCounterBytes);
     p.part = reinterpret_cast<float *>(ws + kAttnHead);
-    const int grid = (int)std::max(1.0, std::min((double)ctas, attn_most(p, kTcTile, kTcHalf)));
+    const int grid = (int)std::max(1.0, std::min((double)ctas, attn_most(p, G::TT, kTcHalf)));
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[1];
     attn_config(cfg, attr, dim3(grid), G::THREADS, G::SMEM, s, pdl);
@@ -183,7 +183,7 @@ cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, A
     const bool tc = rows >= kAttnTcRows;
     if (D == 64) return tc ? attn_tc_call<FMT, 64>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 64>(p, rows, error, plan, s, pdl);
     if (D == 128) return tc ? attn_tc_call<FMT, 128>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 128>(p, rows, error, plan, s, pdl);
-    return attn_rows_pick<FMT, 256>(p, rows, error, plan, s, pdl);
+    return tc ? attn_tc_call<FMT, 256>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 256>(p, rows, error, plan, s, pdl);
 }
 
 }  // namespace bqg

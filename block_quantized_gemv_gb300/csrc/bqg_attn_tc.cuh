@@ -55,9 +55,7 @@
 
 namespace bqg {
 
-constexpr int kTcTile = 128;             // tokens of a tile
 constexpr int kTcHalf = 128;             // rows of a stream
-constexpr int kTcSoftmaxWarps = 8;
 constexpr int kTcMmaWarp = 8, kTcKeyWarp = 9, kTcPlanWarp = 10, kTcValueWarp = 11, kTcBuildWarp = 12;
 constexpr int kTcAhead = 2;              // tiles whose scores may be issued before the first values are needed
 constexpr int kTcMarks = 32;             // tiles or pieces that the copying warps may be ahead of the softmax
@@ -70,6 +68,11 @@ struct TcSet {
 
 template <int FMT, int D> struct TcGeom {
     static constexpr bool QUANT = FMT != BQG_BF16;
+    // head_dim 256: one stream, since two would not fit in tensor memory, and tiles of 64 tokens, a step each
+    static constexpr bool SINGLE = D == 256;
+    static constexpr int TT = SINGLE ? 64 : 128;                        // tokens of a tile
+    static constexpr int STREAMS = SINGLE ? 1 : 2;
+    static constexpr int SOFT = 4 * STREAMS;                            // softmax warps
     static constexpr int BUILD_WARPS = QUANT ? 8 : 0;
     static constexpr int THREADS = 32 * (kTcBuildWarp + BUILD_WARPS);
     // registers per thread at launch, and what the warpgroups make of them: 640 threads x 96 =
@@ -77,20 +80,20 @@ template <int FMT, int D> struct TcGeom {
     static constexpr int REGS_SOFTMAX = 144, REGS_OTHER = 64;
     static_assert(!QUANT || 256 * REGS_SOFTMAX + (THREADS - 256) * REGS_OTHER <= THREADS * 96, "register split");
     // halves of a row group: quantized tiles leave room for one tile of queries
-    static constexpr int NQ = QUANT ? 1 : 2;
+    static constexpr int NQ = QUANT || SINGLE ? 1 : 2;
     static constexpr int ROWS = NQ * kTcHalf;                           // rows of a row group
     static constexpr int HALVES = D / 64;                               // 64 values: one 128-byte swizzle atom wide
-    static constexpr int HALF = kTcTile * 128;                          // bytes of a half of a tile of Q, K or V
-    static constexpr int TILE = HALVES * HALF;
-    static constexpr int NS = (D == 64) ? 6 : 4;                        // ring slots (see tc_k_pos)
+    static constexpr int QHALF = kTcHalf * 128, HALF = TT * 128;        // bytes of 64 values of a tile of Q, of K or V
+    static constexpr int QTILE = HALVES * QHALF, TILE = HALVES * HALF;
+    static constexpr int NS = (D == 64) ? 6 : (SINGLE && FMT == BQG_Q8_0) ? 3 : 4;   // ring slots (see tc_k_pos)
     static constexpr int RB = KvRow<FMT, D>::BYTES;
     static constexpr int NB = D / QK;
     static constexpr int CPT = RB / 16;                                 // 16-byte chunks of a cached row
-    static constexpr int CHUNKS = kTcTile * CPT;                        // of a side (a tile's keys or values)
-    static constexpr int RAW = QUANT ? kTcTile * (RB + 2 * NB) : 0;     // codes, then scales, of a side
-    static constexpr int NR = !QUANT ? 0 : RAW > 16384 ? 3 : 5;         // raw sides in flight: 23 to 51 KiB
+    static constexpr int CHUNKS = TT * CPT;                        // of a side (a tile's keys or values)
+    static constexpr int RAW = QUANT ? TT * (RB + 2 * NB) : 0;     // codes, then scales, of a side
+    static constexpr int NR = !QUANT ? 0 : (SINGLE || RAW > 16384) ? 3 : 5;         // raw sides in flight: 23 to 51 KiB
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_RING = NQ * TILE;
+    static constexpr int OFF_RING = NQ * QTILE;
     static constexpr int OFF_RAW = OFF_RING + NS * TILE;
     static constexpr int OFF_ML = OFF_RAW + NR * RAW;                   // (maximum, sum) per stream and row
     static constexpr int OFF_SIDES = OFF_ML + 2 * kTcHalf * 8;          // what a raw side holds, 16 bytes each
@@ -143,20 +146,20 @@ struct alignas(16) TcPiece {
 // 8 x 5000 tokens q8_0, 64 such groups on 152 CTAs: 46 us with one piece each, 50 with ranges.
 template <int NQ> constexpr int kTcSecond = NQ == 2 ? 10 : 5;
 static_assert(sizeof(TcPiece) == 64, "two pieces in shared memory");
-template <int NQ> struct TcWork {
+template <int NQ, int TT> struct TcWork {
     int64_t per, cur, end, base;
     int most;                   // units of a piece where each CTA has one; 0: ranges of `per` units
     AttnSeq s;
     __device__ static __forceinline__ int64_t cost(const AttnParams &p, const AttnSeq &q)
     {
-        const int tiles = (q.len + kTcTile - 1) / kTcTile, halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
+        const int tiles = (q.len + TT - 1) / TT, halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
         return (int64_t)p.cache.n_kv * tiles * halves;
     }
     // pieces of at most `most` units (a multiple of NQ) of a KV head: of a row group with NQ halves, of one with fewer, of all
     struct Pieces { int groups, full, rest, head; };
     __device__ static __forceinline__ Pieces pieces(const AttnParams &p, const AttnSeq &q, int most)
     {
-        const unsigned tiles = (q.len + kTcTile - 1) / kTcTile, halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
+        const unsigned tiles = (q.len + TT - 1) / TT, halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
         Pieces r;
         r.groups = halves / NQ;
         r.full = (tiles * NQ + most - 1) / (unsigned)most;
@@ -208,7 +211,7 @@ template <int NQ> struct TcWork {
             if (cur >= end) return false;
             const Pieces n = pieces(p, s, most);
             const unsigned off = (unsigned)(cur - base), rem = off % (unsigned)n.head;
-            const unsigned tiles = (s.len + kTcTile - 1) / kTcTile;
+            const unsigned tiles = (s.len + TT - 1) / TT;
             o.h = off / (unsigned)n.head;
             const int g = min((int)(rem / (unsigned)n.full), n.groups);
             const unsigned j = rem - g * n.full, k = g < n.groups ? n.full : n.rest;               // piece j of k
@@ -229,7 +232,7 @@ template <int NQ> struct TcWork {
                 base += cost(p, s);
                 s = attn_seq(p, s.b + 1, ignored);
             }
-            const int tiles = (s.len + kTcTile - 1) / kTcTile, all = s.T * p.group;
+            const int tiles = (s.len + TT - 1) / TT, all = s.T * p.group;
             const int halves = (all + kTcHalf - 1) / kTcHalf, groups = (halves + NQ - 1) / NQ;
             const int64_t off = cur - base, head = (int64_t)tiles * halves;
             o.h = (int)div_pos(off, head);
@@ -330,10 +333,10 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4 &v)
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Byte offset of 16-byte chunk c (eight values) of row r in a swizzled tile.
-__device__ __forceinline__ uint32_t tc_chunk(int r, int c)
+// Byte offset of 16-byte chunk c (eight values) of row r in a swizzled tile of ROWS rows.
+template <int ROWS> __device__ __forceinline__ uint32_t tc_chunk(int r, int c)
 {
-    return (uint32_t)((c >> 3) * (kTcTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    return (uint32_t)((c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 // Value `dim` of cached row `row`, as far as it is an infinity or NaN; 0 otherwise.
@@ -400,12 +403,12 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(bar_s(i), 1);                    // tcgen05.commit
-            mbar_init(bar_p(i), kTcSoftmaxWarps);
+            mbar_init(bar_p(i), G::SOFT);
             mbar_init(bar_pf(i), 1);
-            mbar_init(bar_pe(i), kTcSoftmaxWarps + 3 + G::BUILD_WARPS);
+            mbar_init(bar_pe(i), G::SOFT + 3 + G::BUILD_WARPS);
         }
-        mbar_init(bar_q, kTcSoftmaxWarps);
-        mbar_init(bar_meet, kTcSoftmaxWarps);
+        mbar_init(bar_q, G::SOFT);
+        mbar_init(bar_meet, G::SOFT);
         mbar_init(bar_land, 1);
         for (int i = 0; i < kTcMarks; i++) nan_mark[i] = 0;
         mbar_fence_init();
@@ -440,7 +443,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
         return w.n > 0;
     };
 
-    if (warp < kTcSoftmaxWarps) {
+    if (warp < G::SOFT) {
         // ---------------- softmax and results ----------------
         if constexpr (G::QUANT) regs_more<G::REGS_SOFTMAX>();
         const int st = warp >> 2, r = (warp & 3) * 32 + lane;                // stream, row of its half
@@ -460,50 +463,55 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             // queries into shared memory, a row per CPR lanes
             {
                 constexpr int CPR = D / 8, RPI = 32 / CPR;                   // chunks per row, rows per step
-                // bf16: the warp's 32 rows as they are; else 16 rows, which serve both streams
-                constexpr int QROWS = BF ? 32 : 16, N = QROWS * CPR / 32;
-                const int first = BF ? (warp & 3) * 32 : warp * 16;
-                const int qrow = w.row0 + (BF ? grow : first + (lane & 15)), i0 = qrow / p.group;
+                // bf16: the warp's 32 rows as they are; else rows that serve both streams, if there are two
+                constexpr int QROWS = BF ? 32 : kTcHalf / G::SOFT, N = QROWS * CPR / 32, B = N < 16 ? N : 16;
+                const int first = BF ? (warp & 3) * 32 : warp * QROWS;
+                const int qrow = w.row0 + (BF ? grow : first + lane % QROWS), i0 = qrow / p.group;
                 const int64_t mine = qrow < w.row0 + w.rows ? (int64_t)(w.s.q0 + i0) * p.q_stride
                                                               + (int64_t)(w.h * p.group + qrow - i0 * p.group) * D : -1;
-                const uint32_t dst = sb + G::OFF_Q + (w.nq == 2 ? st : 0) * G::TILE;
+                const uint32_t dst = sb + G::OFF_Q + (w.nq == 2 ? st : 0) * G::QTILE;
                 const int c = lane % CPR;
-                uint4 v[N];
+#pragma unroll 1
+                for (int n = 0; n < N; n += B) {
+                    uint4 v[B];
 #pragma unroll
-                for (int i = 0; i < N; i++) {
-                    const int64_t from = __shfl_sync(0xffffffffu, mine, i * RPI + lane / CPR);
-                    v[i] = from >= 0 ? *reinterpret_cast<const uint4 *>(p.q + from + 8 * c) : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < B; i++) {
+                        const int64_t from = __shfl_sync(0xffffffffu, mine, (n + i) * RPI + lane / CPR);
+                        v[i] = from >= 0 ? *reinterpret_cast<const uint4 *>(p.q + from + 8 * c) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < B; i++)
+                        if (!BF || st == 0 || w.nq == 2) sts128(dst + tc_chunk<kTcHalf>(first + (n + i) * RPI + lane / CPR, c), v[i]);
                 }
-#pragma unroll
-                for (int i = 0; i < N; i++)
-                    if (!BF || st == 0 || w.nq == 2) sts128(dst + tc_chunk(first + i * RPI + lane / CPR, c), v[i]);
                 if constexpr (!BF) {
                     // two lanes per row: its largest value, the power of two, fp16
                     __syncwarp();
-                    const int r2 = first + (lane >> 1);
-                    auto at = [&](int k) { return dst + tc_chunk(r2, (lane & 1) * 4 + (k & 3) + (k >> 2) * 8); };
-                    uint32_t hi = 0;                                         // bf16 without sign order as integers
+#pragma unroll 1
+                    for (int r2 = first + (lane >> 1); r2 < first + QROWS; r2 += 16) {
+                        auto at = [&](int k) { return dst + tc_chunk<kTcHalf>(r2, (lane & 1) * 4 + (k & 3) + (k >> 2) * 8); };
+                        uint32_t hi = 0;                                     // bf16 without sign order as integers
 #pragma unroll
-                    for (int k = 0; k < CPR / 2; k++) {
-                        const uint4 x = lds128(at(k));
-                        hi = __vmaxu2(hi, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-                    }
-                    hi = max(hi >> 16, hi & 0xffffu);
-                    hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-                    float inv = 1.f, scale = p.scale_log2;
-                    if (hi > 0 && hi < 0x7f80u) {
-                        const uint32_t ex = min(hi >> 7, 253u);
-                        inv = __uint_as_float((254u - ex) << 23);
-                        scale = fmaxf(p.scale_log2 * (1.0f / inv), 1.17549435e-38f);
-                    }
-                    if ((lane & 1) == 0) row_scale[r2] = scale;
+                        for (int k = 0; k < CPR / 2; k++) {
+                            const uint4 x = lds128(at(k));
+                            hi = __vmaxu2(hi, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                       __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                        }
+                        hi = max(hi >> 16, hi & 0xffffu);
+                        hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+                        float inv = 1.f, scale = p.scale_log2;
+                        if (hi > 0 && hi < 0x7f80u) {
+                            const uint32_t ex = min(hi >> 7, 253u);
+                            inv = __uint_as_float((254u - ex) << 23);
+                            scale = fmaxf(p.scale_log2 * (1.0f / inv), 1.17549435e-38f);
+                        }
+                        if ((lane & 1) == 0) row_scale[r2] = scale;
 #pragma unroll 2
-                    for (int k = 0; k < CPR / 2; k++) {
-                        float f[8];
-                        bf16x8_to_f32(lds128(at(k)), f);
-                        sts128(at(k), make_uint4(pack2<false>(f[0] * inv, f[1] * inv), pack2<false>(f[2] * inv, f[3] * inv),
-                                                 pack2<false>(f[4] * inv, f[5] * inv), pack2<false>(f[6] * inv, f[7] * inv)));
+                        for (int k = 0; k < CPR / 2; k++) {
+                            float f[8];
+                            bf16x8_to_f32(lds128(at(k)), f);
+                            sts128(at(k), make_uint4(pack2<false>(f[0] * inv, f[1] * inv), pack2<false>(f[2] * inv, f[3] * inv),
+                                                     pack2<false>(f[4] * inv, f[5] * inv), pack2<false>(f[6] * inv, f[7] * inv)));
+                        }
                     }
                 }
             }
@@ -519,7 +527,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 // (the products that were waited for were issued after all warps had brought their queries)
                 if (!BF && m == 0) rs = row_scale[r];
                 const uint32_t ts = lanes + G::S0 + 128 * (c & 1) + 64 * st;
-                const int tok0 = (w.tile0 + i) * kTcTile + 64 * half;
+                const int tok0 = (w.tile0 + i) * G::TT + 64 * half;
                 const unsigned dead = dead_strips[(tiles + i) % kTcMarks] >> (4 * half) & 15;
                 if (warp_ok) {
                     uint32_t v0[32], v1[32];
@@ -600,16 +608,16 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             tc_fence_after();
             // nq = 2: this thread's row, all values; nq = 1: both streams hold the row, this thread takes half of its values
             float w0 = 1.f, w1 = 0.f, mt = top, l = sum;
-            const bool both = w.nq == 1;
-            if (w.nq == 1) {
+            const bool both = !G::SINGLE && w.nq == 1;
+            if (both) {
                 const float m0 = ml[r * 2], l0 = ml[r * 2 + 1], m1 = ml[(kTcHalf + r) * 2], l1 = ml[(kTcHalf + r) * 2 + 1];
                 mt = fmaxf(m0, m1);
                 w0 = m0 == mt ? 1.f : ex2(m0 - mt);
                 w1 = m1 == mt ? 1.f : ex2(m1 - mt);
                 l = w0 * l0 + w1 * l1;
             }
-            const uint32_t ta = lanes + G::O0 + (w.nq == 2 ? 128 * st : 0);
-            const int x0 = w.nq == 2 ? 0 : st * (D / 2), x1 = w.nq == 2 ? D : x0 + D / 2;
+            const uint32_t ta = lanes + G::O0 + (both ? 0 : 128 * st);
+            const int x0 = both ? st * (D / 2) : 0, x1 = both ? x0 + D / 2 : D;
             const bool marked = nan_mark[pieces % kTcMarks] == (uint32_t)pieces + 1;
             const int64_t slot = attn_slot_row<1>(blockIdx.x, w.c0, 0);
             if (warp_ok) {
@@ -632,7 +640,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     }
                     if (marked) {
                         // infinities and NaN among the new tokens of this piece
-                        const int a = max(w.s.ctx, w.tile0 * kTcTile), e = min(w.s.len, (w.tile0 + w.n) * kTcTile);
+                        const int a = max(w.s.ctx, w.tile0 * G::TT), e = min(w.s.len, (w.tile0 + w.n) * G::TT);
 #pragma unroll 1
                         for (int t = a; t < e; t++) {
                             const int page = p.table[(int64_t)w.s.b * p.max_pages + (t >> p.cache.lp)];
@@ -678,7 +686,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             // the whole warp walks the steps, so that operands stay in uniform registers; one lane issues
             constexpr uint32_t TYPE = BF ? 1u : 0u;
             constexpr uint32_t IDESC = (1u << 4) | (TYPE << 7) | (TYPE << 10) | ((uint32_t)(kTcHalf >> 4) << 24);
-            constexpr uint32_t IDESC_S = IDESC | ((uint32_t)(kTcTile >> 3) << 17), IDESC_S64 = IDESC | (64u >> 3 << 17);
+            constexpr uint32_t IDESC_S = IDESC | ((uint32_t)(G::TT >> 3) << 17), IDESC_S64 = IDESC | (64u >> 3 << 17);
             constexpr uint32_t IDESC_O = IDESC | ((uint32_t)(D >> 3) << 17) | (1u << 16);     // B N-major
             const uint64_t k_desc = sw128_desc(sb), v_desc = sw128_desc_mn(sb, G::HALF);
             const bool one = elect_one();
@@ -697,8 +705,8 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     if (!two) {
 #pragma unroll
                         for (int i = 0; i < D / 16; i++) {
-                            const uint32_t o = ((i >> 2) * G::HALF + (i & 3) * 32) >> 4;
-                            umma_f16_ss(ds, k_desc + (uint32_t)((G::OFF_Q >> 4) + o), k + o, IDESC_S, i > 0);
+                            const uint32_t o = ((i >> 2) * G::HALF + (i & 3) * 32) >> 4, oq = ((i >> 2) * G::QHALF + (i & 3) * 32) >> 4;
+                            umma_f16_ss(ds, k_desc + (uint32_t)((G::OFF_Q >> 4) + oq), k + o, IDESC_S, i > 0);
                         }
                     } else {
                         const uint64_t kh = k + (uint32_t)((m & 1) * (64 * 128 >> 4));
@@ -707,7 +715,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
 #pragma unroll
                             for (int i = 0; i < D / 16; i++) {
                                 const uint32_t o = ((i >> 2) * G::HALF + (i & 3) * 32) >> 4;
-                                umma_f16_ss(ds + 64 * s, k_desc + (uint32_t)(((G::OFF_Q + s * G::TILE) >> 4) + o), kh + o, IDESC_S64, i > 0);
+                                umma_f16_ss(ds + 64 * s, k_desc + (uint32_t)(((G::OFF_Q + s * G::QTILE) >> 4) + o), kh + o, IDESC_S64, i > 0);
                             }
                     }
                 };
@@ -748,7 +756,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     if (one) {
                         const uint64_t v = v_desc + (uint32_t)((G::OFF_RING + slot_v * G::TILE) >> 4);
 #pragma unroll
-                        for (int s = 0; s < 2; s++) {
+                        for (int s = 0; s < G::STREAMS; s++) {
                             const uint64_t vs = v + (uint32_t)((two ? m & 1 : s) * (64 * 128 >> 4));   // 64 tokens on
 #pragma unroll
                             for (int i = 0; i < 4; i++)
@@ -775,7 +783,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             // values: a box costs its warp about 100 cycles (16 of them, codes and scales of 16-token pages, 2000 per side).
             // Who waits for a slot's phase has seen the one before, as slots are emptied in the order of the positions.
             const int side = warp == kTcValueWarp;
-            const int box = min(1 << p.cache.lp, kTcTile), boxes = kTcTile / box;
+            const int box = min(1 << p.cache.lp, G::TT), boxes = G::TT / box;
             struct Tile {
                 int64_t row;            // this lane's box: its first cached row
                 bool have;              // ... which exists
@@ -795,18 +803,18 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     if (lane == 0) {
                         // tokens present, first new one (values only), page marks, mark of the piece
                         *reinterpret_cast<int4 *>(smem + G::OFF_SIDES + 16 * slot) =
-                            make_int4(q.len, side ? q.ctx : kTcTile, (int)q.dead, q.mark);
+                            make_int4(q.len, side ? q.ctx : G::TT, (int)q.dead, q.mark);
                         mbar_arrive_expect_tx(bar_rawf(slot), __popc(q.valid) * box * (G::RB + 2 * G::NB));
                     }
                     __syncwarp();
                     if (q.have) {
                         bulk_g2s(dst + lane * box * G::RB, (side ? p.cache.v : p.cache.k) + q.row * G::RB, box * G::RB, bar_rawf(slot));
-                        bulk_g2s(dst + kTcTile * G::RB + lane * box * 2 * G::NB,
+                        bulk_g2s(dst + G::TT * G::RB + lane * box * 2 * G::NB,
                                  (side ? p.cache.v_scale : p.cache.k_scale) + q.row * G::NB, box * 2 * G::NB, bar_rawf(slot));
                     }
                 } else {
                     const uint32_t dst = sb + G::OFF_RING + slot * G::TILE;
-                    const bool fix = side && (q.ctx < kTcTile || q.dead);
+                    const bool fix = side && (q.ctx < G::TT || q.dead);
                     const uint32_t bar = fix ? bar_land : bar_full(slot);
                     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(q.valid) * box * G::HALVES * 128);
                     __syncwarp();
@@ -818,12 +826,12 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                         // zeros behind the end and where there is no page; new tokens' infinities and NaN out, and marked
                         if (!(ok = wait(bar_land, lands++ & 1))) return;
                         bool hit = false;
-                        constexpr int N = 4;                                 // chunks at a time (kTcTile * D / 8 is a multiple of 32 N)
+                        constexpr int N = 4;                                 // chunks at a time (G::TT * D / 8 is a multiple of 32 N)
 #pragma unroll 1
-                        for (int i0 = (q.dead ? 0 : q.ctx) * (D / 8) / (32 * N) * (32 * N) + lane; i0 < kTcTile * (D / 8); i0 += 32 * N) {
+                        for (int i0 = (q.dead ? 0 : q.ctx) * (D / 8) / (32 * N) * (32 * N) + lane; i0 < G::TT * (D / 8); i0 += 32 * N) {
                             uint4 v[N];
 #pragma unroll
-                            for (int n = 0; n < N; n++) v[n] = lds128(dst + tc_chunk((i0 + 32 * n) / (D / 8), (i0 + 32 * n) % (D / 8)));
+                            for (int n = 0; n < N; n++) v[n] = lds128(dst + tc_chunk<G::TT>((i0 + 32 * n) / (D / 8), (i0 + 32 * n) % (D / 8)));
 #pragma unroll
                             for (int n = 0; n < N; n++) {
                                 const int r = (i0 + 32 * n) / (D / 8), c = (i0 + 32 * n) % (D / 8);
@@ -838,7 +846,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                                         if ((u[y] & 0x7f800000u) == 0x7f800000u) { u[y] &= 0xffffu; any = hit = true; }
                                     }
                                 }
-                                if (any) sts128(dst + tc_chunk(r, c), make_uint4(u[0], u[1], u[2], u[3]));
+                                if (any) sts128(dst + tc_chunk<G::TT>(r, c), make_uint4(u[0], u[1], u[2], u[3]));
                             }
                         }
                         if (hit) nan_mark[(q.mark - 1) % kTcMarks] = (uint32_t)q.mark;
@@ -851,22 +859,22 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             while (ok && next()) {
                 const int32_t *table = p.table + (int64_t)w.s.b * p.max_pages;
                 auto page_of = [&](int t) {
-                    const int tok = t * kTcTile + lane * box;
+                    const int tok = t * G::TT + lane * box;
                     return (lane < boxes && tok < w.s.len) ? table[tok >> p.cache.lp] : -2;
                 };
                 int next_page = page_of(w.tile0);
                 for (int t = w.tile0; t < w.tile0 + w.n && ok; t++) {
-                    const int page = next_page, tok = t * kTcTile + lane * box;
+                    const int page = next_page, tok = t * G::TT + lane * box;
                     if (t + 1 < w.tile0 + w.n) next_page = page_of(t + 1);
                     Tile q;
                     q.have = page >= 0 && page < p.cache.n_pages;
                     q.row = q.have ? (((int64_t)page * p.cache.n_kv + w.h) << p.cache.lp) + (tok & ((1 << p.cache.lp) - 1)) : 0;
                     q.valid = __ballot_sync(0xffffffffu, q.have);
                     // strip i lies in box 16 i / box
-                    q.dead = __ballot_sync(0xffffffffu, lane < 8 && t * kTcTile + 16 * lane < w.s.len &&
+                    q.dead = __ballot_sync(0xffffffffu, lane < G::TT / 16 && t * G::TT + 16 * lane < w.s.len &&
                                                             !((q.valid >> (16 * (lane & 7) / box)) & 1));
-                    q.ctx = min(max(0, w.s.ctx - t * kTcTile), kTcTile);
-                    q.len = min(w.s.len - t * kTcTile, kTcTile);
+                    q.ctx = min(max(0, w.s.ctx - t * G::TT), G::TT);
+                    q.len = min(w.s.len - t * G::TT, G::TT);
                     q.mark = pieces + 1;
                     if (side == 0 && lane == 0) {
                         dead_strips[(tiles + t - w.tile0) % kTcMarks] = (uint8_t)q.dead;
@@ -886,7 +894,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             // ---------------- the pieces, for all roles ----------------
             // one copy of this code: a CTA's first microseconds are mostly spent on fetching instructions
             int bad = 0;
-            TcWork<G::NQ> work;
+            TcWork<G::NQ, G::TT> work;
             work.init(p, lane, bad);
             if (bad && blockIdx.x == 0) atomicOr(error, bad);
             for (int i = 0; ok; i++) {
@@ -926,7 +934,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 const uint32_t dst = sb + G::OFF_RING + slot * G::TILE;
                 const uint8_t *src = smem + G::OFF_RAW + rs * G::RAW;
                 constexpr int M = G::CHUNKS / 256;
-                const bool plain = side.x >= kTcTile && side.y >= kTcTile && side.z == 0;
+                const bool plain = side.x >= G::TT && side.y >= G::TT && side.z == 0;
                 bool hit = false;
                 // STEP is a multiple of 8: a thread's chunks have the same place in their rows' swizzle.  Chunks of a row's
                 // second 64 values are stored in the other order: distinct banks
@@ -935,13 +943,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 const int f = FMT == BQG_Q8_0 ? (c >> 2) & 1 : (c >> 1) & 1;
                 uint32_t at[OUT];
 #pragma unroll
-                for (int k = 0; k < OUT; k++) at[k] = dst + tc_chunk(r0, OUT * c + (k ^ (f * (OUT / 2))));
+                for (int k = 0; k < OUT; k++) at[k] = dst + tc_chunk<G::TT>(r0, OUT * c + (k ^ (f * (OUT / 2))));
                 uint4 codes[M];
                 uint32_t scale[M];
 #pragma unroll
                 for (int i = 0; i < M; i++) {
                     codes[i] = *reinterpret_cast<const uint4 *>(src + (i * 256 + lt) * 16);
-                    scale[i] = *reinterpret_cast<const uint16_t *>(src + kTcTile * G::RB + ((r0 + i * STEP) * G::NB
+                    scale[i] = *reinterpret_cast<const uint16_t *>(src + G::TT * G::RB + ((r0 + i * STEP) * G::NB
                                                                                            + (FMT == BQG_Q8_0 ? c >> 1 : c)) * 2);
                 }
                 if (!plain) {
