@@ -3,14 +3,14 @@
 //   out[i, h] = sum_j p_j v_j,   p = softmax over the visible j of scale * q[i, h] . k_j
 //
 // The rows that share a KV head (new tokens x query heads of the group)
-// share its keys and values, so a unit of work is (sequence, KV head, row
-// tile, 64 cached tokens), and the floor is reading every cached row once:
-// with few rows the kernel streams.
+// share its keys and values, so a unit of work is (sequence, KV head, 64 cached
+// tokens), and the floor is reading every cached row once: with few rows the
+// kernel streams.  (At most 16 rows: more go to bqg_attn_tc.cuh.)
 //
 //  * Work is split evenly: the units of all sequences in one line (with a few of no work where a set begins, see
 //    attn_kernel), each CTA a contiguous range of them, so ragged lengths and few (sequence, head)
 //    pairs fill the GPU alike.  A range that begins or ends inside a
-//    (sequence, head, row tile) leaves a partial result (maximum, sum,
+//    (sequence, head) leaves a partial result (maximum, sum,
 //    unnormalised output rows) in the workspace; the CTA whose counted
 //    arrival completes the set joins it, in the order of the ranges, so the
 //    bits do not depend on timing.
@@ -346,15 +346,11 @@ template <int FMT, int D, int RT> struct AttnKernel {
     static constexpr float kShift = BF ? 0.0f : 8.0f;
     static constexpr int MT = D / 16;                         // M tiles of the second product
 
-    // 64-token tiles and row tiles of a sequence, and its units.
+    // 64-token tiles of a sequence, and its units: all its rows (new tokens x heads of a group, at most ROWS) at once.
     static __device__ __forceinline__ int tiles_of(const AttnSeq &s) { return (s.len + kUnit - 1) / kUnit; }
-    static __device__ __forceinline__ int row_tiles_of(const AttnParams &p, const AttnSeq &s)
-    {
-        return (s.T * p.group + G::ROWS - 1) / G::ROWS;
-    }
     static __device__ __forceinline__ int64_t units(const AttnParams &p, const AttnSeq &s, int lead)
     {
-        return (int64_t)p.cache.n_kv * row_tiles_of(p, s) * (tiles_of(s) + lead);
+        return s.T ? (int64_t)p.cache.n_kv * (tiles_of(s) + lead) : 0;
     }
 
     // The queries of rows row0 .. row0 + 7 as they lie (this lane: row lane / 4).  The order of the
@@ -693,14 +689,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
     pdl_wait();
     pdl_launch_dependents();
 
-    // This CTA's range of units.  Where there may be half as many sets (sequence, KV head, row tile) as CTAs, CTAs
+    // This CTA's range of units.  Where there may be half as many sets (sequence, KV head) as CTAs, CTAs
     // with several sets' pieces would be last: a piece's start and end cost 3 to 4 us, so each set begins with
     // kLead units that are no work.  Measured over 2 to 200 sequences of 60 to 3000 tokens, 8 KV heads, q8_0 and bf16, against none:
     // with 2 on average 0.94 of the time, at most 1.05 (200 of 1000 tokens, bf16: 91 us against 103); with 4 0.95, but up to 1.33
     // for short contexts.  With fewer sets a CTA has one piece or is near it, and its range is better left as it is.
     int bad = 0;
-    const int64_t sets = (int64_t)p.n_seq * p.cache.n_kv * ((p.max_q * p.group + G::ROWS - 1) / G::ROWS);
-    const int lead = 2 * sets >= gridDim.x ? kLead : 0;
+    const int lead = 2 * (int64_t)p.n_seq * p.cache.n_kv >= gridDim.x ? kLead : 0;
     auto weight = [&](const AttnSeq &q) { return A::units(p, q, lead); };
     int64_t mine;
     AttnSeq s;
@@ -720,17 +715,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
             s = attn_seq(p, s.b + 1, bad);
         }
         const int64_t off = u - base;
-        const int tiles = A::tiles_of(s), row_tiles = A::row_tiles_of(p, s);
-        const int pair = (int)div_pos(off, tiles + lead), first = (int)(off - (int64_t)pair * (tiles + lead));
+        const int tiles = A::tiles_of(s);
+        const int h = (int)div_pos(off, tiles + lead), first = (int)(off - (int64_t)h * (tiles + lead));
         const int take = (int)min((int64_t)(tiles + lead - first), u_end - u);
-        const int h = pair / row_tiles, row0 = (pair - h * row_tiles) * G::ROWS;
         const int tile0 = max(first - lead, 0), n = first + take - lead - tile0;   // units of this piece
         if (n <= 0) {
             u += take;
             continue;
         }
-        const int64_t seg0 = u - first + lead;                                // first unit of the whole (sequence, head, row tile)
-        const int rows = min(G::ROWS, s.T * p.group - row0);
+        const int64_t seg0 = u - first + lead;                                // first unit of the whole (sequence, head)
+        const int rows = s.T * p.group;
 
         // strips of this warp: tokens 64 (tile0 + j) + 16 warp ..
         const uint32_t ring = sb + warp * S * G::STAGE;
@@ -746,9 +740,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
         typename A::RawQ raw[G::QREG ? RT : 1];
         if constexpr (G::QREG) {
 #pragma unroll
-            for (int m = 0; m < RT; m++) A::fetch_q(p, s, h, row0 + 8 * m, lane, raw[m]);
+            for (int m = 0; m < RT; m++) A::fetch_q(p, s, h, 8 * m, lane, raw[m]);
         } else if (warp < RT) {
-            A::fetch_q(p, s, h, row0 + 8 * warp, lane, raw[0]);
+            A::fetch_q(p, s, h, 8 * warp, lane, raw[0]);
         }
         unsigned valid = 0;                                                   // stages whose page is in the cache
         auto issue = [&](int j, int st) {
@@ -800,7 +794,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                 }
             }
         }
-        if (tid < G::ROWS) row_sees[tid] = attn_sees(p, s, row0 + tid);
+        if (tid < G::ROWS) row_sees[tid] = attn_sees(p, s, tid);
         __syncthreads();
         float rs[RT][2];                                                      // rows 8 m + 2 t, + 1
         float o[RT][MT][4], top[RT][2], sum[RT][2], from[RT][2];              // from: what the exponents are relative to
@@ -940,7 +934,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
         constexpr int E = D / 32;                                             // values per lane of a row
         float *const part_ml = p.part + (int64_t)2 * gridDim.x * G::ROWS * D;
         auto out_row = [&](int row) {
-            const int i = (row0 + row) / p.group, hh = row0 + row - i * p.group;
+            const int i = row / p.group, hh = row - i * p.group;
             return p.out + ((int64_t)(s.q0 + i) * p.n_q + h * p.group + hh) * D + lane * E;
         };
         // rows of `merged`, the warps' results joined: into the output, or the workspace

@@ -36,12 +36,15 @@ inline cudaError_t take_error(int &word, int *out)
     return cudaSuccess;
 }
 
-// Rows from which the tcgen05 kernel serves a call of head_dim 64 or 128.  Measured with 4 heads on each of 8 KV heads
-// of 128 values, 1 to 64 sequences of 200 to 40,000 tokens, each kernel's time over the mma.sync kernel's:
-// 12 and 16 rows (two of its row tiles) 0.6 to 1.4 for bf16, but 0.9 to 2.1 for q8_0 and q4_0; 24 and 32 rows (with
-// four row tiles) 0.4 to 1.1 for bf16 and 0.6 to 1.3 for the quantized formats, above 1.05 only for 64
-// sequences of up to 1500 tokens.
-constexpr int kAttnTcRows = 17;
+// Rows from which the tcgen05 kernel serves a call; below, the mma.sync kernel.  Measured with 4 heads on each of 8 KV
+// heads, its time over the other's:
+//  * 64 and 128 values, 1 to 64 sequences of 200 to 40,000 tokens: 12 and 16 rows 0.6 to 1.4 for bf16, but 0.9 to 2.1 for
+//    q8_0 and q4_0; 24 and 32 rows (mma.sync with four row tiles) 0.4 to 1.1 for bf16 and 0.6 to 1.3 for the quantized
+//    formats, above 1.05 only for 64 sequences of up to 1500 tokens;
+//  * 256 values, 1 to 40 sequences of 300 to 12,000: 12 and 16 rows 0.4 to 1.1 for bf16, but 0.7 to 1.75 for q8_0 and q4_0;
+//    24 and 32 rows (mma.sync in two turns) 0.5 to 0.9 for bf16 and 0.6 to 1.4 for the quantized formats, less the more
+//    rows: 64 rows 0.4 and 0.5.
+template <int FMT, int D> constexpr int kAttnTcRows = FMT == BQG_BF16 && D == 256 ? 9 : 17;
 
 inline void attn_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int threads, int smem, cudaStream_t s,
                         bool pdl)
@@ -153,16 +156,15 @@ template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, Att
     return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D, G::ROWS>, p, grid);
 }
 
-// The mma.sync kernel with one or two row tiles of 8 (more rows are taken in turn: head_dim 256 only).
-template <int FMT, int D> cudaError_t attn_rows_pick(const AttnParams &p, int rows, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+template <int FMT, int D> cudaError_t attn_pick(const AttnParams &p, int rows, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
     if (rows <= 8) return attn_rows_call<FMT, D, 1>(p, error, plan, s, pdl);
-    return attn_rows_call<FMT, D, 2>(p, error, plan, s, pdl);
+    if constexpr (kAttnTcRows<FMT, D> > 9)
+        if (rows < kAttnTcRows<FMT, D>) return attn_rows_call<FMT, D, 2>(p, error, plan, s, pdl);
+    return attn_tc_call<FMT, D>(p, error, plan, s, pdl);
 }
 
-// rows: the most rows (new tokens x heads of a group) of any sequence.  Few
-// on mma.sync; more on tcgen05 for head_dim 64 and 128 (at 256
-// two streams' accumulators do not fit in tensor memory).
+// rows: the most rows (new tokens x heads of a group) of any sequence.
 template <int FMT>
 cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
@@ -180,10 +182,9 @@ cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, A
         }
         error = static_cast<int *>(word);
     }
-    const bool tc = rows >= kAttnTcRows;
-    if (D == 64) return tc ? attn_tc_call<FMT, 64>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 64>(p, rows, error, plan, s, pdl);
-    if (D == 128) return tc ? attn_tc_call<FMT, 128>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 128>(p, rows, error, plan, s, pdl);
-    return tc ? attn_tc_call<FMT, 256>(p, error, plan, s, pdl) : attn_rows_pick<FMT, 256>(p, rows, error, plan, s, pdl);
+    if (D == 64) return attn_pick<FMT, 64>(p, rows, error, plan, s, pdl);
+    if (D == 128) return attn_pick<FMT, 128>(p, rows, error, plan, s, pdl);
+    return attn_pick<FMT, 256>(p, rows, error, plan, s, pdl);
 }
 
 }  // namespace bqg

@@ -17,6 +17,8 @@
 //    run under the softmax of this one (one buffer of 128 tokens per stream
 //    left both waiting for each other's latency: 4240 cycles per 128 tokens
 //    x 256 rows, 2048 of them products).
+//  * head_dim 256 leaves room for one stream of 128 rows (256 columns of O, two buffers of 64 scores), so a tile is 64 tokens
+//    and one step, and warps 4-7 have nothing to do.
 //  * Warps 0-3 and 4-7: softmax of stream 0 and 1, one row per thread, its 64 scores
 //    in registers.  The running maximum is raised only when exceeded by kSlack
 //    (see bqg_attn.cuh), and only then is O rescaled, after the products so far.
@@ -40,7 +42,8 @@
 //    64 tokens x 256 rows takes 2000 cycles, 1400 of them products (N = 64: each MMA reads its 128 x 16 of Q, 56 cycles
 //    instead of 32).  q8_0, 8 x 5000, 13 new, 4 heads on each of 8: 34.5 us: 7 until the first scores, 1.4 per tile of
 //    128 tokens (building its two sides, 1100 to 1300 cycles each), 2 for the results, 3 for the join.  Two
-//    teams of builders, one per side, took 34 % longer.
+//    teams of builders, one per side, took 34 % longer.  head_dim 256, 8 x 4000, 64 new: bf16 84 us, q8_0 98 (mma.sync in
+//    16 turns of 16 rows: 270, 276).
 //
 // A drafted token's infinite or NaN value must not reach rows that do not see
 // it, and 0 x NaN in the product would.  In tiles that hold new tokens zeros
