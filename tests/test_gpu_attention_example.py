@@ -62,3 +62,22 @@ def test_the_kept_path_is_what_the_tree_held():
             step = x.abs().unflatten(-1, (-1, 32)).amax(-1, keepdim=True) / 127
             limit = (step * (0.5 + 127 * 2.0 ** -11)).expand(*step.shape[:-1], 32).flatten(-2)
             assert ((x - y).abs() <= limit * 1.001).all()
+
+
+@pytest.mark.parametrize("fmt", [bqg.BF16, bqg.Q4_0])
+@pytest.mark.parametrize("head_dim,kv_heads", [(128, 2), (256, 1), (64, 1)])
+def test_dependent_launches_change_nothing(fmt, head_dim, kv_heads):
+    """Programmatic dependent launch on: each kernel starts under the one before it and waits; the bits are the same."""
+    mod = example()
+    got = []
+    for on in (False, True):
+        block = mod.AttentionBlock(fmt=fmt, head_dim=head_dim, kv_heads=kv_heads, seed=3)
+        was = bqg.set_pdl(on)
+        try:
+            got.append([mod.run(block).clone() for _ in range(3)])
+            torch.cuda.synchronize()
+        finally:
+            bqg.set_pdl(was)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bqg.last_device_error() == 0
