@@ -32,8 +32,8 @@
 //    12-19 build the tile: codes as fp16 integers (bqg_attn.cuh), times the
 //    block's scale: one rounding (relative 2^-12, for keys too: a block's scale
 //    cannot be applied behind a product that sums over all blocks).
-//  * Tiles are shared out evenly over the CTAs as in bqg_attn.cuh, a tile of two
-//    halves counting twice.  Sets of tiles that several CTAs share leave partial
+//  * Tiles are shared out over the CTAs, a tile of two halves counting twice: one piece for each, or even
+//    ranges (see TcWork).  Sets of tiles that several CTAs share leave partial
 //    results, which a second, small launch joins: with up to 256 rows of
 //    them, the CTA that came last took longer for it than the whole GPU does.
 //  * Every wait is bounded; one that gives up sets the error word, and the
