@@ -184,7 +184,7 @@ template <int NQ, int TT> struct TcWork {
             for (int b = lane + 32; b < p.n_seq; b += 32) n += p.cache.n_kv * pieces(p, attn_seq(p, b, ignored), m).head;
             return __reduce_add_sync(0xffffffffu, n);
         };
-        if (total < (1 << 28)) {
+        if (total < (1 << 28) && (int64_t)p.n_seq * p.cache.n_kv <= gridDim.x) {
             int lo = ((int)per + NQ - 1) / NQ - 1, hi = ((int)per + kTcSecond<NQ>) / NQ;      // too small; enough, if any is
             if (count(hi * NQ) <= gridDim.x) {
                 while (hi - lo > 1) {
