@@ -161,6 +161,15 @@ template <int CPT> __device__ __forceinline__ uint32_t chunk_at(int tok, int c)
     return (uint32_t)(tok * CPT + (c ^ f)) * 16;
 }
 
+// Whether one of 16-bit words w's two scales may take a code past fp16's range (65504), or is an infinity or NaN: from
+// 512 (q8_0, |code| <= 128) or 8192 (q4_0, |code| <= 8) on, which is these exponent bits set.
+template <int FMT> constexpr uint32_t kWideScale = FMT == BQG_Q8_0 ? 0x6000u : 0x7000u;
+template <int FMT> __device__ __forceinline__ bool any_wide_scale(uint32_t w)
+{
+    constexpr uint32_t lo = kWideScale<FMT>, hi = lo << 16;
+    return (w & lo) == lo || (w & hi) == hi;
+}
+
 // One sequence as the kernels work on it.
 struct AttnSeq {
     int b, q0, T, ctx, len;      // first query token, new tokens, context and all cached tokens
@@ -636,7 +645,7 @@ template <int FMT, int D, int RT> struct AttnKernel {
             else return (float)((int)((dim % QK < 16 ? w : w >> 4) & 15u) - 8) * d;
         }
     }
-    // Some value of the staged strip is an infinity or NaN (the same answer in every lane).
+    // Some value of the staged strip may be an infinity or NaN, as it is or in fp16 (the same answer in every lane).
     static __device__ __forceinline__ bool any_nonfinite(uint32_t st, int lane)
     {
         bool bad = false;
@@ -650,7 +659,7 @@ template <int FMT, int D, int RT> struct AttnKernel {
 #pragma unroll 1
             for (int i = lane; i < G::SCALES / 4; i += 32) {
                 const uint32_t w = lds32(st + 2 * kStrip * G::RB + G::SCALES + 4 * i);
-                bad |= (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+                bad |= any_wide_scale<FMT>(w);
             }
         }
         return __any_sync(0xffffffffu, bad);
@@ -879,8 +888,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                 pb[m][0] = transpose8x8(pack2<A::BF>(e[0], e[1]));
                 pb[m][1] = transpose8x8(pack2<A::BF>(e[2], e[3]));
                 if (exact) {
-                    // an infinity or NaN among tokens that some rows do not see: 0 x inf must
-                    // not reach them, so this strip's products are taken one by one in fp32
+                    // an infinity or NaN (or a value that is one in fp16) among tokens that some rows do not see:
+                    // 0 x inf must not reach them, so this strip's products are taken one by one in fp32
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; i++) pw[(8 * (i >> 1) + g) * 8 + 2 * t + (i & 1)] = sc[m][i] == NEG ? -1.f : e[i];

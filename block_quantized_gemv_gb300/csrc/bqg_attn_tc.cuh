@@ -45,10 +45,10 @@
 //    teams of builders, one per side, took 34 % longer.  head_dim 256, 8 x 4000, 64 new: bf16 84 us, q8_0 98 (mma.sync in
 //    16 turns of 16 rows: 270, 276).
 //
-// A drafted token's infinite or NaN value must not reach rows that do not see
-// it, and 0 x NaN in the product would.  In tiles that hold new tokens zeros
+// A drafted token's infinite or NaN value, or one beyond fp16's range, must not reach rows that do not see
+// it, and 0 x NaN or 0 x inf in the product would.  In tiles that hold new tokens zeros
 // are stored for such values and the piece is marked; the rows that see the
-// token add them (infinities and NaN stay what they are) when they are written.
+// token add them (infinities and NaN stay what they are, what fp16 cannot hold is an infinity) when they are written.
 #pragma once
 
 #include <cuda.h>
@@ -342,7 +342,7 @@ template <int ROWS> __device__ __forceinline__ uint32_t tc_chunk(int r, int c)
     return (uint32_t)((c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Value `dim` of cached row `row`, as far as it is an infinity or NaN; 0 otherwise.
+// Value `dim` of cached row `row`, as far as it is an infinity or NaN in the products' type; 0 otherwise.
 template <int FMT, int D> __device__ float tc_nonfinite(const KvCacheDev &c, int64_t row, int dim)
 {
     float f;
@@ -357,7 +357,8 @@ template <int FMT, int D> __device__ float tc_nonfinite(const KvCacheDev &c, int
             f = (float)((dim % QK < 16 ? byte & 15 : byte >> 4) - 8) * d;
         }
     }
-    return isfinite(f) ? 0.f : f;
+    if constexpr (FMT == BQG_BF16) return isfinite(f) ? 0.f : f;
+    else return fabsf(f) < 65520.f ? 0.f : f * __int_as_float(0x7f800000);    // 65520 and above round to an infinity in fp16
 }
 
 // Partial results of a piece: values in groups of four, [slot][D / 4][rows][4] (a warp's 32 rows are then
@@ -956,12 +957,12 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                                                                                            + (FMT == BQG_Q8_0 ? c >> 1 : c)) * 2);
                 }
                 if (!plain) {
-                    // no token: zeros; a new token's infinite or NaN scale: zeros, and marked
+                    // no token: zeros; a new token's scale that may leave fp16's range: its values are looked at below, and the piece marked
 #pragma unroll
                     for (int i = 0; i < M; i++) {
                         const int r = r0 + i * STEP;
                         if (r >= side.x || ((side.z >> (r >> 4)) & 1)) scale[i] = 0;
-                        if (r >= side.y && (scale[i] & 0x7c00u) == 0x7c00u) { scale[i] = 0; hit = true; }
+                        if (r >= side.y && any_wide_scale<FMT>(scale[i])) hit = true;
                     }
                 }
 #pragma unroll
@@ -996,7 +997,27 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                         }
                     }
                 }
-                if (hit) nan_mark[(side.w - 1) % kTcMarks] = (uint32_t)side.w;
+                if (hit) {
+                    // of the new tokens' values, zeros for the infinities and NaN (this thread's chunks, as it stored them)
+                    const volatile int *const again = reinterpret_cast<const volatile int *>(smem + G::OFF_SIDES + 16 * rs);
+#pragma unroll 1
+                    for (int i = 0; i < M; i++) {
+                        if (r0 + i * STEP < again[1]) continue;
+#pragma unroll 1
+                        for (int k = 0; k < OUT; k++) {
+                            const uint32_t chunk = dst + tc_chunk<G::TT>(r0 + i * STEP, OUT * c + k);
+                            const uint4 v = lds128(chunk);
+                            uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int y = 0; y < 4; y++) {
+                                if ((u[y] & 0x7c00u) == 0x7c00u) u[y] &= 0xffff0000u;
+                                if ((u[y] & 0x7c000000u) == 0x7c000000u) u[y] &= 0xffffu;
+                            }
+                            sts128(chunk, make_uint4(u[0], u[1], u[2], u[3]));
+                        }
+                    }
+                    nan_mark[(again[3] - 1) % kTcMarks] = (uint32_t)again[3];
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {

@@ -369,7 +369,8 @@ int bqg_kv_read(const bqg_kv_cache *cache, const int64_t *slots, int64_t T, int 
  * Keys and values enter the products as they are (bf16), or (quantized) values as q d rounded
  * once to fp16 (relative 2^-12), and keys as their integer codes, whose block sums are scaled in fp32, where
  * max_q * n_q / n_kv is at most 16, as q d rounded once to fp16 otherwise.  So
- * quantized keys and values beyond fp16's range (65504) are out of range here.  A quantized call's queries
+ * quantized keys and values beyond fp16's range (65504) are out of range here: a query that sees one may get
+ * infinities, one that does not see it is not touched by it either.  A quantized call's queries
  * are scaled per row by a power of two and rounded to fp16: a value below 2^-16 of its row's largest loses bits.
  * Scores, softmax sums and outputs accumulate in fp32; the probabilities are
  * rounded to the values' type (bf16 or fp16) for the second product; in fp16
