@@ -285,6 +285,24 @@ __device__ __forceinline__ void encode_rows(const F2 (&y)[2][D / 32], int rows, 
                 dh = __float2half_rn(__fdiv_rn(first, -8.0f));
                 d = __half2float(dh);
             }
+            // The maxima pass over a NaN, and its code would be an ordinary one: a block that holds one has a NaN for its scale.
+            // (q8_0 comes here 16 times as often as q4_0, which looks without asking: 8192 tokens of 8 heads 27.0 us with the
+            // question and 27.9 without, q4_0 28.6 and 28.2.)
+            if (!Q8 || __any_sync(0xffffffffu, isnan(near))) {
+                bool nan = false;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    bool has = false;
+#pragma unroll
+                    for (int e = 0; e < E; e++) has |= isnan(value(j, e));
+                    const unsigned lanes = __ballot_sync(0xffffffffu, has) >> (lane & ~(LB - 1));
+                    if (j == 2 * up + up2) nan = lanes & ((1u << LB) - 1);
+                }
+                if (nan) {
+                    dh = __ushort_as_half(0x7fff);
+                    d = __half2float(dh);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const float dj = __shfl_sync(0xffffffffu, d, (lane & ~(LB - 1)) + (j >> 1) * (LB / 2) + (j & 1) * (LB / 4));

@@ -282,7 +282,8 @@ int bqg_decode_layer_q4_0_q8_1(const void *xa, const void *xb, int x_dtype, cons
  *                    holding value j in its low nibble, j + 16 in its high)
  *   k_scale, v_scale [n_pages][n_kv][page_size][head_dim / 32] fp16 block
  *                    scales; ignored for BQG_BF16
- * with the value formulas and rounding rules of the block formats above.
+ * with the value formulas and rounding rules of the block formats above; a block
+ * with a NaN among its values is stored with a NaN scale, so all of it reads as NaN.
  * head_dim 64, 128 or 256; page_size a power of two from 16 to 4096;
  * n_pages * page_size at most 2^40.  The struct is read on the host during the call; the arrays are
  * device memory, 16-byte aligned.  A token's place ("slot") is

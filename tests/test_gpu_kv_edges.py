@@ -1,0 +1,50 @@
+"""The cache's writer where a token is broken."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_gemv_gb300 as bqg
+from block_quantized_gemv_gb300 import build as bqg_build
+from test_gpu_kv_cache import arrays, filled_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    bqg_build.build()
+
+
+@pytest.mark.parametrize("fmt", [bqg.Q8_0, bqg.Q4_0])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_block_with_a_nan_reads_as_nan(fmt, D, dtype):
+    """Wherever in the block it is, and whatever else is there; the other blocks are what they are without it."""
+    n_kv, page, T = 7, 32, 64
+    rng = np.random.default_rng(D)
+    clean = rng.standard_normal((T, n_kv, D), dtype=np.float32)
+    clean[40, :, ::5], clean[41] = np.inf, 0.0
+    clean[42, :, ::2], clean[42, :, 1::2] = -3.0, 3.0
+    x = clean.copy()
+    block = np.zeros((T, n_kv, D // 32), dtype=bool)
+    for t in range(T):
+        h, b = t % n_kv, t % (D // 32)
+        x[t, h, 32 * b + t % 32] = np.nan
+        block[t, h, b] = True
+    x[7, 0, :32], block[7, 0, 0] = np.nan, True
+    got = {}
+    slots = torch.arange(T, device="cuda")
+    for name, a in (("clean", clean), ("x", x)):
+        cache = filled_cache(fmt, T // page, n_kv, page, D)
+        key = torch.from_numpy(a).to(dtype).cuda()
+        bqg.kv_write(key, key.flip(0).contiguous(), slots, cache)
+        got[name] = arrays(cache), bqg.kv_read(cache, slots, dtype=torch.float32)
+    for i, side in enumerate("kv"):
+        hit = torch.from_numpy(block if side == "k" else block[::-1].copy())
+        values = got["x"][1][i].cpu().unflatten(-1, (-1, 32))
+        assert torch.isnan(values[hit]).all()
+        place = lambda t: t.permute(0, 2, 1, 3).reshape(T, n_kv, D // 32, -1)              # [token, head, block, bytes]
+        for n in (side, side + "_scale"):
+            a, b = (place(got[v][0][n].view(torch.int16 if n.endswith("scale") else torch.uint8)) for v in ("clean", "x"))
+            assert torch.equal(a[~hit], b[~hit])
+    assert bqg.last_device_error() == 0
