@@ -408,7 +408,7 @@ template <int FMT, int D, bool F32> __global__ void __launch_bounds__(32 * kWarp
         if (m.what && p.slots) slot = p.slots[m.t];
         int64_t pos = 0;
         const bool turn = m.what < 2 && p.rot;
-        if (turn) pos = p.pos[m.t];
+        if (p.rot) pos = p.pos[m.t];
         F2 y[2][E];
 #pragma unroll
         for (int a = 0; a < 2; a++)
@@ -503,7 +503,8 @@ template <int FMT, int D, bool F32> __global__ void __launch_bounds__(32 * kWarp
             slot = -1;
         }
         if (now.what && p.slots) {
-            if (!lost && slot >= 0)
+            // (a value is not turned, but without a position its token is not stored; its key's row reports it)
+            if (!lost && slot >= 0 && (now.what < 2 || !p.rot || (pos >= 0 && pos < p.n_pos)))
                 encode_rows<FMT, D>(y, now.rows, lane, now.what == 1 ? p.cache.k : p.cache.v,
                                     now.what == 1 ? p.cache.k_scale : p.cache.v_scale, kv_row(p.cache, slot, now.h),
                                     (int64_t)1 << p.cache.lp);

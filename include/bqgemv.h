@@ -302,7 +302,7 @@ typedef struct bqg_kv_cache {
  * set when an index in device memory is out of range.  The access is skipped. */
 enum {
     BQG_DEVERR_SLOT = 16,       /* a slot beyond the cache: not stored, read as zeros          */
-    BQG_DEVERR_POSITION = 32,   /* a position outside the table: zeros out, not stored         */
+    BQG_DEVERR_POSITION = 32,   /* a position outside the table: zeros out, key and value not stored */
     BQG_DEVERR_PAGE = 64,       /* a page index outside the cache: its tokens are not seen     */
     BQG_DEVERR_LENGTH = 128     /* lengths or query offsets that do not fit: clamped to fit    */
 };

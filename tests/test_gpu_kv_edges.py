@@ -4,8 +4,9 @@ import pytest
 import torch
 
 import block_quantized_gemv_gb300 as bqg
+import kv_reference as ref
 from block_quantized_gemv_gb300 import build as bqg_build
-from test_gpu_kv_cache import arrays, filled_cache
+from test_gpu_kv_cache import FMTS, arrays, filled_cache, raw, rope_table
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,34 @@ def test_a_block_with_a_nan_reads_as_nan(fmt, D, dtype):
             a, b = (place(got[v][0][n].view(torch.int16 if n.endswith("scale") else torch.uint8)) for v in ("clean", "x"))
             assert torch.equal(a[~hit], b[~hit])
     assert bqg.last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [8, 1000, -1])
+def test_a_token_without_a_position_is_not_stored(ora, fmt, dtype, bad):
+    """Neither its key nor its value: the place keeps the pair it had.  Its neighbours go in."""
+    n_kv, page, D, T = 5, 16, 128, 4
+    cache = filled_cache(fmt, 2, n_kv, page, D)
+    before = arrays(cache)
+    x = torch.from_numpy(np.random.default_rng(4).standard_normal((2, T, n_kv, D), dtype=np.float32)).to(dtype)
+    pos = np.array([3, bad, 0, 7], dtype=np.int32)
+    slots = [9, 17, 4, 30]
+    table = rope_table(8, 64)
+    q = bqg.qk_norm_rope_kv_write(x[0].cuda(), x[0].cuda(), x[1].cuda(), torch.tensor(slots, device="cuda"), cache,
+                                  torch.from_numpy(pos).cuda(), torch.from_numpy(table).cuda())
+    assert bqg.last_device_error() == bqg.DEVERR_POSITION
+    assert not q[1].any() and q[[0, 2, 3]].any(-1).all()
+    good = [0, 2, 3]
+    after = arrays(cache)
+    for name, t in (("k", ref.norm_rope(x[0, good].float().numpy(), 0, None, 0, pos[good], table, False)),
+                    ("v", x[1, good].float().numpy())):
+        codes, scales = ref.encode(ora, fmt, t)
+        want = {name: torch.from_numpy(codes).to(before[name].dtype)}
+        if scales is not None:
+            want[name + "_scale"] = torch.from_numpy(scales)
+        for n, w in want.items():
+            full = before[n].clone()
+            for i, t in enumerate(good):
+                full[slots[t] // page, :, slots[t] % page] = w[i]
+            assert np.array_equal(raw(after[n]), raw(full)), n
