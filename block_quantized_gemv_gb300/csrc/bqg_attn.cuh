@@ -211,6 +211,11 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b)
     if ((uint64_t)(a | b) >> 32) return a / b;
     return (int64_t)((uint32_t)a / (uint32_t)b);
 }
+// BQG_DEVERR_LENGTH in `bad` where the sequences together do not hold all queries (their own offsets: attn_seq).
+__device__ __forceinline__ void attn_check_ends(const AttnParams &p, int &bad)
+{
+    if (p.q_start[0] != 0 || p.q_start[p.n_seq] != p.n_tokens) bad |= BQG_DEVERR_LENGTH;
+}
 // The units (weight(sequence) of them) of all sequences, and BQG_DEVERR_LENGTH in `bad` of some lanes; s and `mine`:
 // sequence `lane` and its units.  Called by whole warps, as attn_find is, which takes them on.
 template <typename W>
@@ -709,7 +714,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
     int64_t mine;
     AttnSeq s;
     const int64_t total = attn_total(p, lane, weight, bad, s, mine);
-    if (bad && blockIdx.x == 0 && warp == 0) atomicOr(error, bad);
+    if (blockIdx.x == 0 && warp == 0) {
+        attn_check_ends(p, bad);
+        if (bad) atomicOr(error, bad);
+    }
     const int64_t per = div_pos(total + gridDim.x - 1, gridDim.x);
     int64_t u = per * blockIdx.x;
     const int64_t u_end = min(u + per, total);

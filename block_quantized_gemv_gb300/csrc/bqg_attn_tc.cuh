@@ -900,7 +900,6 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             int bad = 0;
             TcWork<G::NQ, G::TT> work;
             work.init(p, lane, bad);
-            if (bad && blockIdx.x == 0) atomicOr(error, bad);
             for (int i = 0; ok; i++) {
                 if (!work.next(p, w)) w.n = 0;
                 if (i >= 2 && !(ok = wait(bar_pe(i), ((i >> 1) - 1) & 1))) break;
@@ -910,6 +909,10 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 }
                 __syncwarp();
                 if (w.n == 0) break;
+            }
+            if (blockIdx.x == 0) {
+                attn_check_ends(p, bad);
+                if (bad) atomicOr(error, bad);
             }
         }
     } else {

@@ -304,7 +304,8 @@ enum {
     BQG_DEVERR_SLOT = 16,       /* a slot beyond the cache: not stored, read as zeros          */
     BQG_DEVERR_POSITION = 32,   /* a position outside the table: zeros out, key and value not stored */
     BQG_DEVERR_PAGE = 64,       /* a page index outside the cache: its tokens are not seen     */
-    BQG_DEVERR_LENGTH = 128     /* lengths or query offsets that do not fit: clamped to fit    */
+    BQG_DEVERR_LENGTH = 128     /* lengths or query offsets that do not fit: clamped to fit; a query that is
+                                   then in no sequence is not computed, its output stays as it was */
 };
 
 /* Per-head RMSNorm and rotation of queries and keys.  q: T tokens of n_q

@@ -93,3 +93,20 @@ def test_a_masked_value_beyond_fp16_reaches_nobody(fmt, D, T, group, which):
     got = c.run()
     assert torch.isfinite(got[~seen]).all()
     within(c, got, where=~far)
+
+
+@pytest.mark.parametrize("D,T,group", [(128, 2, 4), (128, 20, 4), (256, 20, 4)])
+def test_queries_that_no_sequence_holds_are_reported(D, T, group):
+    """q_start is to begin at 0 and end at the number of queries: others are in no sequence, and the call says so.
+    The queries between are served."""
+    c = Case(bqg.Q8_0, D, 2, group, [100, 40], [T, T], page=32, seed=14)
+    keep = c.start.clone()
+    for start in ([1, T, 2 * T], [0, T, 2 * T - 1], [2, T + 1, 2 * T - 1]):
+        c.start.copy_(torch.tensor(start, dtype=torch.int32))
+        got = c.run()
+        assert bqg.last_device_error() == bqg.DEVERR_LENGTH
+        within(c, got, where=((torch.arange(c.n, device="cuda") >= start[0])
+                              & (torch.arange(c.n, device="cuda") < start[-1]))[:, None, None].expand_as(got))
+    c.start.copy_(keep)
+    within(c, c.run())
+    assert bqg.last_device_error() == 0
