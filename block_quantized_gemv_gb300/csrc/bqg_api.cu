@@ -55,9 +55,6 @@ int gemm_read_error(cudaStream_t, int *);
 cudaError_t attn_launch_bf16(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
 cudaError_t attn_launch_q8_0(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
 cudaError_t attn_launch_q4_0(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
-cudaError_t attn_take_error_bf16(int *);
-cudaError_t attn_take_error_q8_0(int *);
-cudaError_t attn_take_error_q4_0(int *);
 }  // namespace bqg
 
 using namespace bqg;
@@ -1335,8 +1332,7 @@ int bqg_last_device_error(cudaStream_t stream, int *out)
     int word = 0;
     if (int st = gemm_read_error(stream, &word)) return st;
     int w = 0;
-    for (auto fn : {gemv_error_bf16, gemv_error_q8_0, gemv_error_q4_0, gemv_error_q4_0_q8_1, layer_take_error, kv_take_error,
-                    attn_take_error_bf16, attn_take_error_q8_0, attn_take_error_q4_0}) {
+    for (auto fn : {gemv_error_bf16, gemv_error_q8_0, gemv_error_q4_0, gemv_error_q4_0_q8_1, layer_take_error}) {
         if (fn(&w) != cudaSuccess) return BQG_ERR_CUDA;
         word |= w;
     }

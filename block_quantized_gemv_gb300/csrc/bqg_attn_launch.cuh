@@ -2,7 +2,6 @@
 #pragma once
 
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -25,16 +24,6 @@ constexpr size_t kAttnHead = kAttnCounterBytes + kAttnSetBytes;
 struct AttnPlan {
     size_t ws_bytes;
 };
-
-inline cudaError_t take_error(int &word, int *out)
-{
-    int v = 0, zero = 0;
-    if (cudaError_t e = cudaMemcpyFromSymbol(&v, word, sizeof(int))) return e;
-    if (v)
-        if (cudaError_t e = cudaMemcpyToSymbol(word, &zero, sizeof(int))) return e;
-    *out = v;
-    return cudaSuccess;
-}
 
 // Rows from which the tcgen05 kernel serves a call; below, the mma.sync kernel.  Measured with 4 heads on each of 8 KV
 // heads, its time over the other's:
@@ -166,22 +155,11 @@ template <int FMT, int D> cudaError_t attn_pick(const AttnParams &p, int rows, i
 
 // rows: the most rows (new tokens x heads of a group) of any sequence.
 template <int FMT>
-cudaError_t attn_launch(const AttnParams &p, int D, int rows, int &error_word, AttnPlan *plan, cudaStream_t s, bool pdl)
+cudaError_t attn_launch(const AttnParams &p, int D, int rows, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
     int *error = nullptr;
-    if (!plan) {
-        // the error word's address: looked up once per device
-        static std::atomic<void *> known[64];
-        int dev = 0;
-        if (cudaError_t e = cudaGetDevice(&dev)) return e;
-        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-        void *word = known[dev].load(std::memory_order_relaxed);
-        if (!word) {
-            if (cudaError_t e = cudaGetSymbolAddress(&word, error_word)) return e;
-            known[dev].store(word, std::memory_order_relaxed);
-        }
-        error = static_cast<int *>(word);
-    }
+    if (!plan)
+        if (cudaError_t e = device_error_word(&error)) return e;
     if (D == 64) return attn_pick<FMT, 64>(p, rows, error, plan, s, pdl);
     if (D == 128) return attn_pick<FMT, 128>(p, rows, error, plan, s, pdl);
     return attn_pick<FMT, 256>(p, rows, error, plan, s, pdl);

@@ -44,17 +44,18 @@
 // SM).  Every mbarrier wait is bounded: on a timeout the kernel sets
 // g_gemm_error, stops issuing work, drains what it started and frees TMEM.
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "bqg_common.cuh"
+#include "bqg_kv.cuh"
 #include "bqg_tc.cuh"
 
 namespace bqg {
 
-// Error word set by bounded device-side waits (0 = none).
+// Error word set by bounded device-side waits (0 = none), and by the kernels that take its address (bqg_kv.cuh).
 __device__ int g_gemm_error;
 
 namespace {
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_bf16_kernel(const __grid_
     pdl_launch_dependents();
 
     auto fail = [&]() {
-        atomicExch(&g_gemm_error, 2);
+        atomicOr(&g_gemm_error, 2);
         *abort_flag = 1;
     };
 
@@ -622,6 +623,21 @@ int gemm_read_error(cudaStream_t stream, int *out)
     if (v && cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof(int)) != cudaSuccess) return BQG_ERR_CUDA;
     *out = v;
     return BQG_OK;
+}
+
+cudaError_t device_error_word(int **out)
+{
+    static std::atomic<void *> known[64];                                // looked up once per device
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    void *word = known[dev].load(std::memory_order_relaxed);
+    if (!word) {
+        if (cudaError_t e = cudaGetSymbolAddress(&word, g_gemm_error)) return e;
+        known[dev].store(word, std::memory_order_relaxed);
+    }
+    *out = static_cast<int *>(word);
+    return cudaSuccess;
 }
 
 size_t gemm_workspace(int, int64_t, int64_t) { return 0; }

@@ -28,19 +28,6 @@
 
 namespace bqg {
 
-// Bits of out-of-range indices met (BQG_DEVERR_*).
-__device__ int g_kv_error;
-
-cudaError_t kv_take_error(int *out)
-{
-    int v = 0, zero = 0;
-    if (cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_error, sizeof(int))) return e;
-    if (v)
-        if (cudaError_t e = cudaMemcpyToSymbol(g_kv_error, &zero, sizeof(int))) return e;
-    *out = v;
-    return cudaSuccess;
-}
-
 namespace {
 
 constexpr int kWarps = 4;      // warps per CTA
@@ -436,7 +423,7 @@ template <int FMT, int D, bool F32> __global__ void __launch_bounds__(32 * kWarp
         int other = lane;
         if (turn) {
             lost = pos < 0 || pos >= p.n_pos;
-            if (lost && lane == 0) atomicOr(&g_kv_error, BQG_DEVERR_POSITION);
+            if (lost && lane == 0) atomicOr(p.error, BQG_DEVERR_POSITION);
             const float *row = p.table + (lost ? 0 : pos) * p.rot;
             if (in) {
                 if (p.interleaved) {
@@ -499,7 +486,7 @@ template <int FMT, int D, bool F32> __global__ void __launch_bounds__(32 * kWarp
             }
         }
         if (slot >= 0 && !kv_slot_ok(p.cache, slot)) {
-            if (lane == 0) atomicOr(&g_kv_error, BQG_DEVERR_SLOT);
+            if (lane == 0) atomicOr(p.error, BQG_DEVERR_SLOT);
             slot = -1;
         }
         if (now.what && p.slots) {
@@ -542,7 +529,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const KvReadParams p)
         const int hj = (int)(rest - t * (n_kv * J)), h = hj / J, j = hj % J;
         int64_t slot = p.slots[t];
         if (slot >= 0 && !kv_slot_ok(p.cache, slot)) {
-            atomicOr(&g_kv_error, BQG_DEVERR_SLOT);
+            atomicOr(p.error, BQG_DEVERR_SLOT);
             slot = -1;
         }
         float f[16];
@@ -622,21 +609,23 @@ template <int FMT, bool F32> void (*kv_read_fn(int D))(KvReadParams)
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormRopeParams &p, int fmt, int D, int sms, cudaStream_t s, bool pdl)
+cudaError_t launch_norm_rope(NormRopeParams p, int fmt, int D, int sms, cudaStream_t s, bool pdl)
 {
     const int64_t groups = (p.n_q + 3) / 4 + ((p.k ? 1 : 0) + (p.v ? 1 : 0)) * ((p.n_kv + 3) / 4);
     const int64_t items = p.T * groups;
     if (items == 0) return cudaSuccess;
+    if (cudaError_t e = device_error_word(&p.error)) return e;
     auto fn = p.x_f32 ? (fmt == BQG_Q8_0 ? norm_rope_fn<BQG_Q8_0, true>(D) : fmt == BQG_Q4_0 ? norm_rope_fn<BQG_Q4_0, true>(D) : norm_rope_fn<BQG_BF16, true>(D))
                       : (fmt == BQG_Q8_0 ? norm_rope_fn<BQG_Q8_0, false>(D) : fmt == BQG_Q4_0 ? norm_rope_fn<BQG_Q4_0, false>(D) : norm_rope_fn<BQG_BF16, false>(D));
     const int per_sm = D == 256 ? resident<256>() : D == 128 ? resident<128>() : resident<64>();
     return launch(fn, p, std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)sms * per_sm), 32 * kWarps, s, pdl);
 }
 
-cudaError_t launch_kv_read(const KvReadParams &p, int fmt, int D, int out_f32, int sms, cudaStream_t s, bool pdl)
+cudaError_t launch_kv_read(KvReadParams p, int fmt, int D, int out_f32, int sms, cudaStream_t s, bool pdl)
 {
     const int64_t n = 2 * p.T * p.cache.n_kv * (D / 16);
     if (n == 0) return cudaSuccess;
+    if (cudaError_t e = device_error_word(&p.error)) return e;
     auto fn = out_f32 ? (fmt == BQG_Q8_0 ? kv_read_fn<BQG_Q8_0, true>(D) : fmt == BQG_Q4_0 ? kv_read_fn<BQG_Q4_0, true>(D) : kv_read_fn<BQG_BF16, true>(D))
                       : (fmt == BQG_Q8_0 ? kv_read_fn<BQG_Q8_0, false>(D) : fmt == BQG_Q4_0 ? kv_read_fn<BQG_Q4_0, false>(D) : kv_read_fn<BQG_BF16, false>(D));
     return launch(fn, p, std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8), 256, s, pdl);

@@ -44,6 +44,7 @@ struct NormRopeParams {
     uint16_t *q_out, *k_out;                     // bf16; k_out null: keys go into the cache
     const int64_t *slots;                        // null: no cache
     KvCacheDev cache;
+    int *error;                                  // device_error_word, set by the launch
 };
 
 struct KvReadParams {
@@ -51,10 +52,13 @@ struct KvReadParams {
     const int64_t *slots;
     int64_t T;
     void *k_out, *v_out;
+    int *error;                                  // as above
 };
 
-cudaError_t launch_norm_rope(const NormRopeParams &p, int fmt, int D, int sms, cudaStream_t s, bool pdl);
-cudaError_t launch_kv_read(const KvReadParams &p, int fmt, int D, int out_f32, int sms, cudaStream_t s, bool pdl);
-cudaError_t kv_take_error(int *out);
+cudaError_t launch_norm_rope(NormRopeParams p, int fmt, int D, int sms, cudaStream_t s, bool pdl);
+cudaError_t launch_kv_read(KvReadParams p, int fmt, int D, int out_f32, int sms, cudaStream_t s, bool pdl);
+// The error word of the current device for the cache's and attention's kernels (bits BQG_DEVERR_*, and those of bounded
+// waits): the prefill GEMM's, so that bqg_last_device_error has no more words to fetch (each costs it 9 us).
+cudaError_t device_error_word(int **out);
 
 }  // namespace bqg

@@ -80,3 +80,19 @@ def test_a_token_without_a_position_is_not_stored(ora, fmt, dtype, bad):
             for i, t in enumerate(good):
                 full[slots[t] // page, :, slots[t] % page] = w[i]
             assert np.array_equal(raw(after[n]), raw(full)), n
+
+
+def test_errors_of_several_calls_come_together_and_once():
+    """What different kernels report between two questions is in one word, which the question clears."""
+    cache = bqg.kv_cache(bqg.Q8_0, 2, 1, 16, 64)
+    x = torch.ones(1, 1, 64, device="cuda")
+    at = lambda *v, dtype=torch.int32: torch.tensor(v, dtype=dtype, device="cuda")
+    bqg.kv_read(cache, at(99, dtype=torch.int64))
+    bqg.qk_norm_rope(x, x, at(5), torch.ones(2, 64, device="cuda"))
+    for rows in (1, 40):
+        q = torch.ones(rows, 1, 64, dtype=torch.bfloat16, device="cuda")
+        ws = bqg.tree_attention_workspace(cache, 1, 1, rows)
+        bqg.tree_attention(q, cache, at(-1, -1, -1).view(1, 3), at(0), at(0, rows), rows, ws=ws)
+        seen = bqg.last_device_error()
+        assert seen == (bqg.DEVERR_SLOT | bqg.DEVERR_POSITION | bqg.DEVERR_PAGE if rows == 1 else bqg.DEVERR_PAGE)
+        assert bqg.last_device_error() == 0
