@@ -457,7 +457,16 @@ class KVCache:
     with rows of head_dim bf16 values (BF16), head_dim int8 codes (Q8_0) or
     head_dim / 2 uint8 code pairs (Q4_0); k_scale, v_scale
     [n_pages, n_kv, page_size, head_dim / 32] fp16 for the quantized formats.
-    Keeps the tensors alive; the shapes are checked once, here."""
+    Keeps the tensors alive; the shapes are checked and the addresses taken
+    once, here, so tensors and sizes cannot be set: other ones, another cache."""
+
+    _FIXED = frozenset(("fmt", "n_pages", "n_kv", "page_size", "head_dim", "k", "v", "k_scale", "v_scale", "device_index",
+                        "_struct", "_ptr"))
+
+    def __setattr__(self, name, value):
+        if name in self._FIXED and name in self.__dict__:
+            raise AttributeError(f"a KVCache's {name} is fixed: its calls use what it was made with")
+        object.__setattr__(self, name, value)
 
     def __init__(self, fmt: int, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
