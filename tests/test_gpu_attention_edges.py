@@ -5,7 +5,7 @@ import torch
 import block_quantized_gemv_gb300 as bqg
 import kv_reference as ref
 from block_quantized_gemv_gb300 import build as bqg_build
-from test_gpu_tree_attention import Case
+from test_gpu_tree_attention import FMTS, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +110,83 @@ def test_queries_that_no_sequence_holds_are_reported(D, T, group):
     c.start.copy_(keep)
     within(c, c.run())
     assert bqg.last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,group", [(1, 4), (3, 4), (9, 4), (30, 4), (64, 4)])
+def test_the_maximum_rises_in_every_tile(fmt, D, T, group):
+    """Keys that grow along the context, several tiles to a CTA: rows' maxima pass the former ones by far more than the
+    slack, so what was summed up before is scaled down again and again."""
+    c = Case(fmt, D, 8, group, [700] * 20, [T] * 20, page=64, tree=True, seed=7, junk=False)
+    grow = torch.logspace(-1.5, 1.0, c.table.shape[1] * 64, dtype=torch.float64, device="cuda")
+    t = c.cache.k if fmt == bqg.BF16 else c.cache.k_scale
+    for b in range(20):
+        pages = c.table[b].long()
+        f = grow.view(-1, 1, 64, 1)
+        t[pages] = (t[pages].double() * f).to(t.dtype)
+    within(c, c.run())
+    assert bqg.last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,group", [(2, 4), (20, 4), (50, 4)])
+@pytest.mark.parametrize("lost", [(1,), (2,), (0, 3, 6), (9,)])
+def test_missing_pages_in_either_half_of_a_tile(fmt, D, T, group, lost):
+    """Page numbers outside the cache, in the context and (page 9) among the new tokens: their tokens count for no row."""
+    c = Case(fmt, D, 2, group, [300], [T], page=32, tree=True, seed=3, junk=False)
+    for i, page in enumerate(lost):
+        c.table[0, page] = (-1, c.cache.n_pages, 2 ** 31 - 1)[i]
+    got = c.run()
+    assert bqg.last_device_error() == bqg.DEVERR_PAGE
+    within(c, got, gone=[32 * page + i for page in lost for i in range(32) if 32 * page + i < 300 + T])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,group", [(1, 1), (3, 4), (9, 4), (40, 4)])
+def test_scales_of_either_sign(D, T, group):
+    """q4_0: the scale has the sign of minus the block's largest value."""
+    c = Case(bqg.Q4_0, D, 2, group, [333, 60], [T, 1], page=32, tree=True, seed=8)
+    g = torch.Generator().manual_seed(9)
+    for t in (c.cache.k_scale, c.cache.v_scale):
+        t.mul_(torch.where(torch.rand(t.shape, generator=g) < 0.5, -1.0, 1.0).to(torch.float16).cuda())
+    within(c, c.run())
+    assert bqg.last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T", [1, 3, 64])
+def test_sixty_four_heads_per_kv_head(fmt, D, T):
+    c = Case(fmt, D, 1, 64, [150, 7], [T, 1], page=16, tree=True, seed=T)
+    within(c, c.run())
+    assert bqg.last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,group", [(1, 4), (40, 4)])
+def test_pages_beyond_32_bits_of_bytes(fmt, T, group):
+    """The same pages at the end of a cache of more than 2^32 bytes a side: the same bits."""
+    c = Case(fmt, 128, 2, group, [900, 130], [T, T], page=64, tree=True, seed=15)
+    want = c.run()
+    small = c.cache
+    row = small.k[0].nbytes
+    c.cache = bqg.kv_cache(fmt, 2 ** 32 // row + small.n_pages + 1, 2, 64, 128)
+    at = c.cache.n_pages - small.n_pages
+    for big, t in ((c.cache.k, small.k), (c.cache.v, small.v), (c.cache.k_scale, small.k_scale), (c.cache.v_scale, small.v_scale)):
+        if t is not None:
+            big[at:] = t
+    c.table = c.table + at
+    assert torch.equal(c.run().view(torch.int16), want.view(torch.int16))
+    assert bqg.last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_workspace_for_more_new_tokens_serves_fewer(fmt, D):
+    """A step checks trees of several sizes over one workspace, made for the largest."""
+    cache = bqg.kv_cache(fmt, 1, 1, 16, D)
+    for group in (1, 2, 3, 4, 5, 7, 8, 16, 64):
+        sizes = [bqg.tree_attention_workspace(cache, group, 4, t).numel() for t in range(1, 65)]
+        assert sizes == sorted(sizes), (group, sizes)
