@@ -20,11 +20,11 @@ from __future__ import annotations
 
 import argparse
 import ctypes
-import glob
 import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -52,22 +52,37 @@ def measured_peaks():
     return {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustained": 1700.0, "source": "fallback"}
 
 
-def source_hash():
+CSRC = os.path.join(ROOT, "block_quantized_gemv_gb300", "csrc")
+# translation unit of a kernel key's kernels (the first prefix that fits)
+KERNEL_SOURCE = (("gemm_", "bqg_gemm.cu"), ("decode_layer_", "bqg_layer.cu"), ("gemv_q4_0_q8_1_", "gemv_q4_0_q8_1.cu"),
+                 ("gemv_q4_0_", "gemv_q4_0.cu"), ("gemv_q8_0_", "gemv_q8_0.cu"), ("gemv_bf16_", "gemv_bf16.cu"))
+
+
+def source_hash(kernel_key, csrc=CSRC):
+    """Hash of the sources that kernel_key's kernels are compiled from: their
+    translation unit and the headers of csrc/ it includes, directly or not."""
+    todo = [next(tu for prefix, tu in KERNEL_SOURCE if kernel_key.startswith(prefix))]
+    texts = {}
+    while todo:
+        name = todo.pop()
+        if name not in texts:
+            texts[name] = open(os.path.join(csrc, name), "rb").read()
+            todo += [n.decode() for n in re.findall(rb'^#include "([^"/]+)"', texts[name], re.M)]
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "block_quantized_gemv_gb300", "csrc", "*"))):
-        h.update(open(f, "rb").read())
+    for name in sorted(texts):
+        h.update(texts[name])
     return h.hexdigest()[:16]
 
 
 def profiled_traffic(kernel_key):
-    """DRAM bytes per launch from the committed ncu summary, if the kernel
-    sources have not changed since it was taken (else None)."""
+    """DRAM bytes per launch from the committed ncu summary, if the kernel's
+    own sources have not changed since it was taken (else None)."""
     p = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(p):
         return None
     d = json.load(open(p))
     e = d.get(kernel_key)
-    if not e or e.get("source_hash") != source_hash():
+    if not e or e.get("source_hash") != source_hash(kernel_key):
         return None
     return e.get("dram_bytes_per_launch")
 

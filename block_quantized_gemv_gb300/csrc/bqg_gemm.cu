@@ -50,7 +50,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "bqg_kv.cuh"
+#include "bqg_common.cuh"
 #include "bqg_tc.cuh"
 
 namespace bqg {
