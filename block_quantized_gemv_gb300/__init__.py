@@ -697,7 +697,8 @@ def tree_attention(q, cache: KVCache, block_table, ctx_len, q_start, max_q: int,
     [n_seq + 1] their first tokens; block_table int32 [n_seq, max_pages];
     ctx_len int32 [n_seq]; mask int64 [n_tokens], bit j set where new token j
     of the sequence is seen (a tree of drafted tokens), or None for causal;
-    scale defaults to head_dim ** -0.5.  Returns bf16 [n_tokens, n_q, head_dim]."""
+    scale defaults to head_dim ** -0.5; ws: from tree_attention_workspace, and
+    a call without one is refused.  Returns bf16 [n_tokens, n_q, head_dim]."""
     cur = _current_device()
     n, n_q, _ = _shape3(q, "q")
     dim = cache.head_dim

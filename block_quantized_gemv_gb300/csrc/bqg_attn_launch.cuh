@@ -25,14 +25,13 @@ struct AttnPlan {
     size_t ws_bytes;
 };
 
-// Rows from which the tcgen05 kernel serves a call; below, the mma.sync kernel.  Measured with 4 heads on each of 8 KV
-// heads, its time over the other's:
-//  * 64 and 128 values, 1 to 64 sequences of 200 to 40,000 tokens: 12 and 16 rows 0.6 to 1.4 for bf16, but 0.9 to 2.1 for
-//    q8_0 and q4_0; 24 and 32 rows (mma.sync with four row tiles) 0.4 to 1.1 for bf16 and 0.6 to 1.3 for the quantized
-//    formats, above 1.05 only for 64 sequences of up to 1500 tokens;
-//  * 256 values, 1 to 40 sequences of 300 to 12,000: 12 and 16 rows 0.4 to 1.1 for bf16, but 0.7 to 1.75 for q8_0 and q4_0;
-//    24 and 32 rows (mma.sync in two turns) 0.5 to 0.9 for bf16 and 0.6 to 1.4 for the quantized formats, less the more
-//    rows: 64 rows 0.4 and 0.5.
+// Rows from which the tcgen05 kernel serves a call; below, the mma.sync kernel, which is built for one and two tiles of 8
+// rows.  Measured with 4 heads on each of 8 KV heads, tcgen05's time over mma.sync's at 12 and 16 rows:
+//  * 64 and 128 values, 1 to 64 sequences of 200 to 40,000 tokens: 0.6 to 1.4 for bf16, but 0.9 to 2.1 for q8_0 and q4_0;
+//  * 256 values, 1 to 40 sequences of 300 to 12,000: 0.4 to 1.1 for bf16, but 0.7 to 1.75 for q8_0 and q4_0.
+// So the threshold is where mma.sync's row tiles end, but for bf16 at 256 values, where it is where its first one does.  More
+// row tiles were built and taken out again: four of them at 24 and 32 rows took longer than tcgen05 but for 64 sequences of up to
+// 1500 tokens, and for 256 values, in turns of 16 rows over the same pages, the longer the more rows (64 rows: 2 to 2.5 times).
 template <int FMT, int D> constexpr int kAttnTcRows = FMT == BQG_BF16 && D == 256 ? 9 : 17;
 
 inline void attn_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, dim3 grid, int threads, int smem, cudaStream_t s,

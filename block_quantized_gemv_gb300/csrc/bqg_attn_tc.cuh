@@ -30,7 +30,7 @@
 //    of 64 values x the tokens of a page.  q8_0 / q4_0: codes and scales as they
 //    lie, one bulk copy each per page, into a ring of their own, from which warps
 //    12-19 build the tile: codes as fp16 integers (bqg_attn.cuh), times the
-//    block's scale: one rounding (relative 2^-12, for keys too: a block's scale
+//    block's scale: one rounding (relative 2^-11, for keys too: a block's scale
 //    cannot be applied behind a product that sums over all blocks).
 //  * Tiles are shared out over the CTAs, a tile of two halves counting twice: one piece for each, or even
 //    ranges (see TcWork).  Sets of tiles that several CTAs share leave partial

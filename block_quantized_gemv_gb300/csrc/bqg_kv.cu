@@ -166,8 +166,8 @@ template <int FMT, int E> __device__ __noinline__ uint64_t codes_exact(const flo
 // halves the rows a lane holds, so a row's scale is worked out in LB / 4 lanes of
 // its block and handed to the others.  A code is round(x / d), halves away
 // from zero, x / d rounded once to fp32.  The quick way is x times the approximate 1 / d, rounded by adding
-// and taking off 1.5 x 2^23, two values per instruction.  It is off by at most 2^-22.4 of |x / d| (1 / d:
-// 2^-23, the product and the quotient 2^-24 each), which is under 2^-14 for q8_0 (127.5) and under 2^-18 for
+// and taking off 1.5 x 2^23, two values per instruction.  It is off by at most 2^-22 of |x / d| (1 / d:
+// 2^-23, the product and the quotient 2^-24 each), so by less than 2^-14 of a step for q8_0 (|x / d| up to 127.5) and 2^-18 for
 // q4_0 (8.05); where a value lies within that of a half, or it or the scale is not an ordinary number, the
 // rows' codes are divided out (one group of four rows in 16, and in 256; with 2^-12 for both it was one
 // in four, and 8192 tokens of 8 heads took 39 us instead of 27).

@@ -369,7 +369,7 @@ int bqg_kv_read(const bqg_kv_cache *cache, const int64_t *slots, int64_t T, int 
  * one n_tokens.  ctx_len: n_seq int32.  block_table: n_seq rows of max_pages int32.
  * 1 <= max_q <= 64.  scale > 0 and finite.
  * Keys and values enter the products as they are (bf16), or (quantized) values as q d rounded
- * once to fp16 (relative 2^-12), and keys as their integer codes, whose block sums are scaled in fp32, where
+ * once to fp16 (relative 2^-11; exact below 2^-14), and keys as their integer codes, whose block sums are scaled in fp32, where
  * max_q * n_q / n_kv is at most 16, as q d rounded once to fp16 otherwise.  So
  * quantized keys and values beyond fp16's range (65504) are out of range here: a query that sees one may get
  * infinities, one that does not see it is not touched by it either.  A quantized call's queries
