@@ -19,8 +19,8 @@
 // in the lanes that ended up with its row; the rotation's cos and sin are loaded once
 // for the four rows.
 //
-// Measured (back to back): 7001 tokens of 64 + 8 + 8 heads of 128 values, bf16, norm and rotation: 96 us, bound by issue
-// (148 instructions per row, 71 % of the slots); 8192 tokens of 8 + 8 heads, f32 into q4_0: 28 us, read back as bf16: 10.4 us,
+// Measured (back to back): 7001 tokens of 64 + 8 + 8 heads of 128 values, bf16, norm and rotation: 97 us, bound by issue
+// (about 150 instructions per row, 71 % of the slots); 8192 tokens of 8 + 8 heads, f32 into q4_0: 28 us, read back as bf16: 10.4 us,
 // 0.6 of the copy rate; one token: 3.6 and 2.2 us, a launch's latency.
 #include <algorithm>
 
