@@ -68,6 +68,9 @@ EXPORTS = {
     "bqg_tree_attention": (["p", "i64", "p", "p", "i64", "p", "p", "i", "i64", "i", "i", "p", "f", "p", "p", "size",
                             "p"], "i"),
     "bqg_tree_attention_workspace_size": (["p", "i", "i", "i"], "size"),
+    "bqg_shared_prefix_attention": (["p", "i64", "p", "p", "i64", "p", "p", "i", "i64", "i", "i", "p", "p", "i", "i64", "p",
+                                     "f", "p", "p", "size", "p"], "i"),
+    "bqg_shared_prefix_attention_workspace_size": (["p", "i", "i", "i", "i64", "i", "i64"], "size"),
     "bqg_gemv_q4_0_q8_1_noalloc": (["p", "p", "p", "i", "i64", "i64", "p"], "i"),
     "bqg_noalloc_scratch_bytes": ([], "size"),
 }
@@ -723,6 +726,57 @@ def tree_attention(q, cache: KVCache, block_table, ctx_len, q_start, max_q: int,
                                      dim ** -0.5 if scale is None else scale,
                                      op, wsp, wsb, _stream(stream)),
            "bqg_tree_attention")
+    return out
+
+
+def shared_prefix_attention_workspace(cache: KVCache, n_q: int, n_seq: int, max_q: int, n_tokens: int, n_prefix: int = 1,
+                                      max_shared: int | None = None) -> torch.Tensor:
+    """A zero-filled workspace for shared_prefix_attention calls of at most these sizes."""
+    n = int(load().bqg_shared_prefix_attention_workspace_size(cache._handle(_current_device()), n_q, n_seq, max_q, n_tokens,
+                                                              n_prefix, n_tokens if max_shared is None else max_shared))
+    if n == 0:
+        raise ValueError("not a shared_prefix_attention call on this device")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)
+
+
+def shared_prefix_attention(q, cache: KVCache, block_table, ctx_len, q_start, max_q: int, prefix_len, seq_start=None,
+                            max_shared: int | None = None, mask=None, scale=None, out=None, ws=None,
+                            stream=None) -> torch.Tensor:
+    """tree_attention where sequences share their first tokens, which are read and multiplied once for all of them.
+
+    Arguments and result as tree_attention's (ctx_len and block_table with the shared tokens), and: prefix_len int32
+    [n_prefix], the tokens that sequences seq_start[g] .. seq_start[g + 1] - 1 share (at most the ctx_len of
+    each; taken from the first one's pages); seq_start int32 [n_prefix + 1], or None for one prefix of all
+    sequences; max_shared: query tokens behind one prefix at most (default: all of the call's); ws: from
+    shared_prefix_attention_workspace, and a call without one is refused."""
+    cur = _current_device()
+    n, n_q, _ = _shape3(q, "q")
+    dim = cache.head_dim
+    qp, qs = _tokens(q, cur, "q", (n, n_q, dim), torch.bfloat16)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_seq, max_pages]")
+    n_seq, max_pages = block_table.shape
+    n_prefix = prefix_len.numel()
+    if seq_start is None and n_prefix != 1:
+        raise ValueError("several prefixes need seq_start")
+    if out is None:
+        out = torch.empty((n, n_q, dim), dtype=torch.bfloat16, device=q.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, cur, "out", torch.bfloat16, n * n_q * dim * 2)
+    if ws is None:
+        wsp, wsb = None, 0
+    else:
+        wsb = ws.nbytes
+        wsp = _ptr(ws, cur, "ws", ws.dtype, wsb)
+    _check(load().bqg_shared_prefix_attention(
+        qp, qs, cache._handle(cur), _ptr(block_table, cur, "block_table", torch.int32, 0), max_pages,
+        _vector(ctx_len, cur, "ctx_len", torch.int32, n_seq), _vector(q_start, cur, "q_start", torch.int32, n_seq + 1), n_seq,
+        n, max_q, n_q, _vector(prefix_len, cur, "prefix_len", torch.int32, n_prefix),
+        None if seq_start is None else _vector(seq_start, cur, "seq_start", torch.int32, n_prefix + 1), n_prefix,
+        n if max_shared is None else max_shared, None if mask is None else _vector(mask, cur, "mask", torch.int64, n),
+        dim ** -0.5 if scale is None else scale, op, wsp, wsb, _stream(stream)),
+        "bqg_shared_prefix_attention")
     return out
 
 

@@ -53,6 +53,9 @@ int gemm_bf16(int, const void *, const void *, float *, int, int64_t, int64_t, c
 size_t gemm_workspace(int, int64_t, int64_t);
 int gemm_read_error(cudaStream_t, int *);
 cudaError_t attn_launch_bf16(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
+cudaError_t shared_launch_bf16(const SharedParams &, int, AttnPlan *, cudaStream_t, bool);
+cudaError_t shared_launch_q8_0(const SharedParams &, int, AttnPlan *, cudaStream_t, bool);
+cudaError_t shared_launch_q4_0(const SharedParams &, int, AttnPlan *, cudaStream_t, bool);
 cudaError_t attn_launch_q8_0(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
 cudaError_t attn_launch_q4_0(const AttnParams &, int, int, AttnPlan *, cudaStream_t, bool);
 }  // namespace bqg
@@ -791,6 +794,27 @@ cudaError_t attn_run(int fmt, const AttnParams &p, int D, AttnPlan *plan, cudaSt
                            : attn_launch_q4_0(p, D, rows, plan, s, pdl);
 }
 
+// What a call behind shared prefixes adds to a tree attention call's parameters.
+int shared_params(const int32_t *prefix_len, const int32_t *seq_start, int n_prefix, int64_t max_shared, SharedParams *p)
+{
+    if (n_prefix < 1 || max_shared < 0 || (!seq_start && n_prefix != 1)) return BQG_ERR_INVALID_ARG;
+    // (a row's number among those of one KV head is an int)
+    if (max_shared > ((int64_t)1 << 30) / p->group) return BQG_ERR_UNSUPPORTED_SHAPE;
+    p->prefix_len = prefix_len;
+    p->seq_start = seq_start;
+    p->n_prefix = n_prefix;
+    p->n_all = p->n_seq;
+    p->max_shared = std::max<int64_t>(max_shared, 1);
+    return BQG_OK;
+}
+
+cudaError_t shared_run(int fmt, const SharedParams &p, int D, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    return fmt == BQG_BF16 ? shared_launch_bf16(p, D, plan, s, pdl)
+         : fmt == BQG_Q8_0 ? shared_launch_q8_0(p, D, plan, s, pdl)
+                           : shared_launch_q4_0(p, D, plan, s, pdl);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1254,6 +1278,47 @@ size_t bqg_tree_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int
         return 0;
     AttnPlan plan;
     return attn_run(cache->fmt, p, cache->head_dim, &plan, 0, false) == cudaSuccess ? plan.ws_bytes : 0;
+}
+
+int bqg_shared_prefix_attention(const void *q, int64_t q_stride, const bqg_kv_cache *cache, const int32_t *block_table,
+                                int64_t max_pages, const int32_t *ctx_len, const int32_t *q_start, int n_seq,
+                                int64_t n_tokens, int max_q, int n_q, const int32_t *prefix_len, const int32_t *seq_start,
+                                int n_prefix, int64_t max_shared, const uint64_t *mask, float scale, void *out, void *ws,
+                                size_t ws_bytes, cudaStream_t stream)
+{
+    SharedParams p{};
+    if (int st = attn_params(q, q_stride, cache, block_table, max_pages, ctx_len, q_start, n_seq, n_tokens, max_q, n_q,
+                             mask, scale, out, &p))
+        return st;
+    if (int st = shared_params(prefix_len, seq_start, n_prefix, max_shared, &p)) return st;
+    if (n_tokens && (!q || !out || !block_table || !ctx_len || !q_start || !prefix_len)) return BQG_ERR_INVALID_ARG;
+    const int D = cache->head_dim;
+    if (n_tokens)
+        if (int st = check_tokens(q, q_stride, n_q, D, BQG_BF16)) return st;
+    if (!aligned16(out) || !aligned(block_table, 4) || !aligned(ctx_len, 4) || !aligned(q_start, 4) || !aligned(mask, 8) ||
+        !aligned(prefix_len, 4) || !aligned(seq_start, 4) || !aligned16(ws))
+        return BQG_ERR_MISALIGNED;
+    DevInfo dev;
+    if (int st = current_device(&dev)) return st;
+    if (n_tokens == 0) return BQG_OK;
+    AttnPlan plan;
+    if (cudaError_t e = shared_run(cache->fmt, p, D, &plan, stream, false)) return cuda_status(e);
+    if (!ws || ws_bytes < plan.ws_bytes) return BQG_ERR_WORKSPACE;
+    p.counters = (int *)ws;
+    return cuda_status(shared_run(cache->fmt, p, D, nullptr, stream, g_pdl.load() != 0));
+}
+
+size_t bqg_shared_prefix_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int n_seq, int max_q, int64_t n_tokens,
+                                                  int n_prefix, int64_t max_shared)
+{
+    SharedParams p{};
+    DevInfo dev;
+    const int32_t some = 0;
+    if (attn_params(nullptr, 0, cache, nullptr, 1, nullptr, nullptr, n_seq, n_tokens, max_q, n_q, nullptr, 1.0f, nullptr, &p) ||
+        shared_params(&some, &some, n_prefix, max_shared, &p) || current_device(&dev))
+        return 0;
+    AttnPlan plan;
+    return shared_run(cache->fmt, p, cache->head_dim, &plan, 0, false) == cudaSuccess ? plan.ws_bytes : 0;
 }
 
 size_t bqg_workspace_size(int op, int M, int64_t N, int64_t K)

@@ -59,7 +59,24 @@ constexpr int kUnit = kAttnWarps * kStrip;
 constexpr int kLead = 2;                 // units that beginning a set counts as, see attn_kernel
 constexpr float kSlack = 6.0f;
 
+// One sequence as the kernels work on it.
+struct AttnSeq {
+    int b, q0, T, ctx, len;      // first query token, new tokens, context and all cached tokens
+};
+// A set of tokens of a pass over shared and own tokens (SharedParams): a prefix, or a sequence without its prefix.
+struct SharedSeq : AttnSeq {
+    int lo;                      // tokens from here on
+    int row;                     // of the block table (b: number of the set)
+};
+// Tokens that a set leaves out; its row of the block table.
+__device__ __forceinline__ int attn_lo(const AttnSeq &) { return 0; }
+__device__ __forceinline__ int attn_lo(const SharedSeq &s) { return s.lo; }
+__device__ __forceinline__ int attn_table_row(const AttnSeq &s) { return s.b; }
+__device__ __forceinline__ int attn_table_row(const SharedSeq &s) { return s.row; }
+
 struct AttnParams {
+    using Seq = AttnSeq;
+    static constexpr bool SHARED = false;
     const uint16_t *q;                   // bf16
     int64_t q_stride;
     KvCacheDev cache;
@@ -176,13 +193,8 @@ template <int FMT> __device__ __forceinline__ bool any_wide_scale(uint32_t w)
     return (w & lo) == lo || (w & hi) == hi;
 }
 
-// One sequence as the kernels work on it.
-struct AttnSeq {
-    int b, q0, T, ctx, len;      // first query token, new tokens, context and all cached tokens
-};
-
 // Sequence b with its lengths made to fit; `bad` collects BQG_DEVERR_LENGTH.
-__device__ __forceinline__ AttnSeq attn_seq(const AttnParams &p, int b, int &bad)
+__device__ __forceinline__ AttnSeq attn_own_seq(const AttnParams &p, int b, int &bad)
 {
     AttnSeq s;
     s.b = b;
@@ -195,6 +207,96 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams &p, int b, int &bad
     s.q0 = (int)q0; s.T = (int)T; s.ctx = (int)ctx;
     s.len = (int)min(ctx + T, cap);
     return s;
+}
+__device__ __forceinline__ AttnSeq attn_seq(const AttnParams &p, int b, int &bad) { return attn_own_seq(p, b, bad); }
+
+// Attention where sequences share their first tokens.  With x the scores of a row, A its shared tokens and B its own,
+//     softmax(x) v = (sum_A e^(x - m) v + sum_B e^(x - m) v) / (sum_A e^(x - m) + sum_B e^(x - m)),
+// so the two sums are taken apart, each relative to a maximum of its own, and put together: the kernels here run
+// twice.  In the first pass a set is a prefix: its rows are the new tokens of all its sequences, which all
+// see all of it, so its keys and values are read once for each 128 or 256 rows (up to 16: once), not once per sequence.  Its
+// unnormalised rows, maxima and sums stay in the workspace in fp32.  In the second a set is a sequence without its
+// prefix; what finishes a row adds the first pass's to it.
+struct SharedParams : AttnParams {
+    using Seq = SharedSeq;
+    static constexpr bool SHARED = true;
+    const int32_t *prefix_len, *seq_start;   // [n_prefix], [n_prefix + 1] (null: one prefix, all sequences)
+    int n_prefix, n_all;                     // prefixes, sequences (n_seq: sets of this pass)
+    int64_t max_shared;                      // new tokens behind one prefix at most
+    int own;                                 // the second pass
+    float *rows, *rows_ml;                   // [n_tokens][n_q][D] unnormalised, (maximum, sum) pairs
+};
+// Prefix g: its sequences, their query tokens and the shared tokens (none where the arguments do not fit, which
+// `bad` then tells: both passes come to the same answer).
+struct SharedGroup { int s0, s1, q0, T, len; };
+__device__ __forceinline__ int64_t attn_cap(const AttnParams &p) { return min((int64_t)0x7fff0000, p.max_pages << p.cache.lp); }
+__device__ __forceinline__ SharedGroup shared_group(const SharedParams &p, int g, int &bad)
+{
+    SharedGroup r;
+    const int a = p.seq_start ? p.seq_start[g] : 0, e = p.seq_start ? p.seq_start[g + 1] : p.n_all;
+    r.s0 = min(max(a, 0), p.n_all);
+    r.s1 = min(max(e, r.s0), p.n_all);
+    const int64_t q0 = min(max((int64_t)p.q_start[r.s0], (int64_t)0), p.n_tokens);
+    const int64_t q1 = min(max((int64_t)p.q_start[r.s1], q0), p.n_tokens);
+    const int64_t n = p.prefix_len[g];
+    r.q0 = (int)q0; r.T = (int)(q1 - q0);
+    r.len = (int)min(max(n, (int64_t)0), attn_cap(p));
+    if (r.s0 != a || r.s1 != e || r.len != n || q1 - q0 > p.max_shared) bad |= BQG_DEVERR_LENGTH;
+    if (q1 - q0 > p.max_shared || r.s0 == r.s1) r.len = 0;
+    return r;
+}
+__device__ __forceinline__ SharedSeq attn_seq(const SharedParams &p, int b, int &bad)
+{
+    SharedSeq s;
+    if (!p.own) {
+        const SharedGroup g = shared_group(p, b, bad);
+        s.b = b;
+        s.row = g.s0;                                // its pages are the first sequence's
+        s.q0 = g.q0;
+        s.T = g.len ? g.T : 0;
+        s.ctx = s.len = g.len;
+        s.lo = 0;
+        return s;
+    }
+    int g = 0;                                       // the last prefix that begins at b or before
+    if (p.seq_start)
+        for (int n = p.n_prefix; n > 1; n -= n >> 1)
+            if (p.seq_start[g + (n >> 1)] <= b) g += n >> 1;
+    int known = 0;                                   // (the first pass reports it)
+    const SharedGroup r = shared_group(p, g, known);
+    static_cast<AttnSeq &>(s) = attn_own_seq(p, b, bad);
+    s.row = b;
+    s.lo = r.s0 <= b && b < r.s1 ? r.len : 0;
+    if (s.ctx < s.lo) {
+        if (s.T) bad |= BQG_DEVERR_LENGTH;
+        s.ctx = s.lo;
+        s.len = (int)min((int64_t)s.lo + s.T, attn_cap(p));
+    }
+    return s;
+}
+// Row `row` of (set, KV head) in SharedParams::rows.
+__device__ __forceinline__ int64_t shared_row(const SharedParams &p, const SharedSeq &s, int h, int row)
+{
+    const int i = row / p.group;
+    return (int64_t)(s.q0 + i) * p.n_q + h * p.group + (row - i * p.group);
+}
+// The set that lane `from` holds (but for its number).
+__device__ __forceinline__ AttnSeq attn_shfl(const AttnSeq &s, int from)
+{
+    AttnSeq r;
+    r.q0 = __shfl_sync(0xffffffffu, s.q0, from);
+    r.T = __shfl_sync(0xffffffffu, s.T, from);
+    r.ctx = __shfl_sync(0xffffffffu, s.ctx, from);
+    r.len = __shfl_sync(0xffffffffu, s.len, from);
+    return r;
+}
+__device__ __forceinline__ SharedSeq attn_shfl(const SharedSeq &s, int from)
+{
+    SharedSeq r;
+    static_cast<AttnSeq &>(r) = attn_shfl(static_cast<const AttnSeq &>(s), from);
+    r.lo = __shfl_sync(0xffffffffu, s.lo, from);
+    r.row = __shfl_sync(0xffffffffu, s.row, from);
+    return r;
 }
 
 // Row `row` (new token row / group, head row % group) of (sequence, KV head): its query, or null past the last.
@@ -222,13 +324,18 @@ __device__ __forceinline__ void attn_check_ends(const AttnParams &p, int &bad)
 {
     if (p.q_start[0] != 0 || p.q_start[p.n_seq] != p.n_tokens) bad |= BQG_DEVERR_LENGTH;
 }
+__device__ __forceinline__ void attn_check_ends(const SharedParams &p, int &bad)
+{
+    if (p.q_start[0] != 0 || p.q_start[p.n_all] != p.n_tokens) bad |= BQG_DEVERR_LENGTH;
+    if (p.seq_start && (p.seq_start[0] != 0 || p.seq_start[p.n_prefix] != p.n_all)) bad |= BQG_DEVERR_LENGTH;
+}
 // The units (weight(sequence) of them) of all sequences, and BQG_DEVERR_LENGTH in `bad` of some lanes; s and `mine`:
 // sequence `lane` and its units.  Called by whole warps, as attn_find is, which takes them on.
-template <typename W>
-__device__ __forceinline__ int64_t attn_total(const AttnParams &p, int lane, W weight, int &bad, AttnSeq &s, int64_t &mine)
+template <typename P, typename W>
+__device__ __forceinline__ int64_t attn_total(const P &p, int lane, W weight, int &bad, typename P::Seq &s, int64_t &mine)
 {
     mine = 0;
-    s = AttnSeq{};
+    s = typename P::Seq{};
     if (lane < p.n_seq) {
         s = attn_seq(p, lane, bad);
         mine = weight(s);
@@ -240,9 +347,9 @@ __device__ __forceinline__ int64_t attn_total(const AttnParams &p, int lane, W w
     return total;
 }
 // The sequence that holds number u (below the total) of the line of all sequences' units; `base`: the number of its first.
-template <typename W>
-__device__ __forceinline__ AttnSeq attn_find(const AttnParams &p, int64_t u, int lane, W weight, AttnSeq s, int64_t mine,
-                                             int64_t &base)
+template <typename P, typename W>
+__device__ __forceinline__ typename P::Seq attn_find(const P &p, int64_t u, int lane, W weight, typename P::Seq s, int64_t mine,
+                                                     int64_t &base)
 {
     base = 0;
     for (int b0 = 0; b0 < p.n_seq; b0 += 32) {
@@ -264,12 +371,8 @@ __device__ __forceinline__ AttnSeq attn_find(const AttnParams &p, int64_t u, int
         if (past) {
             const int first = __ffs(past) - 1;
             base += __shfl_sync(0xffffffffu, sum - mine, first);
-            AttnSeq r;
+            typename P::Seq r = attn_shfl(s, first);
             r.b = b0 + first;
-            r.q0 = __shfl_sync(0xffffffffu, s.q0, first);
-            r.T = __shfl_sync(0xffffffffu, s.T, first);
-            r.ctx = __shfl_sync(0xffffffffu, s.ctx, first);
-            r.len = __shfl_sync(0xffffffffu, s.len, first);
             return r;
         }
         base += __shfl_sync(0xffffffffu, sum, 31);
@@ -367,8 +470,11 @@ template <int FMT, int D, int RT> struct AttnKernel {
     static constexpr int MT = D / 16;                         // M tiles of the second product
 
     // 64-token tiles of a sequence, and its units: all its rows (new tokens x heads of a group, at most ROWS) at once.
-    static __device__ __forceinline__ int tiles_of(const AttnSeq &s) { return (s.len + kUnit - 1) / kUnit; }
-    static __device__ __forceinline__ int64_t units(const AttnParams &p, const AttnSeq &s, int lead)
+    template <typename Seq> static __device__ __forceinline__ int tiles_of(const Seq &s)
+    {
+        return (s.len + kUnit - 1) / kUnit - attn_lo(s) / kUnit;
+    }
+    template <typename Seq> static __device__ __forceinline__ int64_t units(const AttnParams &p, const Seq &s, int lead)
     {
         return s.T ? (int64_t)p.cache.n_kv * (tiles_of(s) + lead) : 0;
     }
@@ -691,9 +797,10 @@ template <int RT, int KS> struct QShared {
     }
 };
 
-template <int FMT, int D, int RT>
-__global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams p, int *error)
+template <int FMT, int D, int RT, typename P = AttnParams>
+__global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *error)
 {
+    using Seq = typename P::Seq;
     using G = AttnGeom<FMT, D, RT>;
     using A = AttnKernel<FMT, D, RT>;
     constexpr int S = G::S, MT = A::MT;
@@ -716,9 +823,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
     // for short contexts.  With fewer sets a CTA has one piece or is near it, and its range is better left as it is.
     int bad = 0;
     const int lead = 2 * (int64_t)p.n_seq * p.cache.n_kv >= gridDim.x ? kLead : 0;
-    auto weight = [&](const AttnSeq &q) { return A::units(p, q, lead); };
+    auto weight = [&](const Seq &q) { return A::units(p, q, lead); };
     int64_t mine;
-    AttnSeq s;
+    Seq s;
     const int64_t total = attn_total(p, lane, weight, bad, s, mine);
     if (blockIdx.x == 0 && warp == 0) {
         attn_check_ends(p, bad);
@@ -741,7 +848,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
         const int tiles = A::tiles_of(s);
         const int h = (int)div_pos(off, tiles + lead), first = (int)(off - (int64_t)h * (tiles + lead));
         const int take = (int)min((int64_t)(tiles + lead - first), u_end - u);
-        const int tile0 = max(first - lead, 0), n = first + take - lead - tile0;   // units of this piece
+        const int tile0 = max(first - lead, 0) + attn_lo(s) / kUnit;
+        const int n = first + take - lead + attn_lo(s) / kUnit - tile0;       // units of this piece
         if (n <= 0) {
             u += take;
             continue;
@@ -751,11 +859,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
 
         // strips of this warp: tokens 64 (tile0 + j) + 16 warp ..
         const uint32_t ring = sb + warp * S * G::STAGE;
-        const int32_t *table = p.table + (int64_t)s.b * p.max_pages;
+        const int32_t *table = p.table + (int64_t)attn_table_row(s) * p.max_pages;
         // pages of the warp's strips j0 .. j0 + 31, one per lane
         auto pages_from = [&](int j0) {
             const int tok0 = (tile0 + j0 + lane) * kUnit + warp * kStrip;
-            return (j0 + lane < n && tok0 < s.len) ? table[tok0 >> p.cache.lp] : -1;
+            return (j0 + lane < n && tok0 < s.len && tok0 + kStrip > attn_lo(s)) ? table[tok0 >> p.cache.lp] : -1;
         };
         int pages = pages_from(0);
         // queries (their loads are under way when the first strips are requested)
@@ -772,7 +880,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
             const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
             const int page = __shfl_sync(0xffffffffu, pages, j & 31);
             valid &= ~(1u << st);
-            if (j < n && tok0 < s.len) {
+            if (j < n && tok0 < s.len && tok0 + kStrip > attn_lo(s)) {
                 const bool ok = page >= 0 && page < p.cache.n_pages;
                 if (!ok) pages_bad = BQG_DEVERR_PAGE;
                 valid |= (unsigned)ok << st;
@@ -845,10 +953,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
             const uint32_t st = ring + stage * G::STAGE;
             const bool ok = (valid >> stage) & 1;
             stage = stage + 1 == S ? 0 : stage + 1;
+            if (P::SHARED && tok0 + kStrip <= attn_lo(s)) continue;           // all of it is shared
 
             float sc[RT][4];
             A::scores(st, lane, qf, sb + G::OFF_BIAS + t * 8, sc);
-            const bool edge = tok0 + kStrip > s.ctx || !ok;                   // new tokens, the end, or no page
+            const bool edge = tok0 + kStrip > s.ctx || !ok || tok0 < attn_lo(s);   // new tokens, the end, no page, shared ones
             if (edge) {
 #pragma unroll
                 for (int m = 0; m < RT; m++)
@@ -858,7 +967,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
 #pragma unroll
                         for (int x = 0; x < 2; x++) {
                             const int tok = tok0 + 8 * x + g;
-                            const bool see = ok && (tok < s.ctx || (tok < s.len && ((sees >> (tok - s.ctx)) & 1)));
+                            const bool see = ok && tok >= attn_lo(s) && (tok < s.ctx || (tok < s.len && ((sees >> (tok - s.ctx)) & 1)));
                             if (!see) sc[m][2 * x + r] = NEG;
                         }
                     }
@@ -979,6 +1088,28 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const AttnParams 
                     for (int e = 0; e < E; e++) v[e] += c * src[e];
                 }
                 if (last) {
+                    if constexpr (P::SHARED) {
+                        const int64_t at = shared_row(p, s, h, row);
+                        float *shared = p.rows + at * D + lane * E;
+                        if (!p.own) {
+#pragma unroll
+                            for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(shared + e) = make_float2(v[e], v[e + 1]);
+                            if (lane == 0) *reinterpret_cast<float2 *>(p.rows_ml + at * 2) = make_float2(mt, l);
+                            continue;
+                        }
+                        if (s.lo) {
+                            const float2 q = __ldcg(reinterpret_cast<const float2 *>(p.rows_ml + at * 2));
+                            const float up = fmaxf(mt, q.x);
+                            const float a = mt == up ? 1.f : ex2(mt - up), b = q.x == up ? 1.f : ex2(q.x - up);
+                            l = l * a + q.y * b;
+#pragma unroll
+                            for (int e = 0; e < E; e += 2) {
+                                const float2 f = __ldcg(reinterpret_cast<const float2 *>(shared + e));
+                                v[e] = v[e] * a + f.x * b;
+                                v[e + 1] = v[e + 1] * a + f.y * b;
+                            }
+                        }
+                    }
                     attn_store_row<E>(out_row(row), v, l);
                 } else {
                     const int64_t at = attn_slot_row<G::ROWS>(cta, c0, row);

@@ -78,12 +78,12 @@ inline double attn_most(const AttnParams &p, int tile, int rows)
 }
 
 // mma.sync kernel: plans the call (plan) or, plan null, launches it.
-template <int FMT, int D, int RT>
-cudaError_t attn_rows_call(AttnParams p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+template <int FMT, int D, int RT, typename P>
+cudaError_t attn_rows_call(P p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
     using G = AttnGeom<FMT, D, RT>;
     struct Kern {
-        void (*fn)(const AttnParams, int *) = attn_kernel<FMT, D, RT>;
+        void (*fn)(const P, int *) = attn_kernel<FMT, D, RT, P>;
         int most = kAttnMaxCtas;
     } kern;
     int ctas = 0;
@@ -101,11 +101,11 @@ cudaError_t attn_rows_call(AttnParams p, int *error, AttnPlan *plan, cudaStream_
 }
 
 // tcgen05 kernel and its join.
-template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+template <int FMT, int D, typename P> cudaError_t attn_tc_call(P p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
     using G = TcGeom<FMT, D>;
     struct Kern {
-        void (*fn)(const AttnParams, const CUtensorMap, const CUtensorMap, int *) = attn_tc_kernel<FMT, D>;
+        void (*fn)(const P, const CUtensorMap, const CUtensorMap, int *) = attn_tc_kernel<FMT, D, P>;
         int most = (int)(kAttnSetBytes / sizeof(TcSet));
     } kern;
     int ctas = 0;
@@ -139,17 +139,51 @@ template <int FMT, int D> cudaError_t attn_tc_call(AttnParams p, int *error, Att
     if (cudaError_t e = cudaLaunchKernelEx(&cfg, kern.fn, p, kmap, vmap, error)) return e;
     if (grid == 1) return cudaSuccess;                              // nothing is shared
     // the join may be set up while the first kernel runs: it waits for it before it reads
-    const int rows = std::min(G::ROWS, p.max_q * p.group);
+    const int rows = (int)std::min<int64_t>(G::ROWS, (int64_t)p.max_q * p.group);
     attn_config(cfg, attr, dim3(grid, (rows + 31) / 32), 256, 0, s, true);
-    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D, G::ROWS>, p, grid);
+    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D, G::ROWS, P>, p, grid);
 }
 
-template <int FMT, int D> cudaError_t attn_pick(const AttnParams &p, int rows, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+template <int FMT, int D, typename P> cudaError_t attn_pick(const P &p, int64_t rows, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
-    if (rows <= 8) return attn_rows_call<FMT, D, 1>(p, error, plan, s, pdl);
+    if (rows <= 8) return attn_rows_call<FMT, D, 1, P>(p, error, plan, s, pdl);
     if constexpr (kAttnTcRows<FMT, D> > 9)
-        if (rows < kAttnTcRows<FMT, D>) return attn_rows_call<FMT, D, 2>(p, error, plan, s, pdl);
-    return attn_tc_call<FMT, D>(p, error, plan, s, pdl);
+        if (rows < kAttnTcRows<FMT, D>) return attn_rows_call<FMT, D, 2, P>(p, error, plan, s, pdl);
+    return attn_tc_call<FMT, D, P>(p, error, plan, s, pdl);
+}
+
+// Shared tokens, then own ones (SharedParams).  Workspace: as for one pass, then the first one's rows.
+template <int FMT, int D>
+cudaError_t shared_call(SharedParams p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    SharedParams pre = p;
+    pre.own = 0;
+    pre.n_seq = p.n_prefix;
+    pre.max_q = (int)p.max_shared;
+    p.own = 1;
+    AttnPlan a, b;
+    const int64_t rows = (int64_t)p.max_q * p.group, shared = p.max_shared * p.group;
+    if (cudaError_t e = attn_pick<FMT, D>(pre, shared, error, &a, s, pdl)) return e;
+    if (cudaError_t e = attn_pick<FMT, D>(p, rows, error, &b, s, pdl)) return e;
+    const size_t at = (std::max(a.ws_bytes, b.ws_bytes) + 255) & ~(size_t)255, all = (size_t)p.n_tokens * p.n_q;
+    if (plan) {
+        plan->ws_bytes = at + all * (D + 2) * sizeof(float);
+        return cudaSuccess;
+    }
+    pre.rows = p.rows = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.counters) + at);
+    pre.rows_ml = p.rows_ml = p.rows + all * D;
+    if (cudaError_t e = attn_pick<FMT, D>(pre, shared, error, nullptr, s, pdl)) return e;
+    // the second pass may be set up while the first runs: it waits for it before it reads
+    return attn_pick<FMT, D>(p, rows, error, nullptr, s, true);
+}
+template <int FMT> cudaError_t shared_launch(const SharedParams &p, int D, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    int *error = nullptr;
+    if (!plan)
+        if (cudaError_t e = device_error_word(&error)) return e;
+    if (D == 64) return shared_call<FMT, 64>(p, error, plan, s, pdl);
+    if (D == 128) return shared_call<FMT, 128>(p, error, plan, s, pdl);
+    return shared_call<FMT, 256>(p, error, plan, s, pdl);
 }
 
 // rows: the most rows (new tokens x heads of a group) of any sequence.

@@ -66,7 +66,8 @@ constexpr int kTcMarks = 32;             // tiles or pieces that the copying war
 // A set of tiles shared by several CTAs, as its first CTA describes it for the join (rows 0: none).
 struct TcSet {
     int rows, row0, h, q0;      // rows of the group, the first one; KV head; the sequence's first query token
-    int c0, c1, pad0, pad1;     // CTAs
+    int c0, c1;                 // CTAs
+    int lo, pad;                // tokens left out (SharedSeq)
 };
 
 template <int FMT, int D> struct TcGeom {
@@ -135,8 +136,8 @@ template <bool QUANT> __device__ __forceinline__ int tc_v_pos(int before, int t,
 }
 
 // The pieces of one CTA: consecutive tiles of one (sequence, KV head, row group).
-struct alignas(16) TcPiece {
-    AttnSeq s;
+template <typename Seq> struct alignas(16) TcPieceOf {
+    Seq s;
     int h, row0, rows;          // first row of the group, its rows
     int nq;                     // 2: the streams are two halves of the rows; 1: of each tile's tokens
     int tile0, n;               // tiles of the piece
@@ -148,21 +149,25 @@ struct alignas(16) TcPiece {
 // than CTAs, or few of unlike lengths) each takes an equal range of the line of all units.
 // 8 x 5000 tokens q8_0, 64 such groups on 152 CTAs: 46 us with one piece each, 50 with ranges.
 template <int NQ> constexpr int kTcSecond = NQ == 2 ? 10 : 5;
-static_assert(sizeof(TcPiece) == 64, "two pieces in shared memory");
-template <int NQ, int TT> struct TcWork {
+static_assert(sizeof(TcPieceOf<AttnSeq>) == 64 && sizeof(TcPieceOf<SharedSeq>) == 64, "two pieces in shared memory");
+template <int NQ, int TT, typename P> struct TcWork {
+    using Seq = typename P::Seq;
+    using TcPiece = TcPieceOf<Seq>;
     int64_t per, cur, end, base;
     int most;                   // units of a piece where each CTA has one; 0: ranges of `per` units
-    AttnSeq s;
-    __device__ static __forceinline__ int64_t cost(const AttnParams &p, const AttnSeq &q)
+    Seq s;
+    // tiles of a sequence
+    __device__ static __forceinline__ unsigned tiles_of(const Seq &q) { return (q.len + TT - 1) / TT - attn_lo(q) / TT; }
+    __device__ static __forceinline__ int64_t cost(const P &p, const Seq &q)
     {
-        const int tiles = (q.len + TT - 1) / TT, halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
+        const int tiles = tiles_of(q), halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
         return (int64_t)p.cache.n_kv * tiles * halves;
     }
     // pieces of at most `most` units (a multiple of NQ) of a KV head: of a row group with NQ halves, of one with fewer, of all
     struct Pieces { int groups, full, rest, head; };
-    __device__ static __forceinline__ Pieces pieces(const AttnParams &p, const AttnSeq &q, int most)
+    __device__ static __forceinline__ Pieces pieces(const P &p, const Seq &q, int most)
     {
-        const unsigned tiles = (q.len + TT - 1) / TT, halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
+        const unsigned tiles = tiles_of(q), halves = (q.T * p.group + kTcHalf - 1) / kTcHalf;
         Pieces r;
         r.groups = halves / NQ;
         r.full = (tiles * NQ + most - 1) / (unsigned)most;
@@ -170,9 +175,9 @@ template <int NQ, int TT> struct TcWork {
         r.head = r.groups * r.full + r.rest;
         return r;
     }
-    __device__ __forceinline__ void init(const AttnParams &p, int lane, int &bad)
+    __device__ __forceinline__ void init(const P &p, int lane, int &bad)
     {
-        auto weight = [&](const AttnSeq &q) { return cost(p, q); };
+        auto weight = [&](const Seq &q) { return cost(p, q); };
         int64_t mine;
         const int64_t total = attn_total(p, lane, weight, bad, s, mine);
         // at least NQ, so that every range between a set's first and last holds the beginning of a tile
@@ -195,7 +200,7 @@ template <int NQ, int TT> struct TcWork {
             }
         }
         if (most) {
-            auto number = [&](const AttnSeq &q) { return (int64_t)p.cache.n_kv * pieces(p, q, most).head; };
+            auto number = [&](const Seq &q) { return (int64_t)p.cache.n_kv * pieces(p, q, most).head; };
             mine = lane < p.n_seq ? number(s) : 0;
             cur = blockIdx.x;
             end = min(cur + 1, (int64_t)count(most));
@@ -208,13 +213,13 @@ template <int NQ, int TT> struct TcWork {
         base = 0;
         if (cur < end) s = attn_find(p, cur, lane, weight, s, mine, base);
     }
-    __device__ __forceinline__ bool next(const AttnParams &p, TcPiece &o)
+    __device__ __forceinline__ bool next(const P &p, TcPiece &o)
     {
         if (most) {
             if (cur >= end) return false;
             const Pieces n = pieces(p, s, most);
             const unsigned off = (unsigned)(cur - base), rem = off % (unsigned)n.head;
-            const unsigned tiles = (s.len + TT - 1) / TT;
+            const unsigned tiles = tiles_of(s);
             o.h = off / (unsigned)n.head;
             const int g = min((int)(rem / (unsigned)n.full), n.groups);
             const unsigned j = rem - g * n.full, k = g < n.groups ? n.full : n.rest;               // piece j of k
@@ -225,6 +230,7 @@ template <int NQ, int TT> struct TcWork {
             o.n = tiles / k + (j < tiles % k);
             o.c0 = blockIdx.x - j;
             o.c1 = o.c0 + k - 1;
+            o.tile0 += attn_lo(s) / TT;
             o.s = s;
             cur = end;
             return true;
@@ -235,7 +241,7 @@ template <int NQ, int TT> struct TcWork {
                 base += cost(p, s);
                 s = attn_seq(p, s.b + 1, ignored);
             }
-            const int tiles = (s.len + TT - 1) / TT, all = s.T * p.group;
+            const int tiles = tiles_of(s), all = s.T * p.group;
             const int halves = (all + kTcHalf - 1) / kTcHalf, groups = (halves + NQ - 1) / NQ;
             const int64_t off = cur - base, head = (int64_t)tiles * halves;
             o.h = (int)div_pos(off, head);
@@ -252,6 +258,7 @@ template <int NQ, int TT> struct TcWork {
             if (o.n <= 0) continue;
             o.c0 = (int)div_pos(seg, per);
             o.c1 = (int)div_pos(seg + (int64_t)(tiles - 1) * o.nq, per);
+            o.tile0 += attn_lo(s) / TT;
             o.s = s;
             return true;
         }
@@ -384,13 +391,18 @@ template <int FMT, int D> __device__ float tc_nonfinite(const KvCacheDev &c, int
     else return fabsf(f) < 65520.f ? 0.f : f * __int_as_float(0x7f800000);    // 65520 and above round to an infinity in fp16
 }
 
+// Whether this launch's rows are the call's results.
+__device__ __forceinline__ bool tc_own(const AttnParams &) { return true; }
+__device__ __forceinline__ bool tc_own(const SharedParams &p) { return p.own; }
+
 // Partial results of a piece: values in groups of four, [slot][D / 4][rows][4] (a warp's 32 rows are then
 // 512 contiguous bytes), and (maximum, sum) [slot][rows].
-template <int FMT, int D>
+template <int FMT, int D, typename P = AttnParams>
 __global__ void __launch_bounds__(TcGeom<FMT, D>::THREADS, 1)
-attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int *error)
+attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int *error)
 {
     using G = TcGeom<FMT, D>;
+    using TcPiece = TcPieceOf<typename P::Seq>;
     constexpr bool BF = (FMT == BQG_BF16);
     constexpr float NEG = -__builtin_huge_valf();
     constexpr float kShift = BF ? 0.0f : 8.0f;
@@ -562,13 +574,17 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     tmem_ld32_nowait(ts + 32, v1);
                     tmem_wait_ld(v0);
                     tmem_wait_ld(v1);
-                    if (tok0 + 64 > w.s.ctx || dead) {                   // tokens that this row does not see
+                    if (tok0 + 64 > w.s.ctx || dead || tok0 < attn_lo(w.s)) {   // tokens that this row does not see
 #pragma unroll
                         for (int c = 0; c < 2; c++) {
                             const int t0 = tok0 + 32 * c, before = w.s.ctx - t0, all = w.s.len - t0;
                             uint32_t m = before >= 32 ? ~0u : before > 0 ? (1u << before) - 1 : 0u;
                             if (before < 32) m |= before > 0 ? (uint32_t)sees << before : -before < 64 ? (uint32_t)(sees >> -before) : 0u;
                             m &= all >= 32 ? ~0u : all > 0 ? (1u << all) - 1 : 0u;
+                            if constexpr (P::SHARED) {
+                                const int shared = w.s.lo - t0;
+                                m &= shared >= 32 ? 0u : shared > 0 ? ~0u << shared : ~0u;
+                            }
                             if ((dead >> (2 * c)) & 1) m &= 0xffff0000u;
                             if ((dead >> (2 * c + 1)) & 1) m &= 0x0000ffffu;
 #pragma unroll
@@ -647,6 +663,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             const int x0 = both ? st * (D / 2) : 0, x1 = both ? x0 + D / 2 : D;
             const bool marked = nan_mark[pieces % kTcMarks] == (uint32_t)pieces + 1;
             const int64_t slot = attn_slot_row<1>(blockIdx.x, w.c0, 0);
+            float lj = l;                                                    // with the shared tokens'
             if (warp_ok) {
 #pragma unroll 1
                 for (int x = x0; x < x1; x += 32) {
@@ -670,7 +687,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                         const int a = max(w.s.ctx, w.tile0 * G::TT), e = min(w.s.len, (w.tile0 + w.n) * G::TT);
 #pragma unroll 1
                         for (int t = a; t < e; t++) {
-                            const int page = p.table[(int64_t)w.s.b * p.max_pages + (t >> p.cache.lp)];
+                            const int page = p.table[(int64_t)attn_table_row(w.s) * p.max_pages + (t >> p.cache.lp)];
                             if (page < 0 || page >= p.cache.n_pages) continue;
                             const int64_t crow = kv_row(p.cache, ((int64_t)page << p.cache.lp) + (t & ((1 << p.cache.lp) - 1)), w.h);
                             const bool see = (sees >> (t - w.s.ctx)) & 1;
@@ -681,7 +698,30 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                             }
                         }
                     }
-                    if (row_ok && w.c0 == w.c1) {
+                    if constexpr (P::SHARED)
+                        if (row_ok && w.c0 == w.c1) {
+                            const int64_t at = shared_row(p, w.s, w.h, row);
+                            float4 *shared = reinterpret_cast<float4 *>(p.rows + at * D + x);
+                            if (!p.own) {
+#pragma unroll
+                                for (int y = 0; y < 32; y += 4) shared[y / 4] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+                            } else if (w.s.lo) {
+                                const float2 q = *reinterpret_cast<const float2 *>(p.rows_ml + at * 2);
+                                const float up = fmaxf(mt, q.x);
+                                const float a = mt == up ? 1.f : ex2(mt - up), b = q.x == up ? 1.f : ex2(q.x - up);
+                                if (x == x0) lj = l * a + q.y * b;
+#pragma unroll
+                                for (int y = 0; y < 32; y += 4) {
+                                    const float4 f = shared[y / 4];
+                                    v[y] = v[y] * a + f.x * b; v[y + 1] = v[y + 1] * a + f.y * b;
+                                    v[y + 2] = v[y + 2] * a + f.z * b; v[y + 3] = v[y + 3] * a + f.w * b;
+                                }
+                            }
+                        }
+                    if (P::SHARED && !tc_own(p) && w.c0 == w.c1) {
+                        // (a prefix's rows have been written)
+                    } else if (row_ok && w.c0 == w.c1) {
+                        const float l = lj;
                         const float inv_l = l == 0.f ? 0.f : 1.0f / l;
                         uint16_t *dst = p.out + ((int64_t)(w.s.q0 + qi) * p.n_q + w.h * p.group + qh) * D + x;
 #pragma unroll
@@ -697,10 +737,13 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 }
             }
             tc_fence_before();
+            if constexpr (P::SHARED)
+                if (!p.own && w.c0 == w.c1 && row_ok && (w.nq == 2 || st == 0))
+                    *reinterpret_cast<float2 *>(p.rows_ml + shared_row(p, w.s, w.h, row) * 2) = make_float2(mt, l);
             if (w.c0 != w.c1) {
                 if (row_ok && (w.nq == 2 || st == 0))
                     *reinterpret_cast<float2 *>(part_ml + (slot * G::ROWS + grow) * 2) = make_float2(mt, l);
-                if (w.c0 == (int)blockIdx.x) set = TcSet{w.rows, w.row0, w.h, w.s.q0, w.c0, w.c1, 0, 0};
+                if (w.c0 == (int)blockIdx.x) set = TcSet{w.rows, w.row0, w.h, w.s.q0, w.c0, w.c1, attn_lo(w.s), 0};
             }
             tiles += w.n;
             pieces++;
@@ -816,6 +859,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 bool have;              // ... which exists
                 unsigned valid, dead;   // boxes that exist; 16-token strips without a page
                 int ctx, len, mark;     // first new token and end within the tile; mark of the piece
+                int lo;                 // tokens left out
             };
             constexpr int RING = G::QUANT ? NR : NS;
             int pieces = 0, tiles = 0, lands = 0;
@@ -830,7 +874,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     if (lane == 0) {
                         // tokens present, first new one (values only), page marks, mark of the piece
                         *reinterpret_cast<int4 *>(smem + G::OFF_SIDES + 16 * slot) =
-                            make_int4(q.len, side ? q.ctx : G::TT, (int)q.dead, q.mark);
+                            make_int4(q.len, side ? q.ctx : G::TT, (int)q.dead | (P::SHARED ? q.lo << 8 : 0), q.mark);
                         mbar_arrive_expect_tx(bar_rawf(slot), __popc(q.valid) * box * (G::RB + 2 * G::NB));
                     }
                     __syncwarp();
@@ -841,7 +885,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     }
                 } else {
                     const uint32_t dst = sb + G::OFF_RING + slot * G::TILE;
-                    const bool fix = side && (q.ctx < G::TT || q.dead);
+                    const bool fix = side && (q.ctx < G::TT || q.dead || (P::SHARED && q.lo));
                     const uint32_t bar = fix ? bar_land : bar_full(slot);
                     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(q.valid) * box * G::HALVES * 128);
                     __syncwarp();
@@ -855,7 +899,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                         bool hit = false;
                         constexpr int N = 4;                                 // chunks at a time (G::TT * D / 8 is a multiple of 32 N)
 #pragma unroll 1
-                        for (int i0 = (q.dead ? 0 : q.ctx) * (D / 8) / (32 * N) * (32 * N) + lane; i0 < G::TT * (D / 8); i0 += 32 * N) {
+                        for (int i0 = (q.dead || (P::SHARED && q.lo) ? 0 : q.ctx) * (D / 8) / (32 * N) * (32 * N) + lane; i0 < G::TT * (D / 8); i0 += 32 * N) {
                             uint4 v[N];
 #pragma unroll
                             for (int n = 0; n < N; n++) v[n] = lds128(dst + tc_chunk<G::TT>((i0 + 32 * n) / (D / 8), (i0 + 32 * n) % (D / 8)));
@@ -863,7 +907,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                             for (int n = 0; n < N; n++) {
                                 const int r = (i0 + 32 * n) / (D / 8), c = (i0 + 32 * n) % (D / 8);
                                 uint32_t u[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
-                                bool any = r >= q.len || ((q.dead >> (r >> 4)) & 1);
+                                bool any = r >= q.len || ((q.dead >> (r >> 4)) & 1) || (P::SHARED && r < q.lo);
                                 if (any) {
                                     u[0] = u[1] = u[2] = u[3] = 0;
                                 } else if (r >= q.ctx) {
@@ -884,10 +928,10 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                 }
             };
             while (ok && next()) {
-                const int32_t *table = p.table + (int64_t)w.s.b * p.max_pages;
+                const int32_t *table = p.table + (int64_t)attn_table_row(w.s) * p.max_pages;
                 auto page_of = [&](int t) {
                     const int tok = t * G::TT + lane * box;
-                    return (lane < boxes && tok < w.s.len) ? table[tok >> p.cache.lp] : -2;
+                    return (lane < boxes && tok < w.s.len && tok + box > attn_lo(w.s)) ? table[tok >> p.cache.lp] : -2;
                 };
                 int next_page = page_of(w.tile0);
                 for (int t = w.tile0; t < w.tile0 + w.n && ok; t++) {
@@ -899,10 +943,12 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
                     q.valid = __ballot_sync(0xffffffffu, q.have);
                     // strip i lies in box 16 i / box
                     q.dead = __ballot_sync(0xffffffffu, lane < G::TT / 16 && t * G::TT + 16 * lane < w.s.len &&
+                                                            t * G::TT + 16 * lane + 16 > attn_lo(w.s) &&
                                                             !((q.valid >> (16 * (lane & 7) / box)) & 1));
                     q.ctx = min(max(0, w.s.ctx - t * G::TT), G::TT);
                     q.len = min(w.s.len - t * G::TT, G::TT);
                     q.mark = pieces + 1;
+                    q.lo = min(max(0, attn_lo(w.s) - t * G::TT), G::TT);
                     if (side == 0 && lane == 0) {
                         dead_strips[(tiles + t - w.tile0) % kTcMarks] = (uint8_t)q.dead;
                         if (q.dead) atomicOr(error, BQG_DEVERR_PAGE);
@@ -921,7 +967,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
             // ---------------- the pieces, for all roles ----------------
             // one copy of this code: a CTA's first microseconds are mostly spent on fetching instructions
             int bad = 0;
-            TcWork<G::NQ, G::TT> work;
+            TcWork<G::NQ, G::TT, P> work;
             work.init(p, lane, bad);
             for (int i = 0; ok; i++) {
                 if (!work.next(p, w)) w.n = 0;
@@ -987,7 +1033,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
 #pragma unroll
                     for (int i = 0; i < M; i++) {
                         const int r = r0 + i * STEP;
-                        if (r >= side.x || ((side.z >> (r >> 4)) & 1)) scale[i] = 0;
+                        if (r >= side.x || ((side.z >> (r >> 4)) & 1) || (P::SHARED && r < side.z >> 8)) scale[i] = 0;
                         if (r >= side.y && (scale[i] & kWideScale<FMT>) == kWideScale<FMT>) hit = true;
                     }
                 }
@@ -1054,7 +1100,7 @@ attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap, con
 // Joins the pieces of the sets that several CTAs shared: 32 rows of one set
 // per CTA (blockIdx.x: the set's first CTA), one row per lane, an eighth of the values
 // per warp.  In the order of the CTAs.
-template <int D, int ROWS> __global__ void __launch_bounds__(256) attn_tc_join_kernel(const AttnParams p, int ctas)
+template <int D, int ROWS, typename P = AttnParams> __global__ void __launch_bounds__(256) attn_tc_join_kernel(const P p, int ctas)
 {
     pdl_wait();
     pdl_launch_dependents();
@@ -1091,6 +1137,30 @@ template <int D, int ROWS> __global__ void __launch_bounds__(256) attn_tc_join_k
             for (int i = 0; i < V; i++) {
                 v[4 * i] = v[4 * i] * w0 + w * a[n][i].x; v[4 * i + 1] = v[4 * i + 1] * w0 + w * a[n][i].y;
                 v[4 * i + 2] = v[4 * i + 2] * w0 + w * a[n][i].z; v[4 * i + 3] = v[4 * i + 3] * w0 + w * a[n][i].w;
+            }
+        }
+    }
+    if constexpr (P::SHARED) {
+        SharedSeq s{};
+        s.q0 = set.q0;
+        const int64_t at = shared_row(p, s, set.h, set.row0 + row);
+        float4 *shared = reinterpret_cast<float4 *>(p.rows + at * D + warp * 4 * V);
+        if (!p.own) {
+#pragma unroll
+            for (int i = 0; i < V; i++) shared[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (warp == 0) *reinterpret_cast<float2 *>(p.rows_ml + at * 2) = make_float2(mt, l);
+            return;
+        }
+        if (set.lo) {
+            const float2 q = *reinterpret_cast<const float2 *>(p.rows_ml + at * 2);
+            const float up = fmaxf(mt, q.x);
+            const float a = mt == up ? 1.f : ex2(mt - up), b = q.x == up ? 1.f : ex2(q.x - up);
+            l = l * a + q.y * b;
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+                const float4 f = shared[i];
+                v[4 * i] = v[4 * i] * a + f.x * b; v[4 * i + 1] = v[4 * i + 1] * a + f.y * b;
+                v[4 * i + 2] = v[4 * i + 2] * a + f.z * b; v[4 * i + 3] = v[4 * i + 3] * a + f.w * b;
             }
         }
     }

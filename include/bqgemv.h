@@ -391,6 +391,30 @@ int bqg_tree_attention(const void *q, int64_t q_stride, const bqg_kv_cache *cach
  * device; 0 when they are not valid. */
 size_t bqg_tree_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int n_seq, int max_q);
 
+/* The same attention where sequences share their first tokens: one prompt, sampled or branched many times.  Arguments and
+ * results are bqg_tree_attention's (ctx_len and block_table hold the shared tokens too), and the shared
+ * tokens' keys and values are read and multiplied once for all sequences behind them, not once for each.
+ * Sequences seq_start[g] .. seq_start[g + 1] - 1 begin with the same prefix_len[g] tokens: 0 <= prefix_len[g] <= the
+ * ctx_len of each.  These are taken from the pages of the first of them; tokens from there on come from each one's own
+ * (a prefix need not end with a page: the page where it ends is then read in part from both, and a place of it that is
+ * not needed is not read).  prefix_len: n_prefix int32; seq_start: n_prefix + 1 int32, ascending from 0, the last one
+ * n_seq; NULL: one prefix, which all sequences share.  max_shared: query tokens behind one
+ * prefix at most (it picks the kernels; n_tokens is always enough); a prefix with more counts as not shared, and
+ * BQG_DEVERR_LENGTH is set.  n_prefix >= 1; max_shared * n_q / n_kv at most 2^30.
+ * Roundings as bqg_tree_attention's, keys as codes for the shared tokens where max_shared * n_q / n_kv is at most 16, for
+ * the own ones where max_q * n_q / n_kv is; what the two parts come to is put together in fp32.
+ * ws: bqg_shared_prefix_attention_workspace_size(...) bytes, 16-byte aligned, ZERO before the first call on it; one made
+ * for more tokens, sequences or rows does.  Calls that share a workspace must not overlap.  Two to four launches. */
+int bqg_shared_prefix_attention(const void *q, int64_t q_stride, const bqg_kv_cache *cache, const int32_t *block_table,
+                                int64_t max_pages, const int32_t *ctx_len, const int32_t *q_start, int n_seq,
+                                int64_t n_tokens, int max_q, int n_q, const int32_t *prefix_len, const int32_t *seq_start,
+                                int n_prefix, int64_t max_shared, const uint64_t *mask, float scale, void *out, void *ws,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of bqg_shared_prefix_attention for these arguments on the current device; 0 when they are not valid. */
+size_t bqg_shared_prefix_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int n_seq, int max_q, int64_t n_tokens,
+                                                  int n_prefix, int64_t max_shared);
+
 /* Prefill GEMM ("llama-3x-prompt-speed", "the tile"): each weight tile is
  * dequantized once to bf16 into the tensor memory the MMA reads and fed to
  * the tensor cores with fp32 accumulation.  For K >= 1024 each weight
