@@ -71,6 +71,9 @@ EXPORTS = {
     "bqg_shared_prefix_attention": (["p", "i64", "p", "p", "i64", "p", "p", "i", "i64", "i", "i", "p", "p", "i", "i64", "p",
                                      "f", "p", "p", "size", "p"], "i"),
     "bqg_shared_prefix_attention_workspace_size": (["p", "i", "i", "i", "i64", "i", "i64"], "size"),
+    "bqg_tree_verify": (["p", "p", "i", "i64", "i64", "i64", "p", "p", "p", "i", "i64", "i", "p", "p", "p", "p", "p"], "i"),
+    "bqg_kv_compact": (["p", "p", "i64", "p", "p", "p", "i", "i", "p", "p"], "i"),
+    "bqg_kv_fork": (["p", "p", "i64", "i", "p", "p", "p", "p", "i", "p"], "i"),
     "bqg_gemv_q4_0_q8_1_noalloc": (["p", "p", "p", "i", "i64", "i64", "p"], "i"),
     "bqg_noalloc_scratch_bytes": ([], "size"),
 }
@@ -444,7 +447,7 @@ def debug_q4_0_q8_1_block_dots_kslice(Wp, Xq, N, K, out=None, stream=None):
 
 
 # --- attention over a paged cache ------------------------------------------------
-DEVERR_SLOT, DEVERR_POSITION, DEVERR_PAGE, DEVERR_LENGTH = 16, 32, 64, 128
+DEVERR_SLOT, DEVERR_POSITION, DEVERR_PAGE, DEVERR_LENGTH, DEVERR_ROW, DEVERR_DRAFT = 16, 32, 64, 128, 256, 512
 _KV_DTYPE = {BF16: torch.bfloat16, Q8_0: torch.int8, Q4_0: torch.uint8}
 
 
@@ -778,6 +781,88 @@ def shared_prefix_attention(q, cache: KVCache, block_table, ctx_len, q_start, ma
         dim ** -0.5 if scale is None else scale, op, wsp, wsb, _stream(stream)),
         "bqg_shared_prefix_attention")
     return out
+
+
+# --- verification of drafts, and what follows from it for the cache -------------
+def _rows(t, cur, name, shape, dtype):
+    """(pointer, row stride) of [rows, n] values, each row contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    check_device(t.device.index, cur, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {list(t.shape)}, needs {list(shape)}")
+    s = t.stride()
+    if t.numel() and shape[1] > 1 and s[1] != 1:
+        raise ValueError(f"each row of {name} must be contiguous")
+    return t.data_ptr(), s[0] if shape[0] > 1 else shape[1]
+
+
+def tree_verify(target, tokens, q_start, max_q: int, u, parent=None, draft=None, out=None, stream=None):
+    """Drafted tokens accepted or rejected against the target's probabilities, and the token that follows.
+
+    target [n_tokens, vocab], bf16 or fp32 (rows may lie apart): the distribution behind each token; tokens int32
+    [n_tokens], sequence after sequence (at most max_q <= 64 each), q_start int32 [n_seq + 1] their first ones, each
+    one's token 0 the last given out; parent int32 [n_tokens], the token of its sequence that a draft stands
+    behind, or None for chains; draft: as target, the distributions that the drafts were drawn from, or None for
+    drafts that were chosen; u fp32 [n_tokens], numbers in [0, 1).  Returns int32 (n_accepted [n_seq], path
+    [n_seq, max_q], next_token [n_seq]): how many tokens are kept, with token 0; their places, then -1; the next token."""
+    cur = _current_device()
+    if not isinstance(target, torch.Tensor) or target.dim() != 2:
+        raise ValueError("target must be a [n_tokens, vocab] tensor")
+    n, vocab = target.shape
+    dt = _x_dtype(target, "target")
+    tp, ts = _rows(target, cur, "target", (n, vocab), target.dtype)
+    dp, ds = (None, 0) if draft is None else _rows(draft, cur, "draft", (n, vocab), target.dtype)
+    n_seq = q_start.numel() - 1
+    if n_seq < 0:
+        raise ValueError("q_start must hold n_seq + 1 values")
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=target.device)
+        out = torch.empty(n_seq, **i32), torch.empty((n_seq, max(max_q, 0)), **i32), torch.empty(n_seq, **i32)
+    _check(load().bqg_tree_verify(tp, dp, dt, ts, ds, vocab, _vector(tokens, cur, "tokens", torch.int32, n),
+                                  None if parent is None else _vector(parent, cur, "parent", torch.int32, n),
+                                  _vector(q_start, cur, "q_start", torch.int32, n_seq + 1), n_seq, n, max_q,
+                                  _vector(u, cur, "u", torch.float32, n), _vector(out[0], cur, "out[0]", torch.int32, n_seq),
+                                  _vector(out[1], cur, "out[1]", torch.int32, n_seq * max(max_q, 0)),
+                                  _vector(out[2], cur, "out[2]", torch.int32, n_seq), _stream(stream)), "bqg_tree_verify")
+    return out
+
+
+def _table(t, cur):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("block_table must be [rows, max_pages]")
+    return _ptr(t, cur, "block_table", torch.int32, 0), t.shape
+
+
+def kv_compact(cache: KVCache, block_table, ctx_len, path, n_path, out=None, stream=None) -> torch.Tensor:
+    """The accepted path's keys and values moved behind the context: new token path[b, k] of sequence b goes to place
+    ctx_len[b] + k, for k < n_path[b] (path int32 [n_seq, max_q], ascending; as tree_verify gives them).  Returns the new
+    lengths ctx_len + n_path, int32 [n_seq] (`out` must not be ctx_len itself)."""
+    cur = _current_device()
+    bp, (n_seq, max_pages) = _table(block_table, cur)
+    if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[0] != n_seq:
+        raise ValueError("path must be [n_seq, max_q]")
+    if out is None:
+        out = torch.empty(n_seq, dtype=torch.int32, device=block_table.device)
+    _check(load().bqg_kv_compact(cache._handle(cur), bp, max_pages, _vector(ctx_len, cur, "ctx_len", torch.int32, n_seq),
+                                 _ptr(path, cur, "path", torch.int32, 0), _vector(n_path, cur, "n_path", torch.int32, n_seq),
+                                 n_seq, path.shape[1], _vector(out, cur, "out", torch.int32, n_seq), _stream(stream)),
+           "bqg_kv_compact")
+    return out
+
+
+def kv_fork(cache: KVCache, block_table, ctx_len, parent, child, fresh, stream=None) -> None:
+    """Sequences branched: row child[i] of block_table int32 [rows, max_pages] gets row parent[i]'s full pages and, as the
+    next one, page fresh[i] with a copy of the tokens in the parent's page in use; ctx_len int32 [rows] gets its length.
+    parent, child, fresh: int32 [n]; children distinct and no parents, fresh pages distinct and in no row.  In place."""
+    cur = _current_device()
+    bp, (rows, max_pages) = _table(block_table, cur)
+    n = parent.numel()
+    _check(load().bqg_kv_fork(cache._handle(cur), bp, max_pages, rows, _vector(ctx_len, cur, "ctx_len", torch.int32, rows),
+                              _vector(parent, cur, "parent", torch.int32, n), _vector(child, cur, "child", torch.int32, n),
+                              _vector(fresh, cur, "fresh", torch.int32, n), n, _stream(stream)), "bqg_kv_fork")
 
 
 # --- utilities -----------------------------------------------------------------

@@ -14,6 +14,8 @@
 #include "bqg_attn_launch.cuh"
 #include "bqg_gemv.cuh"
 #include "bqg_gemv_mma.cuh"
+#include "bqg_pages.cuh"
+#include "bqg_verify.cuh"
 
 namespace bqg {
 cudaError_t gemv_run_bf16(const GemvParams &, int, int, dim3, int, size_t, cudaStream_t, bool, int *);
@@ -1319,6 +1321,78 @@ size_t bqg_shared_prefix_attention_workspace_size(const bqg_kv_cache *cache, int
         return 0;
     AttnPlan plan;
     return shared_run(cache->fmt, p, cache->head_dim, &plan, 0, false) == cudaSuccess ? plan.ws_bytes : 0;
+}
+
+int bqg_tree_verify(const void *target, const void *draft, int x_dtype, int64_t target_stride, int64_t draft_stride,
+                    int64_t vocab, const int32_t *tokens, const int32_t *parent, const int32_t *q_start, int n_seq,
+                    int64_t n_tokens, int max_q, const float *u, int32_t *n_accepted, int32_t *path, int32_t *next_token,
+                    cudaStream_t stream)
+{
+    if (n_seq < 0 || n_tokens < 0 || max_q < 1 || vocab < 1 || (x_dtype != BQG_BF16 && x_dtype != BQG_F32))
+        return BQG_ERR_INVALID_ARG;
+    if (n_seq && (!q_start || !n_accepted || !path || !next_token)) return BQG_ERR_INVALID_ARG;
+    if (n_tokens && (!target || !tokens || !u || target_stride < vocab || (draft && draft_stride < vocab)))
+        return BQG_ERR_INVALID_ARG;
+    if (max_q > 64 || n_tokens > (int64_t)64 * n_seq || n_tokens >= kMaxTokens || vocab > (1 << 30) || n_seq > (1 << 27) ||
+        target_stride > ((int64_t)1 << 40) || draft_stride > ((int64_t)1 << 40))
+        return BQG_ERR_UNSUPPORTED_SHAPE;
+    const int size = x_dtype == BQG_F32 ? 4 : 2;
+    if (!aligned(target, size) || !aligned(draft, size) || !aligned(tokens, 4) || !aligned(parent, 4) ||
+        !aligned(q_start, 4) || !aligned(u, 4) || !aligned(n_accepted, 4) || !aligned(path, 4) || !aligned(next_token, 4))
+        return BQG_ERR_MISALIGNED;
+    VerifyParams p{};
+    p.target = target; p.draft = draft;
+    p.target_stride = target_stride; p.draft_stride = draft_stride;
+    p.vocab = (int)vocab;
+    p.tokens = tokens; p.parent = parent; p.q_start = q_start;
+    p.n_seq = n_seq; p.n_tokens = n_tokens; p.max_q = max_q;
+    p.u = u;
+    p.n_accepted = n_accepted; p.path = path; p.next_token = next_token;
+    DevInfo dev;
+    if (int st = current_device(&dev)) return st;
+    if (n_seq == 0) return BQG_OK;
+    return cuda_status(launch_verify(p, x_dtype == BQG_F32, stream, g_pdl.load() != 0));
+}
+
+int bqg_kv_compact(const bqg_kv_cache *cache, const int32_t *block_table, int64_t max_pages, const int32_t *ctx_len,
+                   const int32_t *path, const int32_t *n_path, int n_seq, int max_q, int32_t *new_ctx, cudaStream_t stream)
+{
+    CompactParams p{};
+    if (int st = check_cache(cache, &p.cache)) return st;
+    if (n_seq < 0 || max_q < 1 || max_pages < 1) return BQG_ERR_INVALID_ARG;
+    if (n_seq && (!block_table || !ctx_len || !path || !n_path)) return BQG_ERR_INVALID_ARG;
+    if (max_q > 64 || max_pages > ((int64_t)1 << 31)) return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(block_table, 4) || !aligned(ctx_len, 4) || !aligned(path, 4) || !aligned(n_path, 4) || !aligned(new_ctx, 4))
+        return BQG_ERR_MISALIGNED;
+    // several CTAs read a sequence's length, one writes the new one
+    if (n_seq && new_ctx && new_ctx < ctx_len + n_seq && ctx_len < new_ctx + n_seq) return BQG_ERR_INVALID_ARG;
+    p.table = block_table; p.max_pages = max_pages;
+    p.ctx_len = ctx_len; p.path = path; p.n_path = n_path;
+    p.n_seq = n_seq; p.max_q = max_q;
+    p.ctx_out = new_ctx;
+    DevInfo dev;
+    if (int st = current_device(&dev)) return st;
+    if (n_seq == 0) return BQG_OK;
+    return cuda_status(launch_compact(p, cache->fmt, cache->head_dim, dev.sms, stream, g_pdl.load() != 0));
+}
+
+int bqg_kv_fork(const bqg_kv_cache *cache, int32_t *block_table, int64_t max_pages, int n_rows, int32_t *ctx_len,
+                const int32_t *parent, const int32_t *child, const int32_t *fresh, int n, cudaStream_t stream)
+{
+    ForkParams p{};
+    if (int st = check_cache(cache, &p.cache)) return st;
+    if (n_rows < 0 || n < 0 || max_pages < 1) return BQG_ERR_INVALID_ARG;
+    if (n && (!block_table || !ctx_len || !parent || !child || !fresh)) return BQG_ERR_INVALID_ARG;
+    if (max_pages > ((int64_t)1 << 31)) return BQG_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(block_table, 4) || !aligned(ctx_len, 4) || !aligned(parent, 4) || !aligned(child, 4) || !aligned(fresh, 4))
+        return BQG_ERR_MISALIGNED;
+    p.table = block_table; p.max_pages = max_pages; p.n_rows = n_rows;
+    p.ctx_len = ctx_len;
+    p.parent = parent; p.child = child; p.fresh = fresh; p.n = n;
+    DevInfo dev;
+    if (int st = current_device(&dev)) return st;
+    if (n == 0) return BQG_OK;
+    return cuda_status(launch_fork(p, cache->fmt, cache->head_dim, dev.sms, stream, g_pdl.load() != 0));
 }
 
 size_t bqg_workspace_size(int op, int M, int64_t N, int64_t K)

@@ -304,8 +304,10 @@ enum {
     BQG_DEVERR_SLOT = 16,       /* a slot beyond the cache: not stored, read as zeros          */
     BQG_DEVERR_POSITION = 32,   /* a position outside the table: zeros out, key and value not stored */
     BQG_DEVERR_PAGE = 64,       /* a page index outside the cache: its tokens are not seen     */
-    BQG_DEVERR_LENGTH = 128     /* lengths or query offsets that do not fit: clamped to fit; a query that is
+    BQG_DEVERR_LENGTH = 128,    /* lengths or query offsets that do not fit: clamped to fit; a query that is
                                    then in no sequence is not computed, its output stays as it was */
+    BQG_DEVERR_ROW = 256,       /* a row outside the block table, or a sequence that is to be its own branch: not branched */
+    BQG_DEVERR_DRAFT = 512      /* a drafted token outside the vocabulary, or a parent that is not before it: not accepted */
 };
 
 /* Per-head RMSNorm and rotation of queries and keys.  q: T tokens of n_q
@@ -414,6 +416,49 @@ int bqg_shared_prefix_attention(const void *q, int64_t q_stride, const bqg_kv_ca
 /* Workspace bytes of bqg_shared_prefix_attention for these arguments on the current device; 0 when they are not valid. */
 size_t bqg_shared_prefix_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int n_seq, int max_q, int64_t n_tokens,
                                                   int n_prefix, int64_t max_shared);
+
+/* Drafted tokens accepted or rejected against the target's probabilities, and the token that follows.  Sequence b has
+ * tokens q_start[b] .. q_start[b + 1] - 1 (at most max_q), as bqg_tree_attention's: token 0 is the last one given out,
+ * each other one i is a draft behind its parent[i], a token of the sequence before it (numbered from 0; parent NULL:
+ * i - 1, a chain).  target: a row of `vocab` probabilities per token, p(x) of the token behind it; draft: likewise the
+ * distributions q that the drafts behind each token were drawn from, independently of each other; draft NULL: the
+ * drafts were chosen, not drawn (the likeliest ones, say).  x_dtype (both) BQG_F32 or BQG_BF16, rows target_stride and draft_stride values apart;
+ * a value that is no positive finite number counts as 0.  u: a number in [0, 1) per token.
+ * From token 0 on, the drafts behind a token are taken in their order: i, of token t, is accepted, and its own drafts are next, when
+ *     u[i] q(t) Z < r(t),
+ * r = p and Z = 1 before the first rejection behind that token.  A rejection makes r(x) = max(p(x) - c q(x), 0) with c
+ * the sum of the Z so far and Z the sum of the new r (chosen drafts: q(t) = 1, r is p without the
+ * rejected tokens, Z = 1 - the sum of their p).  When no draft is left the next token is the first x at which the running
+ * sum of r exceeds u[0] times all of it, r = p where nothing is left.  With sampled drafts the tokens then are
+ * distributed as the target's.
+ * n_accepted: n_seq int32, the accepted tokens with token 0 (0: a sequence without tokens); path: n_seq rows of max_q int32,
+ * their places, ascending from 0, then -1; next_token: n_seq int32 (-1: no token, or a row without a probability).
+ * Sums are kept to about 2^-45: answers are those of the formulas but where u is that near to a border.
+ * Token rows and numbers in device memory; pointers aligned to their values; 1 <= max_q <= 64; vocab at most 2^30.
+ * One launch. */
+int bqg_tree_verify(const void *target, const void *draft, int x_dtype, int64_t target_stride, int64_t draft_stride,
+                    int64_t vocab, const int32_t *tokens, const int32_t *parent, const int32_t *q_start, int n_seq,
+                    int64_t n_tokens, int max_q, const float *u, int32_t *n_accepted, int32_t *path, int32_t *next_token,
+                    cudaStream_t stream);
+
+/* The accepted path's keys and values moved behind the context: new token path[b][k] of sequence b (at place ctx_len[b]
+ * + path[b][k], as bqg_tree_attention has it) goes to place ctx_len[b] + k, for k < n_path[b], codes and scales as they
+ * are.  path: n_seq rows of max_q int32, ascending (as bqg_tree_verify gives it); what stands behind
+ * the kept tokens stays as it is.  new_ctx (may be NULL): n_seq int32, ctx_len[b] + n_path[b]; not overlapping ctx_len.
+ * A path that stops ascending or leaves the sequence's pages is cut off there (BQG_DEVERR_LENGTH); a move from or to a
+ * page outside the cache is left out (BQG_DEVERR_PAGE).  1 <= max_q <= 64.  One launch. */
+int bqg_kv_compact(const bqg_kv_cache *cache, const int32_t *block_table, int64_t max_pages, const int32_t *ctx_len,
+                   const int32_t *path, const int32_t *n_path, int n_seq, int max_q, int32_t *new_ctx, cudaStream_t stream);
+
+/* Sequences branched: for each i < n, row child[i] of block_table (n_rows of max_pages) becomes a branch of row parent[i].
+ * With c = ctx_len[parent[i]]: its first c / page_size entries are the parent's (full pages, shared from now on), the next
+ * one is fresh[i], whose first c % page_size tokens are copied from the parent's page there, and ctx_len[child[i]]
+ * is c; the row's other entries and the page's other tokens stay as they are.  Where c % page_size is 0, fresh[i] is only entered
+ * (and may be negative: no page yet).  Children must be distinct and none of them a parent in the same call, fresh pages
+ * distinct and in no row: else rows and pages hold one or the other.  Which pages are free is
+ * the caller's to keep.  One launch. */
+int bqg_kv_fork(const bqg_kv_cache *cache, int32_t *block_table, int64_t max_pages, int n_rows, int32_t *ctx_len,
+                const int32_t *parent, const int32_t *child, const int32_t *fresh, int n, cudaStream_t stream);
 
 /* Prefill GEMM ("llama-3x-prompt-speed", "the tile"): each weight tile is
  * dequantized once to bf16 into the tensor memory the MMA reads and fed to
