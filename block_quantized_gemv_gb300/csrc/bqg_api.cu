@@ -1351,7 +1351,7 @@ int bqg_tree_verify(const void *target, const void *draft, int x_dtype, int64_t 
     DevInfo dev;
     if (int st = current_device(&dev)) return st;
     if (n_seq == 0) return BQG_OK;
-    return cuda_status(launch_verify(p, x_dtype == BQG_F32, stream, g_pdl.load() != 0));
+    return cuda_status(launch_verify(p, x_dtype == BQG_F32, dev.sms, stream, g_pdl.load() != 0));
 }
 
 int bqg_kv_compact(const bqg_kv_cache *cache, const int32_t *block_table, int64_t max_pages, const int32_t *ctx_len,

@@ -19,6 +19,8 @@
 //    about 2^-45 of the sum.  The few numbers of the walk itself are fp64.
 //  * The crossing is looked for in the sums of CTAs, of warps (contiguous ranges), then in the warp's range, which one
 //    warp reads again: first lane by lane, then token by token.
+#include <climits>
+
 #include <cooperative_groups.h>
 
 #include "bqg_verify.cuh"
@@ -27,65 +29,165 @@ namespace bqg {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCtas = 8, kMaxDrafts = 64;
+constexpr int kMaxCtas = 8, kMaxDrafts = 64;
 constexpr int kLeast = 2048;           // values of a row that a CTA is taken for
 
-// An unevaluated sum of two fp32 numbers.
+// An unevaluated sum of two fp32 numbers, none of which is negative.
 struct Pair {
     float hi = 0.f, lo = 0.f;
     __device__ __forceinline__ void add(float h, float l)
     {
-        float e;
-        two_sum(hi, h, hi, e);
-        lo = __fadd_rn(lo, __fadd_rn(e, l));
+        // the smaller number's error in the sum is exact (Dekker): five operations, two_sum takes six
+        const float a = fmaxf(hi, h), b = fminf(hi, h);
+        hi = __fadd_rn(a, b);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(b, __fsub_rn(hi, a)), l));
     }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+};
+// hi + lo of a pair, hi the nearest fp32 number (|hi| >= |lo| or near it).
+__device__ __forceinline__ Pair tidy(float hi, float lo)
+{
+    Pair r;
+    two_sum(hi, lo, r.hi, r.lo);
+    return r;
+}
+// Parts of a row's sum as whole numbers: units of about 2^-61 of it, so that what follows is exact and quick (fp64 takes
+// 16 cycles per warp and operation here, and its latency).
+struct Units {
+    float by[2];                       // two powers of two: one would leave fp32's range for sums below 2^-66
+    __device__ __forceinline__ explicit Units(float whole)
+    {
+        const int k = 60 - (int)(__float_as_uint(whole) >> 23) + 127;             // (a denormal one counts as 2^-127)
+        const int a = k >> 1, b = k - a;
+        by[0] = __uint_as_float((uint32_t)(127 + a) << 23);
+        by[1] = __uint_as_float((uint32_t)(127 + b) << 23);
+    }
+    __device__ __forceinline__ long long of(float x) const { return __float2ll_rn(__fmul_rn(__fmul_rn(x, by[0]), by[1])); }
+    // (what is less than a unit still counts as something)
+    __device__ __forceinline__ long long of(const Pair &v) const { return max(of(v.hi) + of(v.lo), (long long)(__fadd_rn(v.hi, v.lo) > 0.f)); }
+};
+
+// Two numbers per register pair, each rounded by itself.
+struct F2 { uint64_t v; };
+__device__ __forceinline__ F2 f2(float a, float b) { F2 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b)); return r; }
+__device__ __forceinline__ float lower(F2 x) { return __uint_as_float((uint32_t)x.v); }
+__device__ __forceinline__ float upper(F2 x) { return __uint_as_float((uint32_t)(x.v >> 32)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { F2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { F2 r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v)); return r; }
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return fma2(b, f2(-1.f, -1.f), a); }      // (one rounding: b times -1 is exact)
+// Two pairs at once.
+struct Pair2 {
+    F2 hi, lo;
+    __device__ __forceinline__ void add(F2 h, F2 l)
+    {
+        const F2 s = add2(hi, h), b = sub2(s, hi);
+        const F2 e = add2(sub2(hi, sub2(s, b)), sub2(h, b));       // Knuth's: no comparison, which would not be packed
+        hi = s;
+        lo = add2(lo, add2(e, l));
+    }
+    __device__ __forceinline__ Pair both() const
+    {
+        Pair r{lower(hi), lower(lo)};
+        r.add(upper(hi), upper(lo));
+        return r;
+    }
 };
 
 struct Order {
-    int sum;                           // 0: the end
+    int sum;                           // 0: the end; the token is looked for with what follows as it was
     int row;                           // of target and draft
     float c_hi, c_lo;                  // what q is taken off with
+    int at;                            // the end: which of all warps looks for the token (-1: none does)
+    float whole;                       // ... with Units(whole)
+    long long goal;
     int n_gone;                        // chosen drafts that were rejected here
     int gone[kMaxDrafts];
 };
 
-// A probability: what is no positive number counts as none.
-__device__ __forceinline__ float prob(float x) { return x > 0.f && x < __int_as_float(0x7f800000) ? x : 0.f; }
-template <bool F32> __device__ __forceinline__ float load_prob(const void *x, int64_t i)
+// A probability: from 0 to 1 (a NaN: 0).
+__device__ __forceinline__ float prob(float x) { return __saturatef(x); }
+template <bool F32> __device__ __forceinline__ float load_raw(const void *x, int64_t i)
 {
-    if constexpr (F32) return prob(__ldg(reinterpret_cast<const float *>(x) + i));
-    else return prob(__uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(x) + i) << 16));
+    if constexpr (F32) return __ldg(reinterpret_cast<const float *>(x) + i);
+    else return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(x) + i) << 16);
+}
+template <bool F32> __device__ __forceinline__ float load_prob(const void *x, int64_t i) { return prob(load_raw<F32>(x, i)); }
+// One row: probabilities of `vocab` tokens, of which 16 bytes are loaded at once where they lie on such a boundary and in the row.
+template <bool F32> struct Row {
+    static constexpr int E = F32 ? 4 : 8;                  // values of 16 bytes
+    const uint8_t *at;
+    int vocab, off;                                        // off: tokens x with (x + off) % E == 0 lie on a boundary
+    __device__ __forceinline__ Row(const void *base, int64_t first, int vocab)
+        : at(reinterpret_cast<const uint8_t *>(base) + first * (F32 ? 4 : 2)), vocab(vocab),
+          off((int)(reinterpret_cast<uintptr_t>(at) / (F32 ? 4 : 2)) & (E - 1))
+    {
+    }
+    // tokens x .. x + E - 1 as they lie, zeros where they are none; `there`: they lie on a boundary
+    __device__ __forceinline__ uint4 load(int x, bool there) const
+    {
+        if (there && x >= 0 && x <= vocab - E) return __ldg(reinterpret_cast<const uint4 *>(at + (int64_t)x * (F32 ? 4 : 2)));
+        return one_by_one(at, x, vocab);
+    }
+    static __device__ __noinline__ uint4 one_by_one(const uint8_t *at, int x, int vocab)
+    {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < E; i++)
+            if (x + i >= 0 && x + i < vocab) {
+                if constexpr (F32) w[i % 4] = __ldg(reinterpret_cast<const uint32_t *>(at) + x + i);
+                else w[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(at) + x + i) << (16 * (i & 1));
+            }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ void values(const uint4 &q, float (&v)[E])
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < E; i++) v[i] = prob(F32 ? __uint_as_float(w[i % 4]) : (i & 1) ? bf16_hi(w[i / 2 % 4]) : bf16_lo(w[i / 2 % 4]));
+    }
+};
+
+// max(p - c q, 0) as a pair; ONE: c is 1, as it is after a first rejection.
+template <bool ONE> __device__ __forceinline__ void rest(float p, float q, float ch, float cl, float &hi, float &lo)
+{
+    if constexpr (ONE) {
+        const float a = fmaxf(p, q);                       // a - q and its error, exact as a >= q
+        hi = __fsub_rn(a, q);
+        lo = __fsub_rn(__fsub_rn(a, hi), q);
+    } else {
+        const float m = __fmul_rn(q, ch);
+        const float me = __fadd_rn(fmaf(q, ch, -m), __fmul_rn(q, cl));
+        const float a = fmaxf(p, m);
+        hi = __fsub_rn(a, m);
+        lo = __fsub_rn(__fsub_rn(__fsub_rn(a, hi), m), me);
+        lo = p >= m ? fmaxf(lo, -hi) : 0.f;
+    }
 }
 
-// What is left of p after c q: a pair, (0, 0) if it is not positive.
-__device__ __forceinline__ void rest(float p, float q, float ch, float cl, float &hi, float &lo)
+// Two at once.
+template <bool ONE> __device__ __forceinline__ void rest2(float p0, float p1, float q0, float q1, float ch, float cl, F2 &hi, F2 &lo)
 {
-    const float m = __fmul_rn(q, ch);
-    const float me = __fadd_rn(fmaf(q, ch, -m), __fmul_rn(q, cl));
-    float e;
-    two_sum(p, -m, hi, e);
-    lo = __fsub_rn(e, me);
-    if (!(__fadd_rn(hi, lo) > 0.f)) hi = lo = 0.f;
+    if constexpr (ONE) {
+        const F2 a = f2(fmaxf(p0, q0), fmaxf(p1, q1)), q = f2(q0, q1);
+        hi = sub2(a, q);
+        lo = sub2(sub2(a, hi), q);
+    } else {
+        float h[2], l[2];
+        rest<false>(p0, q0, ch, cl, h[0], l[0]);
+        rest<false>(p1, q1, ch, cl, h[1], l[1]);
+        hi = f2(h[0], h[1]);
+        lo = f2(l[0], l[1]);
+    }
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-template <bool F32, bool DRAFT> struct Verify {
-    // r at token x < vocab of the order's row.
-    static __device__ __forceinline__ void left(const VerifyParams &p, const Order &o, int64_t t0, int64_t q0, int x, unsigned long long gone,
-                                                float &hi, float &lo)
-    {
-        hi = load_prob<F32>(p.target, t0 + x);
-        lo = 0.f;
-        if constexpr (DRAFT) {
-            if (o.c_hi > 0.f) rest(hi, load_prob<F32>(p.draft, q0 + x), o.c_hi, o.c_lo, hi, lo);
-        } else {
-            for (; gone; gone &= gone - 1)
-                if (o.gone[__ffsll(gone) - 1] == x) hi = 0.f;
-        }
-    }
+template <bool F32, bool DRAFT, int kWarps> struct Verify {
+    static constexpr int E = Row<F32>::E;
+    static constexpr int kStep = 32 * E;                  // values that a warp takes at once: 16 bytes per lane
+    static constexpr int kKept = kWarps == 16 ? 8 : 16;   // parts of a warp's range whose sums are kept
+    static constexpr int U = kWarps == 16 ? 4 : 2;        // steps whose loads are in flight together
+
     // Which of the rejected tokens lie in [a, e).
     static __device__ __forceinline__ unsigned long long gone_in(const Order &o, int a, int e, int lane)
     {
@@ -94,102 +196,193 @@ template <bool F32, bool DRAFT> struct Verify {
         const bool hi = lane + 32 < o.n_gone && o.gone[lane + 32] >= a && o.gone[lane + 32] < e;
         return (unsigned long long)__ballot_sync(0xffffffffu, lo) | (unsigned long long)__ballot_sync(0xffffffffu, hi) << 32;
     }
-    // The sum of r over tokens a .. e - 1, in all lanes.
-    static __device__ __forceinline__ Pair sum(const VerifyParams &p, const Order &o, int a, int e, int lane)
+    // The sum of r over the E tokens from x on.
+    template <bool FIRST>
+    static __device__ __forceinline__ Pair2 some(const Order &o, const uint4 &pw, const uint4 &qw, int x, unsigned long long gone)
     {
-        const int64_t t0 = (int64_t)o.row * p.target_stride, q0 = (int64_t)o.row * p.draft_stride;
-        const unsigned long long gone = gone_in(o, a, e, lane);
-        constexpr int U = 8;
-        Pair acc[2];
-        for (int x0 = a; x0 < e; x0 += 32 * U) {
-            float pv[U], qv[U];
+        float p[E], q[E];
+        Row<F32>::values(pw, p);
+        if constexpr (DRAFT) Row<F32>::values(qw, q);
+        if (!DRAFT && gone) {
+#pragma unroll 1
+            for (unsigned long long g = gone; g; g &= g - 1) {
+                const int at = o.gone[__ffsll(g) - 1] - x;
 #pragma unroll
-            for (int i = 0; i < U; i++) {
-                const int x = x0 + 32 * i + lane;
-                pv[i] = x < e ? load_prob<F32>(p.target, t0 + x) : 0.f;
-                if constexpr (DRAFT) qv[i] = x < e && o.c_hi > 0.f ? load_prob<F32>(p.draft, q0 + x) : 0.f;
-            }
-            if (!DRAFT && gone) {
-#pragma unroll
-                for (int i = 0; i < U; i++)
-                    for (unsigned long long g = gone; g; g &= g - 1)
-                        if (o.gone[__ffsll(g) - 1] == x0 + 32 * i + lane) pv[i] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < U; i++) {
-                float hi = pv[i], lo = 0.f;
-                if constexpr (DRAFT) rest(pv[i], qv[i], o.c_hi, o.c_lo, hi, lo);
-                acc[i & 1].add(hi, lo);
+                for (int i = 0; i < E; i++)
+                    if (at == i) p[i] = 0.f;
             }
         }
-        acc[0].add(acc[1].hi, acc[1].lo);
+        Pair2 s;
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1)
-            acc[0].add(__shfl_xor_sync(0xffffffffu, acc[0].hi, s), __shfl_xor_sync(0xffffffffu, acc[0].lo, s));
-        return acc[0];
+        for (int i = 0; i < E; i += 2) {
+            F2 hi = f2(p[i], p[i + 1]), lo = f2(0.f, 0.f);
+            if constexpr (DRAFT) rest2<FIRST>(p[i], p[i + 1], q[i], q[i + 1], o.c_hi, o.c_lo, hi, lo);
+            if (i == 0) { s.hi = hi; s.lo = lo; }
+            else s.add(hi, lo);
+        }
+        return s;
     }
-    // The first of 32 consecutive parts (this lane's: v) whose running sum from `base` on exceeds `goal`; without one,
-    // which is a matter of rounding, the last part that is not nothing; -1: all are.  base: the sum before it, or of all.
-    static __device__ __forceinline__ int cross(double v, double goal, int lane, double &base)
+    // The sum of r over a warp's tokens, from a on and before e, in lane 0.  kept[k][lane]: the sums of the lane's tokens in the k-th
+    // `steps` steps of it.
+    template <bool FIRST>
+    static __device__ __forceinline__ Pair sum(const VerifyParams &p, const Order &o, int a, int e, int steps, float2 (*kept)[32], int lane)
     {
-        double run = v;
+        const Row<F32> target(p.target, (int64_t)o.row * p.target_stride, p.vocab), draft(p.draft, (int64_t)o.row * p.draft_stride, p.vocab);
+        const unsigned long long gone = gone_in(o, a, e, lane);
+        const bool q = DRAFT && (FIRST || o.c_hi > 0.f);
+        Pair2 all{f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll 1
+        for (int k0 = 0; a + k0 * kStep < e; k0 += U) {
+            uint4 pw[U], qw[U];
 #pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int x = a + (k0 + u) * kStep + E * lane;
+                pw[u] = qw[u] = make_uint4(0, 0, 0, 0);
+                if (x < e) {
+                    pw[u] = target.load(x, true);
+                    if (q) qw[u] = draft.load(x, draft.off == target.off);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int k = k0 + u, x = a + k * kStep;
+                if (x >= e) break;
+                const Pair2 s = some<FIRST>(o, pw[u], qw[u], x + E * lane, gone);
+                all.add(s.hi, s.lo);
+                Pair one = s.both();
+                if (steps == 1) {
+                    kept[k][lane] = make_float2(one.hi, one.lo);
+                } else {
+                    const int at = k / steps;
+                    if (at * steps != k) {
+                        const float2 f = kept[at][lane];
+                        one.add(f.x, f.y);
+                    }
+                    kept[at][lane] = make_float2(one.hi, one.lo);
+                }
+            }
+        }
+        return over_lanes(all.both());
+    }
+    static __device__ __forceinline__ Pair over_lanes(Pair v)
+    {
+#pragma unroll 1
+        for (int s = 16; s > 0; s >>= 1) v.add(__shfl_xor_sync(0xffffffffu, v.hi, s), __shfl_xor_sync(0xffffffffu, v.lo, s));
+        return v;
+    }
+    // The first of 32 consecutive parts (this lane's: v) whose running sum exceeds `goal`, which then is what is left of the
+    // goal in that part.  Without one, which is a matter of rounding, the last part that is not nothing, and the goal is out of reach.
+    static __device__ __noinline__ int cross(long long v, long long &goal, int lane)
+    {
+        long long run = v;
+#pragma unroll 1
         for (int s = 1; s < 32; s <<= 1) {
-            const double o = __shfl_up_sync(0xffffffffu, run, s);
+            const long long o = __shfl_up_sync(0xffffffffu, run, s);
             if (lane >= s) run += o;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, base + run > goal), some = __ballot_sync(0xffffffffu, v > 0.0);
-        const int at = past & some ? __ffs(past & some) - 1 : -1;
-        const double before = __shfl_sync(0xffffffffu, run - v, at < 0 ? 0 : at), all = __shfl_sync(0xffffffffu, run, 31);
-        if (at < 0) {
-            base += all;
-            return -1;
-        }
-        base += before;
+        const unsigned some = __ballot_sync(0xffffffffu, v > 0), past = __ballot_sync(0xffffffffu, run > goal) & some;
+        const int at = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
+        goal = past ? goal - __shfl_sync(0xffffffffu, run - v, at) : LLONG_MAX;
         return at;
     }
-    // ... among tokens a .. e - 1, at least one of which has something left.
-    static __device__ int token(const VerifyParams &p, const Order &o, int a, int e, double base, double goal, int lane)
+    static __device__ __forceinline__ long long over_lanes(long long v)
     {
-        const int64_t t0 = (int64_t)o.row * p.target_stride, q0 = (int64_t)o.row * p.draft_stride;
-        const unsigned long long gone = gone_in(o, a, e, lane);
-        const int per = (e - a + 31) / 32, b = min(a + lane * per, e), n = min(per, e - b);
+#pragma unroll 1
+        for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+        return v;
+    }
+    // ... among a warp's tokens, from a on and before e, whose sums are kept.
+    static __device__ __forceinline__ int token(const VerifyParams &p, const Order &o, int a, int e, int steps, const float2 (*kept)[32],
+                                                const Units &units, long long goal, int lane)
+    {
+        // the kept part: 32 / kKept lanes add up one (from different banks)
+        constexpr int L = 32 / kKept;
         Pair s;
+        const int k = lane / L;
+        if (a + k * steps * kStep < e) {
 #pragma unroll 4
-        for (int i = 0; i < n; i++) {
-            float hi, lo;
-            left(p, o, t0, q0, b + i, gone, hi, lo);
-            s.add(hi, lo);
+            for (int i = 0; i < 32 / L; i++) {
+                const float2 f = kept[k][lane % L * (32 / L) + ((i + k) & (32 / L - 1))];
+                s.add(f.x, f.y);
+            }
         }
-        const double v = s.value();
-        int l = cross(v, goal, lane, base);
-        if (l < 0) {
-            l = 31 - __clz(__ballot_sync(0xffffffffu, v > 0.0) | 1u);
-            goal = __longlong_as_double(0x7ff0000000000000ll);         // its last token
+#pragma unroll
+        for (int i = 1; i < L; i <<= 1) s.add(__shfl_xor_sync(0xffffffffu, s.hi, i), __shfl_xor_sync(0xffffffffu, s.lo, i));
+        const int part = cross(lane % L ? 0 : units.of(s), goal, lane) / L;
+        a += part * steps * kStep;
+        const Row<F32> target(p.target, (int64_t)o.row * p.target_stride, p.vocab), draft(p.draft, (int64_t)o.row * p.draft_stride, p.vocab);
+        const bool q = DRAFT && o.c_hi > 0.f;
+        long long v;
+        if (steps == 1) {
+            const float2 f = kept[part][lane];
+            v = units.of(Pair{f.x, f.y});
+        } else {
+            v = step_of(o, target, draft, a, min(a + steps * kStep, e), units, goal, lane);
         }
-        const int first = __shfl_sync(0xffffffffu, b, l), count = __shfl_sync(0xffffffffu, n, l);
-        int last = first;
-        for (int i = 0; i < count; i += 32) {
-            float hi = 0.f, lo = 0.f;
-            if (i + lane < count) left(p, o, t0, q0, first + i + lane, gone, hi, lo);
-            const double r = (double)hi + (double)lo;
-            const int at = cross(r, goal, lane, base);
-            if (at >= 0) return first + i + at;
-            const unsigned some = __ballot_sync(0xffffffffu, r > 0.0);
-            if (some) last = first + i + 31 - __clz(some);
+        // the lane, then its token
+        const int l = cross(v, goal, lane), x = a + E * l + lane;
+        Pair r;
+        if (lane < E && x >= 0 && x < e) {
+            r.hi = load_prob<F32>(target.at, x);
+            if constexpr (DRAFT)
+                if (q) rest<false>(r.hi, load_prob<F32>(draft.at, x), o.c_hi, o.c_lo, r.hi, r.lo);
+            if (!DRAFT)
+                for (int i = 0; i < o.n_gone; i++)
+                    if (o.gone[i] == x) r.hi = 0.f;
         }
-        return last;
+        return a + E * l + cross(units.of(r), goal, lane);
+    }
+    // The step of a part of several, as `a`; returns this lane's share of it.
+    static __device__ __noinline__ long long step_of(const Order &o, const Row<F32> &target, const Row<F32> &draft, int &a, int e,
+                                                     const Units &units, long long &goal, int lane)
+    {
+        const unsigned long long gone = gone_in(o, a, e, lane);
+        const int first = a;
+        int last = -1;
+#pragma unroll 1
+        for (;;) {
+            const int x = a + E * lane;
+            uint4 pw = make_uint4(0, 0, 0, 0), qw = pw;
+            if (x < e) {
+                pw = target.load(x, true);
+                if (DRAFT && o.c_hi > 0.f) qw = draft.load(x, draft.off == target.off);
+            }
+            const long long v = units.of(some<false>(o, pw, qw, x, gone).both()), all = over_lanes(v);
+            if (all > goal || last == a) return v;
+            if (all > 0) last = a;
+            if (goal != LLONG_MAX) goal -= all;
+            a += kStep;
+            if (a >= e) {                                              // rounding: the last one that is not nothing
+                goal = LLONG_MAX;
+                a = last = last < 0 ? first : last;
+            }
+        }
     }
 };
 
-template <bool F32, bool DRAFT>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, int ctas)
+// A draft as the walk needs it.
+struct Draft {
+    float u, p, q;
+    int token;
+};
+// u q Z < r(t) of it, r as a pair.
+__device__ __forceinline__ bool accepted(const Draft &d, const Pair &r, const Pair &Z)
+{
+    const float m = __fmul_rn(d.u, d.q), me = fmaf(d.u, d.q, -m);
+    const float y = __fmul_rn(m, Z.hi), ye = __fadd_rn(fmaf(m, Z.hi, -y), fmaf(m, Z.lo, __fmul_rn(me, Z.hi)));
+    // near each other their difference is exact
+    return __fadd_rn(__fsub_rn(y, r.hi), __fsub_rn(ye, r.lo)) < 0.f;
+}
+
+template <bool F32, bool DRAFT, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 1) verify_kernel(const VerifyParams p, int ctas)
 {
     namespace cg = cooperative_groups;
-    using V = Verify<F32, DRAFT>;
+    using V = Verify<F32, DRAFT, kWarps>;
     __shared__ Order order;
     __shared__ Pair warp_sum[kWarps];
-    __shared__ double cta_sum;
+    __shared__ float2 kept[kWarps][V::kKept][32];
+    __shared__ Draft drafts[kMaxDrafts];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = blockIdx.x % ctas, b = blockIdx.x / ctas;
@@ -197,11 +390,14 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
     pdl_wait();
     pdl_launch_dependents();
 
-    // values of a row per warp, a multiple of 32
-    const int per = (int)((((int64_t)p.vocab + ctas * kWarps - 1) / (ctas * kWarps) + 31) & ~31ll);
-    auto range = [&](int cta, int w, int &a, int &e) {
-        a = (int)min((int64_t)(cta * kWarps + w) * per, (int64_t)p.vocab);
-        e = (int)min((int64_t)a + per, (int64_t)p.vocab);
+    // A warp's part of a row: whole steps from a boundary of 16 bytes on, which for the first one is up to E - 1 values before the row.
+    int steps;                                 // of a kept part
+    auto range = [&](int row, int w, int &a, int &e) {
+        const int off = Row<F32>(p.target, (int64_t)row * p.target_stride, p.vocab).off;
+        const int all = (p.vocab + off + V::kStep - 1) / V::kStep, per = (all + ctas * kWarps - 1) / (ctas * kWarps);
+        steps = (per + V::kKept - 1) / V::kKept;
+        a = min(w * per, all) * V::kStep - off;
+        e = min(a + per * V::kStep, p.vocab);
     };
     auto meet = [&]() {
         if (ctas == 1) return __syncthreads();
@@ -212,19 +408,20 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
     // nobody reads another CTA's memory.)
     auto round = [&]() {
         meet();
-        if (!order.sum) return false;
-        int a, e;
-        range(rank, warp, a, e);
-        const Pair s = V::sum(p, order, a, e, lane);
-        if (lane == 0) warp_sum[warp] = s;
-        __syncthreads();
-        if (warp == 0) {
-            Pair t;
-            if (lane < kWarps) t = warp_sum[lane];
-#pragma unroll
-            for (int i = kWarps / 2; i > 0; i >>= 1) t.add(__shfl_xor_sync(0xffffffffu, t.hi, i), __shfl_xor_sync(0xffffffffu, t.lo, i));
-            if (lane == 0) cta_sum = t.value();
+        if (!order.sum) {
+            if (order.at == rank * kWarps + warp) {
+                int a, e;
+                range(order.row, order.at, a, e);
+                const int x = V::token(p, order, a, e, steps, kept[warp], Units(order.whole), order.goal, lane);
+                if (lane == 0) p.next_token[b] = min(max(x, 0), p.vocab - 1);
+            }
+            return false;
         }
+        int a, e;
+        range(order.row, rank * kWarps + warp, a, e);
+        const Pair s = order.c_hi == 1.f && order.c_lo == 0.f ? V::template sum<true>(p, order, a, e, steps, kept[warp], lane)
+                                                              : V::template sum<false>(p, order, a, e, steps, kept[warp], lane);
+        if (lane == 0) warp_sum[warp] = s;
         meet();
         return true;
     };
@@ -242,63 +439,75 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
     int bad = q0 != a0 || q1 != e0 || T != q1 - q0 ? BQG_DEVERR_LENGTH : 0;
     if (b == 0 && (a0 != 0 || p.q_start[p.n_seq] != p.n_tokens)) bad |= BQG_DEVERR_LENGTH;
     // drafts `lane` and 32 on
-    int up[2], tok[2];
-    float u[2], pt[2], qt[2];
+    int up[2];
 #pragma unroll
     for (int j = 0; j < 2; j++) {
         const int i = lane + 32 * j;
-        up[j] = tok[j] = -1;
-        u[j] = pt[j] = 0.f;
-        qt[j] = 1.f;
+        up[j] = -1;
         if (i >= T) continue;
-        u[j] = p.u[q0 + i];
-        if (i == 0) continue;
-        tok[j] = p.tokens[q0 + i];
-        up[j] = p.parent ? p.parent[q0 + i] : i - 1;
-        if (up[j] < 0 || up[j] >= i || tok[j] < 0 || tok[j] >= p.vocab) {
-            bad |= BQG_DEVERR_DRAFT;
-            up[j] = -1;
-            continue;
+        Draft d{p.u[q0 + i], 0.f, 1.f, -1};
+        if (i) {
+            d.token = p.tokens[q0 + i];
+            up[j] = p.parent ? p.parent[q0 + i] : i - 1;
+            if (up[j] < 0 || up[j] >= i || d.token < 0 || d.token >= p.vocab) {
+                bad |= BQG_DEVERR_DRAFT;
+                up[j] = -1;
+            } else {
+                const int64_t row = q0 + up[j];
+                d.p = load_prob<F32>(p.target, row * p.target_stride + d.token);
+                if constexpr (DRAFT) d.q = load_prob<F32>(p.draft, row * p.draft_stride + d.token);
+            }
         }
-        const int64_t row = q0 + up[j];
-        pt[j] = load_prob<F32>(p.target, row * p.target_stride + tok[j]);
-        if constexpr (DRAFT) qt[j] = load_prob<F32>(p.draft, row * p.draft_stride + tok[j]);
+        drafts[i] = d;
     }
     if (bad) atomicOr(p.error, bad);
     __syncwarp();
     if (ctas > 1) cluster_wait();
-    auto pick = [&](auto (&v)[2], int i) {
-        const auto lo = __shfl_sync(0xffffffffu, v[0], i & 31), hi = __shfl_sync(0xffffffffu, v[1], i & 31);
-        return i < 32 ? lo : hi;
-    };
-    auto give = [&](int sum, int64_t row, double c, int n_gone) {
+    const Pair zero, one{1.f, 0.f};
+    // A round: the warps' sums, in their order, each lane the next few.
+    constexpr int NE = kMaxCtas * kWarps / 32;
+    const int each = max(ctas * kWarps / 32, 1);
+    Pair parts[NE];
+    auto give = [&](int sum, int64_t row, const Pair &c, int n_gone, int at = -1, float whole = 1.f, long long goal = 0) {
         __syncwarp();
         if (lane < ctas) {                                // to one CTA per lane
             Order *o = ctas > 1 ? cluster.map_shared_rank(&order, lane) : &order;
             o->sum = sum;
-            o->row = (int)row;
-            o->c_hi = (float)c;
-            o->c_lo = (float)(c - (double)(float)c);
-            o->n_gone = n_gone;
-            if (lane)
-                for (int i = 0; i < n_gone; i++) o->gone[i] = order.gone[i];
+            o->at = at;
+            o->whole = whole;
+            o->goal = goal;
+            if (sum) {
+                o->row = (int)row;
+                o->c_hi = c.hi;
+                o->c_lo = c.lo;
+                o->n_gone = n_gone;
+                if (lane)
+                    for (int i = 0; i < n_gone; i++) o->gone[i] = order.gone[i];
+            }
         }
         __syncwarp();
-        round();
-        double z = 0.0;                                   // the CTAs' sums, in their order: one per lane
-        if (sum && lane < ctas) z = ctas > 1 ? *cluster.map_shared_rank(&cta_sum, lane) : cta_sum;
-        return z;
-    };
-    auto all_of = [&](double z) {
+        if (!round()) return zero;
 #pragma unroll
-        for (int s = 4; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-        return __shfl_sync(0xffffffffu, z, 0);
+        for (int i = 0; i < NE; i++) {
+            const int w = lane * each + i;
+            parts[i] = Pair();
+            if (i < each && w < ctas * kWarps)
+                parts[i] = ctas > 1 ? *cluster.map_shared_rank(&warp_sum[w % kWarps], w / kWarps) : warp_sum[w];
+        }
+        Pair z;
+#pragma unroll
+        for (int i = 0; i < NE; i++) z.add(parts[i].hi, parts[i].lo);
+        z = V::over_lanes(z);
+        return tidy(__shfl_sync(0xffffffffu, z.hi, 0), __shfl_sync(0xffffffffu, z.lo, 0));
     };
-    int node = 0, count = T > 0, place[2] = {lane == 0 && T > 0 ? 0 : -1, -1}, next = -1;   // place: of the path
+    int node = 0, count = T > 0, place[2] = {lane == 0 && T > 0 ? 0 : -1, -1};   // place: of the path
+    int finder = -1;                                      // the warp that holds the next token
+    float whole = 1.f;
+    long long goal = 0;
     if (T > 0) {
         int last = 0, n_gone = 0;                         // the last draft looked at
-        double Z = 1.0, c = 0.0, parts = 0.0;
-        bool known = false;                               // `parts` and the warps' sums are those of r
+        Pair Z = one, c;
+        bool known = false;                               // `parts` and what the CTAs hold are those of r
         for (;;) {
             unsigned long long below = (unsigned long long)__ballot_sync(0xffffffffu, up[0] == node) |
                                        (unsigned long long)__ballot_sync(0xffffffffu, up[1] == node) << 32;
@@ -306,82 +515,89 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
             if (!below) break;
             const int i = __ffsll(below) - 1;
             last = i;
-            const double ui = pick(u, i), qi = pick(qt, i);
-            double pi = pick(pt, i);
-            const int ti = pick(tok, i);
-            bool yes;
+            Draft d = drafts[i];
+            Pair r{d.p, 0.f};
             if constexpr (DRAFT) {
-                const double l = pi - c * qi;
-                yes = ui * qi * Z < (l > 0.0 ? l : 0.0);
+                rest<false>(d.p, d.q, c.hi, c.lo, r.hi, r.lo);
             } else {
-                const bool again = (lane < n_gone && order.gone[lane] == ti) || (lane + 32 < n_gone && order.gone[lane + 32] == ti);
-                if (__any_sync(0xffffffffu, again)) pi = 0.0;
-                yes = ui * Z < pi;
+                const bool again = (lane < n_gone && order.gone[lane] == d.token) || (lane + 32 < n_gone && order.gone[lane + 32] == d.token);
+                if (__any_sync(0xffffffffu, again)) r.hi = 0.f;
             }
-            if (yes) {
+            if (accepted(d, r, Z)) {
                 node = i;
                 if (lane == (count & 31)) place[count >> 5] = i;
                 count++;
-                Z = 1.0;
-                c = 0.0;
+                Z = one;
+                c = zero;
                 n_gone = 0;
                 known = false;
             } else if constexpr (DRAFT) {
-                c += Z;
-                parts = give(1, q0 + node, c, 0);
-                Z = all_of(parts);
+                float h, l;
+                two_sum(c.hi, Z.hi, h, l);
+                c = tidy(h, __fadd_rn(l, __fadd_rn(c.lo, Z.lo)));
+                Z = give(1, q0 + node, c, 0);
                 known = true;
             } else {
-                Z -= pi;
-                if (lane == 0) order.gone[n_gone] = ti;
+                float h, l;
+                two_sum(Z.hi, -r.hi, h, l);
+                Z = tidy(h, __fadd_rn(l, Z.lo));
+                __syncwarp();
+                if (lane == 0) order.gone[n_gone] = d.token;
                 n_gone++;
                 __syncwarp();
             }
         }
         if (!known) {
-            parts = give(1, q0 + node, 0.0, n_gone);
-            Z = all_of(parts);
+            Z = give(1, q0 + node, zero, n_gone);
         }
-        if (!(Z > 0.0) && (known || n_gone)) {            // nothing left: the target's own
-            parts = give(1, q0 + node, 0.0, 0);
-            Z = all_of(parts);
+        if (!(Z.hi > 0.f) && (known || n_gone)) {         // nothing left: the target's own
+            Z = give(1, q0 + node, zero, 0);
         }
-        if (Z > 0.0) {
-            const double goal = (double)__shfl_sync(0xffffffffu, u[0], 0) * Z;
-            double base = 0.0;
-            double far = goal;
-            int cta = V::cross(parts, far, lane, base);
-            if (cta < 0) {
-                cta = 31 - __clz(__ballot_sync(0xffffffffu, parts > 0.0) | 1u);
-                far = __longlong_as_double(0x7ff0000000000000ll);
+        if (Z.hi > 0.f) {
+            // u Z: what the running sum has to exceed, in whole units
+            whole = Z.hi;
+            const Units units(whole);
+            const float u = drafts[0].u;
+            const float m = __fmul_rn(u, Z.hi), me = fmaf(u, Z.hi, -m);
+            goal = (u >= 0.f ? units.of(m) : 0) + __float2ll_rd(__fmul_rn(__fmul_rn(fmaf(u, Z.lo, me), units.by[0]), units.by[1]));
+            // the lane's warps, then the warp
+            long long part[NE], sum = 0;
+#pragma unroll
+            for (int i = 0; i < NE; i++) {
+                part[i] = units.of(parts[i]);
+                sum += part[i];
             }
-            const Pair *sums = ctas > 1 ? cluster.map_shared_rank(warp_sum, cta) : warp_sum;
-            const double w = lane < kWarps ? sums[lane].value() : 0.0;
-            int at = V::cross(w, far, lane, base);
-            if (at < 0) {
-                at = 31 - __clz(__ballot_sync(0xffffffffu, w > 0.0) | 1u);
-                far = __longlong_as_double(0x7ff0000000000000ll);
+            const int l = V::cross(sum, goal, lane);
+            int at = 0;
+            bool past = false;
+#pragma unroll
+            for (int i = 0; i < NE; i++) {
+                const long long n = __shfl_sync(0xffffffffu, part[i], l);
+                if (n > 0 && !past) {
+                    at = i;
+                    past = n > goal;
+                    if (!past && goal != LLONG_MAX) goal -= n;
+                }
             }
-            int a, e;
-            range(cta, at, a, e);
-            if (a < e) next = V::token(p, order, a, e, base, far, lane);
+            if (!past) goal = LLONG_MAX;
+            finder = min(l * each + at, ctas * kWarps - 1);
         }
     }
     if (lane == 0) {
         p.n_accepted[b] = count;
-        p.next_token[b] = next;
+        if (finder < 0) p.next_token[b] = -1;
     }
 #pragma unroll
     for (int j = 0; j < 2; j++)
         if (lane + 32 * j < p.max_q) p.path[(int64_t)b * p.max_q + lane + 32 * j] = place[j];
-    give(0, 0, 0.0, 0);
+    give(0, 0, zero, 0, finder, whole, goal);
 }
 
-template <bool F32, bool DRAFT> cudaError_t run(const VerifyParams &p, int ctas, cudaStream_t s, bool pdl)
+template <bool F32, bool DRAFT, int kWarps> cudaError_t run_warps(const VerifyParams &p, int ctas, cudaStream_t s, bool pdl)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.n_seq * ctas));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32 * kWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -391,18 +607,23 @@ template <bool F32, bool DRAFT> cudaError_t run(const VerifyParams &p, int ctas,
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<F32, DRAFT>, p, ctas);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<F32, DRAFT, kWarps>, p, ctas);
+}
+// 16 warps per CTA while all CTAs are resident together that way, for the shorter rows; else 8.
+template <bool F32, bool DRAFT> cudaError_t run(const VerifyParams &p, int ctas, int sms, cudaStream_t s, bool pdl)
+{
+    return (int64_t)p.n_seq * ctas <= sms ? run_warps<F32, DRAFT, 16>(p, ctas, s, pdl) : run_warps<F32, DRAFT, 8>(p, ctas, s, pdl);
 }
 
 }  // namespace
 
-cudaError_t launch_verify(VerifyParams p, int x_f32, cudaStream_t s, bool pdl)
+cudaError_t launch_verify(VerifyParams p, int x_f32, int sms, cudaStream_t s, bool pdl)
 {
     if (cudaError_t e = device_error_word(&p.error)) return e;
     int ctas = 1;
     while (ctas < kMaxCtas && (int64_t)ctas * kLeast < p.vocab) ctas *= 2;
-    return x_f32 ? (p.draft ? run<true, true>(p, ctas, s, pdl) : run<true, false>(p, ctas, s, pdl))
-                 : (p.draft ? run<false, true>(p, ctas, s, pdl) : run<false, false>(p, ctas, s, pdl));
+    return x_f32 ? (p.draft ? run<true, true>(p, ctas, sms, s, pdl) : run<true, false>(p, ctas, sms, s, pdl))
+                 : (p.draft ? run<false, true>(p, ctas, sms, s, pdl) : run<false, false>(p, ctas, sms, s, pdl));
 }
 
 }  // namespace bqg

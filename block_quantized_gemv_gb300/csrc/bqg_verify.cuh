@@ -19,6 +19,6 @@ struct VerifyParams {
     int *error;                          // device_error_word, set by the launch
 };
 
-cudaError_t launch_verify(VerifyParams p, int x_f32, cudaStream_t s, bool pdl);
+cudaError_t launch_verify(VerifyParams p, int x_f32, int sms, cudaStream_t s, bool pdl);
 
 }  // namespace bqg

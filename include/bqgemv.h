@@ -423,7 +423,7 @@ size_t bqg_shared_prefix_attention_workspace_size(const bqg_kv_cache *cache, int
  * i - 1, a chain).  target: a row of `vocab` probabilities per token, p(x) of the token behind it; draft: likewise the
  * distributions q that the drafts behind each token were drawn from, independently of each other; draft NULL: the
  * drafts were chosen, not drawn (the likeliest ones, say).  x_dtype (both) BQG_F32 or BQG_BF16, rows target_stride and draft_stride values apart;
- * a value that is no positive finite number counts as 0.  u: a number in [0, 1) per token.
+ * a value is taken as between 0 and 1, a NaN as 0.  u: a number in [0, 1) per token.
  * From token 0 on, the drafts behind a token are taken in their order: i, of token t, is accepted, and its own drafts are next, when
  *     u[i] q(t) Z < r(t),
  * r = p and Z = 1 before the first rejection behind that token.  A rejection makes r(x) = max(p(x) - c q(x), 0) with c

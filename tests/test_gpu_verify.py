@@ -21,7 +21,7 @@ def built():
 def verify(target, tokens, lens, u, parent, draft, max_q, number=Fraction):
     """The header's definition, sequence by sequence.  Fraction: exact; float: fp64."""
     V = target.shape[1]
-    clean = lambda row: [number(x) if x > 0 and x < float("inf") else number(0) for x in row.tolist()]
+    clean = lambda row: [number(min(x, 1.0)) if x > 0 else number(0) for x in row.tolist()]
     accepted, paths, nexts, start = [], [], [], 0
     for n in lens:
         path, nxt = [], -1
