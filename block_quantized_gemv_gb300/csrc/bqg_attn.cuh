@@ -212,11 +212,11 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams &p, int b, int &bad
 
 // Attention where sequences share their first tokens.  With x the scores of a row, A its shared tokens and B its own,
 //     softmax(x) v = (sum_A e^(x - m) v + sum_B e^(x - m) v) / (sum_A e^(x - m) + sum_B e^(x - m)),
-// so the two sums are taken apart, each relative to a maximum of its own, and put together: the kernels here run
-// twice.  In the first pass a set is a prefix: its rows are the new tokens of all its sequences, which all
+// so the two sums are taken apart, each relative to a maximum of its own, and put together, in two passes.
+// In the first a set is a prefix: its rows are the new tokens of all its sequences, which all
 // see all of it, so its keys and values are read once for each 128 or 256 rows (up to 16: once), not once per sequence.  Its
 // unnormalised rows, maxima and sums stay in the workspace in fp32.  In the second a set is a sequence without its
-// prefix; what finishes a row adds the first pass's to it.
+// prefix (attn_tc_kernel again, or for few rows bqg_own.cuh); what finishes a row adds the first pass's to it.
 struct SharedParams : AttnParams {
     using Seq = SharedSeq;
     static constexpr bool SHARED = true;
@@ -470,11 +470,8 @@ template <int FMT, int D, int RT> struct AttnKernel {
     static constexpr int MT = D / 16;                         // M tiles of the second product
 
     // 64-token tiles of a sequence, and its units: all its rows (new tokens x heads of a group, at most ROWS) at once.
-    template <typename Seq> static __device__ __forceinline__ int tiles_of(const Seq &s)
-    {
-        return (s.len + kUnit - 1) / kUnit - attn_lo(s) / kUnit;
-    }
-    template <typename Seq> static __device__ __forceinline__ int64_t units(const AttnParams &p, const Seq &s, int lead)
+    static __device__ __forceinline__ int tiles_of(const AttnSeq &s) { return (s.len + kUnit - 1) / kUnit; }
+    static __device__ __forceinline__ int64_t units(const AttnParams &p, const AttnSeq &s, int lead)
     {
         return s.T ? (int64_t)p.cache.n_kv * (tiles_of(s) + lead) : 0;
     }
@@ -781,6 +778,111 @@ template <int FMT, int D, int RT> struct AttnKernel {
         }
         return __any_sync(0xffffffffu, bad);
     }
+
+    // What a warp has of its rows (this lane: 8 m + 2 t and the next): outputs and their maximum and sum so far.
+    struct Rows {
+        float o[RT][MT][4], top[RT][2], sum[RT][2], from[RT][2], rs[RT][2];   // from: what the exponents are relative to; softmax scale
+        __device__ __forceinline__ void begin(const float *row_scale, int t)
+        {
+#pragma unroll
+            for (int m = 0; m < RT; m++) {
+                rs[m][0] = row_scale[8 * m + 2 * t];
+                rs[m][1] = row_scale[8 * m + 2 * t + 1];
+                top[m][0] = top[m][1] = -__builtin_huge_valf();
+                sum[m][0] = sum[m][1] = 0.f;
+                from[m][0] = from[m][1] = kShift;
+#pragma unroll
+                for (int x = 0; x < MT; x++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) o[m][x][i] = 0.f;
+            }
+        }
+    };
+    // The strip in stage `st`, tokens tok0 .. of s, into w; ok: its page is in the cache.  bias: this lane's part of the row
+    // tiles' biases (make_q); row_sees: the new tokens that each row sees; pw: room for the probabilities of the exact path.
+    template <typename QF, typename Seq>
+    static __device__ __forceinline__ void strip(uint32_t st, int lane, const QF &qf, uint32_t bias, const unsigned long long *row_sees,
+                                                 const Seq &s, int tok0, bool ok, float *pw, Rows &w)
+    {
+        constexpr float NEG = -__builtin_huge_valf();
+        const int g = lane >> 2, t = lane & 3;
+        float sc[RT][4];
+        scores(st, lane, qf, bias, sc);
+        const bool edge = tok0 + kStrip > s.ctx || !ok || tok0 < attn_lo(s);   // new tokens, the end, no page, shared ones
+        if (edge) {
+#pragma unroll
+            for (int m = 0; m < RT; m++)
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    const unsigned long long sees = row_sees[8 * m + 2 * t + r];
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const int tok = tok0 + 8 * x + g;
+                        const bool see = ok && tok >= attn_lo(s) && (tok < s.ctx || (tok < s.len && ((sees >> (tok - s.ctx)) & 1)));
+                        if (!see) sc[m][2 * x + r] = NEG;
+                    }
+                }
+        }
+        // raise the running maximum where a score is well above it
+        bool raise = false;
+#pragma unroll
+        for (int m = 0; m < RT; m++)
+#pragma unroll
+            for (int r = 0; r < 2; r++) raise |= fmaxf(sc[m][r], sc[m][2 + r]) * w.rs[m][r] > w.top[m][r] + kSlack;
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int m = 0; m < RT; m++)
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    float v = fmaxf(sc[m][r], sc[m][2 + r]) * w.rs[m][r];
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    v = fmaxf(v, w.top[m][r]);
+                    const float c = (v == w.top[m][r]) ? 1.f : ex2(w.top[m][r] - v);
+                    w.top[m][r] = v;
+                    w.from[m][r] = kShift - (v == NEG ? 0.f : v);
+                    w.sum[m][r] *= c;
+#pragma unroll
+                    for (int x = 0; x < MT; x++) { w.o[m][x][r] *= c; w.o[m][x][2 + r] *= c; }
+                }
+        }
+        uint32_t pb[RT][2];
+        const bool exact = edge && any_nonfinite(st, lane);
+#pragma unroll
+        for (int m = 0; m < RT; m++) {
+            float e[4];
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                e[r] = ex2(fmaf(sc[m][r], w.rs[m][r], w.from[m][r]));
+                e[2 + r] = ex2(fmaf(sc[m][2 + r], w.rs[m][r], w.from[m][r]));
+                w.sum[m][r] += e[r] + e[2 + r];
+            }
+            pb[m][0] = transpose8x8(pack2<BF>(e[0], e[1]));
+            pb[m][1] = transpose8x8(pack2<BF>(e[2], e[3]));
+            if (exact) {
+                // an infinity or NaN (or a value that is one in fp16) among tokens that some rows do not see:
+                // 0 x inf must not reach them, so this strip's products are taken one by one in fp32
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; i++) pw[(8 * (i >> 1) + g) * 8 + 2 * t + (i & 1)] = sc[m][i] == NEG ? -1.f : e[i];
+                __syncwarp();
+#pragma unroll 1
+                for (int k = 0; k < kStrip; k++) {
+                    const float p0 = pw[k * 8 + 2 * t], p1 = pw[k * 8 + 2 * t + 1];
+#pragma unroll
+                    for (int x = 0; x < MT; x++)
+#pragma unroll
+                        for (int hi = 0; hi < 2; hi++) {
+                            const float v = value_of(st, k, dim_of(x, g, hi));
+                            if (!(p0 < 0.f)) w.o[m][x][2 * hi] = fmaf(p0, v, w.o[m][x][2 * hi]);
+                            if (!(p1 < 0.f)) w.o[m][x][2 * hi + 1] = fmaf(p1, v, w.o[m][x][2 * hi + 1]);
+                        }
+                }
+            }
+        }
+        if (!exact) add_values(st, lane, pb, w.o);
+    }
 };
 
 // Query fragments in registers, or shared by the CTA's warps in shared memory.
@@ -848,8 +950,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
         const int tiles = A::tiles_of(s);
         const int h = (int)div_pos(off, tiles + lead), first = (int)(off - (int64_t)h * (tiles + lead));
         const int take = (int)min((int64_t)(tiles + lead - first), u_end - u);
-        const int tile0 = max(first - lead, 0) + attn_lo(s) / kUnit;
-        const int n = first + take - lead + attn_lo(s) / kUnit - tile0;       // units of this piece
+        const int tile0 = max(first - lead, 0), n = first + take - lead - tile0;   // units of this piece
         if (n <= 0) {
             u += take;
             continue;
@@ -863,7 +964,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
         // pages of the warp's strips j0 .. j0 + 31, one per lane
         auto pages_from = [&](int j0) {
             const int tok0 = (tile0 + j0 + lane) * kUnit + warp * kStrip;
-            return (j0 + lane < n && tok0 < s.len && tok0 + kStrip > attn_lo(s)) ? table[tok0 >> p.cache.lp] : -1;
+            return (j0 + lane < n && tok0 < s.len) ? table[tok0 >> p.cache.lp] : -1;
         };
         int pages = pages_from(0);
         // queries (their loads are under way when the first strips are requested)
@@ -880,7 +981,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
             const int tok0 = (tile0 + j) * kUnit + warp * kStrip;
             const int page = __shfl_sync(0xffffffffu, pages, j & 31);
             valid &= ~(1u << st);
-            if (j < n && tok0 < s.len && tok0 + kStrip > attn_lo(s)) {
+            if (j < n && tok0 < s.len) {
                 const bool ok = page >= 0 && page < p.cache.n_pages;
                 if (!ok) pages_bad = BQG_DEVERR_PAGE;
                 valid |= (unsigned)ok << st;
@@ -927,20 +1028,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
         }
         if (tid < G::ROWS) row_sees[tid] = attn_sees(p, s, tid);
         __syncthreads();
-        float rs[RT][2];                                                      // rows 8 m + 2 t, + 1
-        float o[RT][MT][4], top[RT][2], sum[RT][2], from[RT][2];              // from: what the exponents are relative to
-#pragma unroll
-        for (int m = 0; m < RT; m++) {
-            rs[m][0] = row_scale[8 * m + 2 * t];
-            rs[m][1] = row_scale[8 * m + 2 * t + 1];
-            top[m][0] = top[m][1] = NEG;
-            sum[m][0] = sum[m][1] = 0.f;
-            from[m][0] = from[m][1] = A::kShift;
-#pragma unroll
-            for (int x = 0; x < MT; x++)
-#pragma unroll
-                for (int i = 0; i < 4; i++) o[m][x][i] = 0.f;
-        }
+        typename A::Rows r;
+        r.begin(row_scale, t);
 
         int stage = 0;                                                        // j % S
 #pragma unroll 1
@@ -953,85 +1042,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
             const uint32_t st = ring + stage * G::STAGE;
             const bool ok = (valid >> stage) & 1;
             stage = stage + 1 == S ? 0 : stage + 1;
-            if (P::SHARED && tok0 + kStrip <= attn_lo(s)) continue;           // all of it is shared
-
-            float sc[RT][4];
-            A::scores(st, lane, qf, sb + G::OFF_BIAS + t * 8, sc);
-            const bool edge = tok0 + kStrip > s.ctx || !ok || tok0 < attn_lo(s);   // new tokens, the end, no page, shared ones
-            if (edge) {
-#pragma unroll
-                for (int m = 0; m < RT; m++)
-#pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        const unsigned long long sees = row_sees[8 * m + 2 * t + r];
-#pragma unroll
-                        for (int x = 0; x < 2; x++) {
-                            const int tok = tok0 + 8 * x + g;
-                            const bool see = ok && tok >= attn_lo(s) && (tok < s.ctx || (tok < s.len && ((sees >> (tok - s.ctx)) & 1)));
-                            if (!see) sc[m][2 * x + r] = NEG;
-                        }
-                    }
-            }
-            // raise the running maximum where a score is well above it
-            bool raise = false;
-#pragma unroll
-            for (int m = 0; m < RT; m++)
-#pragma unroll
-                for (int r = 0; r < 2; r++) raise |= fmaxf(sc[m][r], sc[m][2 + r]) * rs[m][r] > top[m][r] + kSlack;
-            if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                for (int m = 0; m < RT; m++)
-#pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        float v = fmaxf(sc[m][r], sc[m][2 + r]) * rs[m][r];
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        v = fmaxf(v, top[m][r]);
-                        const float c = (v == top[m][r]) ? 1.f : ex2(top[m][r] - v);
-                        top[m][r] = v;
-                        from[m][r] = A::kShift - (v == NEG ? 0.f : v);
-                        sum[m][r] *= c;
-#pragma unroll
-                        for (int x = 0; x < MT; x++) { o[m][x][r] *= c; o[m][x][2 + r] *= c; }
-                    }
-            }
-            uint32_t pb[RT][2];
-            const bool exact = edge && A::any_nonfinite(st, lane);
-            float *const pw = reinterpret_cast<float *>(smem + G::OFF_P) + warp * 8 * kStrip;
-#pragma unroll
-            for (int m = 0; m < RT; m++) {
-                float e[4];
-#pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    e[r] = ex2(fmaf(sc[m][r], rs[m][r], from[m][r]));
-                    e[2 + r] = ex2(fmaf(sc[m][2 + r], rs[m][r], from[m][r]));
-                    sum[m][r] += e[r] + e[2 + r];
-                }
-                pb[m][0] = transpose8x8(pack2<A::BF>(e[0], e[1]));
-                pb[m][1] = transpose8x8(pack2<A::BF>(e[2], e[3]));
-                if (exact) {
-                    // an infinity or NaN (or a value that is one in fp16) among tokens that some rows do not see:
-                    // 0 x inf must not reach them, so this strip's products are taken one by one in fp32
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 4; i++) pw[(8 * (i >> 1) + g) * 8 + 2 * t + (i & 1)] = sc[m][i] == NEG ? -1.f : e[i];
-                    __syncwarp();
-#pragma unroll 1
-                    for (int k = 0; k < kStrip; k++) {
-                        const float p0 = pw[k * 8 + 2 * t], p1 = pw[k * 8 + 2 * t + 1];
-#pragma unroll
-                        for (int x = 0; x < MT; x++)
-#pragma unroll
-                            for (int hi = 0; hi < 2; hi++) {
-                                const float v = A::value_of(st, k, A::dim_of(x, g, hi));
-                                if (!(p0 < 0.f)) o[m][x][2 * hi] = fmaf(p0, v, o[m][x][2 * hi]);
-                                if (!(p1 < 0.f)) o[m][x][2 * hi + 1] = fmaf(p1, v, o[m][x][2 * hi + 1]);
-                            }
-                    }
-                }
-            }
-            if (!exact) A::add_values(st, lane, pb, o);
+            A::strip(st, lane, qf, sb + G::OFF_BIAS + t * 8, row_sees, s, tok0, ok,
+                     reinterpret_cast<float *>(smem + G::OFF_P) + warp * 8 * kStrip, r);
         }
         cp_async_wait<0>();
         __syncthreads();                                                      // the ring's memory is free
@@ -1040,23 +1052,23 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
 #pragma unroll
         for (int m = 0; m < RT; m++)
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 4);
-                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 8);
-                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 16);
-                const int row = 8 * m + 2 * t + r;
+            for (int i = 0; i < 2; i++) {
+                r.sum[m][i] += __shfl_xor_sync(0xffffffffu, r.sum[m][i], 4);
+                r.sum[m][i] += __shfl_xor_sync(0xffffffffu, r.sum[m][i], 8);
+                r.sum[m][i] += __shfl_xor_sync(0xffffffffu, r.sum[m][i], 16);
+                const int row = 8 * m + 2 * t + i;
                 if (g == 0) {
-                    ml[(warp * G::ROWS + row) * 2] = top[m][r];
-                    ml[(warp * G::ROWS + row) * 2 + 1] = sum[m][r];
+                    ml[(warp * G::ROWS + row) * 2] = r.top[m][i];
+                    ml[(warp * G::ROWS + row) * 2 + 1] = r.sum[m][i];
                 }
                 float *dst = merged + (warp * G::ROWS + row) * (D + G::PAD);
 #pragma unroll
                 for (int x = 0; x < MT; x++) {
                     if constexpr (A::BF) {
-                        dst[16 * x + g] = o[m][x][r];
-                        dst[16 * x + 8 + g] = o[m][x][2 + r];
+                        dst[16 * x + g] = r.o[m][x][i];
+                        dst[16 * x + 8 + g] = r.o[m][x][2 + i];
                     } else {
-                        *reinterpret_cast<float2 *>(dst + 16 * x + 2 * g) = make_float2(o[m][x][r], o[m][x][2 + r]);
+                        *reinterpret_cast<float2 *>(dst + 16 * x + 2 * g) = make_float2(r.o[m][x][i], r.o[m][x][2 + i]);
                     }
                 }
             }
@@ -1088,27 +1100,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
                     for (int e = 0; e < E; e++) v[e] += c * src[e];
                 }
                 if (last) {
-                    if constexpr (P::SHARED) {
+                    if constexpr (P::SHARED) {                                // a prefix: for the second pass
                         const int64_t at = shared_row(p, s, h, row);
-                        float *shared = p.rows + at * D + lane * E;
-                        if (!p.own) {
+                        float *dst = p.rows + at * D + lane * E;
 #pragma unroll
-                            for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(shared + e) = make_float2(v[e], v[e + 1]);
-                            if (lane == 0) *reinterpret_cast<float2 *>(p.rows_ml + at * 2) = make_float2(mt, l);
-                            continue;
-                        }
-                        if (s.lo) {
-                            const float2 q = __ldcg(reinterpret_cast<const float2 *>(p.rows_ml + at * 2));
-                            const float up = fmaxf(mt, q.x);
-                            const float a = mt == up ? 1.f : ex2(mt - up), b = q.x == up ? 1.f : ex2(q.x - up);
-                            l = l * a + q.y * b;
-#pragma unroll
-                            for (int e = 0; e < E; e += 2) {
-                                const float2 f = __ldcg(reinterpret_cast<const float2 *>(shared + e));
-                                v[e] = v[e] * a + f.x * b;
-                                v[e + 1] = v[e + 1] * a + f.y * b;
-                            }
-                        }
+                        for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(dst + e) = make_float2(v[e], v[e + 1]);
+                        if (lane == 0) *reinterpret_cast<float2 *>(p.rows_ml + at * 2) = make_float2(mt, l);
+                        continue;
                     }
                     attn_store_row<E>(out_row(row), v, l);
                 } else {

@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include "bqg_attn_tc.cuh"
+#include "bqg_own.cuh"
 
 namespace bqg {
 
@@ -152,6 +153,37 @@ template <int FMT, int D, typename P> cudaError_t attn_pick(const P &p, int64_t 
     return attn_tc_call<FMT, D, P>(p, error, plan, s, pdl);
 }
 
+// Own tokens, a piece per warp (bqg_own.cuh).
+template <int FMT, int D, int RT> cudaError_t own_call(SharedParams p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    using G = OwnGeom<FMT, D, RT>;
+    struct Kern {
+        void (*fn)(const SharedParams, int *) = own_kernel<FMT, D, RT>;
+        int most = kAttnMaxCtas / kAttnWarps;
+    } kern;
+    int ctas = 0;
+    if (cudaError_t e = attn_ctas(kern, 32 * kAttnWarps, G::SMEM, &ctas)) return e;
+    if (plan) {
+        plan->ws_bytes = kAttnHead + (size_t)2 * ctas * kAttnWarps * G::ROWS * (D + 2) * sizeof(float);
+        return cudaSuccess;
+    }
+    p.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.counters) + kAttnHead);
+    const unsigned grid = (unsigned)std::max(1.0, std::min((double)ctas, attn_most(p, kStrip, G::ROWS)));
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    attn_config(cfg, attr, dim3(grid), 32 * kAttnWarps, G::SMEM, s, pdl);
+    return cudaLaunchKernelEx(&cfg, kern.fn, p, error);
+}
+// Up to two row tiles (256 values: one), as the queries are held in registers; more rows go to tcgen05.  At 32 rows, 96 sequences of
+// 400 tokens, 8 heads on each of 8, bf16, two sets of 16 rows over the same tokens took as long as tcgen05 (75 us).
+template <int FMT, int D> cudaError_t own_pick(const SharedParams &p, int64_t rows, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
+{
+    if (rows <= 8) return own_call<FMT, D, 1>(p, error, plan, s, pdl);
+    if constexpr (D < 256)
+        if (rows <= 16) return own_call<FMT, D, 2>(p, error, plan, s, pdl);
+    return attn_tc_call<FMT, D, SharedParams>(p, error, plan, s, pdl);
+}
+
 // Shared tokens, then own ones (SharedParams).  Workspace: as for one pass, then the first one's rows.
 template <int FMT, int D>
 cudaError_t shared_call(SharedParams p, int *error, AttnPlan *plan, cudaStream_t s, bool pdl)
@@ -164,7 +196,7 @@ cudaError_t shared_call(SharedParams p, int *error, AttnPlan *plan, cudaStream_t
     AttnPlan a, b;
     const int64_t rows = (int64_t)p.max_q * p.group, shared = p.max_shared * p.group;
     if (cudaError_t e = attn_pick<FMT, D>(pre, shared, error, &a, s, pdl)) return e;
-    if (cudaError_t e = attn_pick<FMT, D>(p, rows, error, &b, s, pdl)) return e;
+    if (cudaError_t e = own_pick<FMT, D>(p, rows, error, &b, s, pdl)) return e;
     const size_t at = (std::max(a.ws_bytes, b.ws_bytes) + 255) & ~(size_t)255, all = (size_t)p.n_tokens * p.n_q;
     if (plan) {
         plan->ws_bytes = at + all * (D + 2) * sizeof(float);
@@ -174,7 +206,7 @@ cudaError_t shared_call(SharedParams p, int *error, AttnPlan *plan, cudaStream_t
     pre.rows_ml = p.rows_ml = p.rows + all * D;
     if (cudaError_t e = attn_pick<FMT, D>(pre, shared, error, nullptr, s, pdl)) return e;
     // the second pass may be set up while the first runs: it waits for it before it reads
-    return attn_pick<FMT, D>(p, rows, error, nullptr, s, true);
+    return own_pick<FMT, D>(p, rows, error, nullptr, s, true);
 }
 template <int FMT> cudaError_t shared_launch(const SharedParams &p, int D, AttnPlan *plan, cudaStream_t s, bool pdl)
 {
