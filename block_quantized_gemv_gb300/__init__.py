@@ -786,17 +786,28 @@ def shared_prefix_attention(q, cache: KVCache, block_table, ctx_len, q_start, ma
 # --- verification of drafts, and what follows from it for the cache -------------
 def _rows(t, cur, name, shape, dtype):
     """(pointer, row stride) of [rows, n] values, each row contiguous."""
+    if type(t) is torch.Tensor and t.get_device() == cur and t.dtype is dtype and t.shape == shape:
+        s = t.stride()
+        if s[1] == 1:
+            return t.data_ptr(), s[0] if shape[0] > 1 else shape[1]
+    return _rows_checked(t, name, shape, dtype)
+
+
+def _rows_checked(t, name, shape, dtype):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    check_device(t.device.index, cur, name)
+    check_device(t.device.index, _current_device(), name)
+    return t.data_ptr(), _row_stride(t, name, shape, dtype)
+
+
+def _row_stride(t, name, shape, dtype):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} is {list(t.shape)}, needs {list(shape)}")
-    s = t.stride()
-    if t.numel() and shape[1] > 1 and s[1] != 1:
+    if t.numel() and shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"each row of {name} must be contiguous")
-    return t.data_ptr(), s[0] if shape[0] > 1 else shape[1]
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def tree_verify(target, tokens, q_start, max_q: int, u, parent=None, draft=None, out=None, stream=None):

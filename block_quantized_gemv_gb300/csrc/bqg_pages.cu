@@ -230,7 +230,7 @@ cudaError_t launch_compact(CompactParams p, int fmt, int D, int sms, cudaStream_
 {
     if (cudaError_t e = device_error_word(&p.error)) return e;
     // as many CTAs as are resident together, if there are heads for them
-    p.slices = (int)std::min<int64_t>(2 * p.cache.n_kv, std::max<int64_t>(1, (int64_t)sms * 4 / p.n_seq));
+    p.slices = (int)std::min<int64_t>(2 * p.cache.n_kv, std::max<int64_t>(1, (int64_t)sms * 6 / p.n_seq));
     auto fn = fmt == BQG_Q8_0 ? compact_fn<BQG_Q8_0>(D) : fmt == BQG_Q4_0 ? compact_fn<BQG_Q4_0>(D) : compact_fn<BQG_BF16>(D);
     return launch(fn, p, (int64_t)p.n_seq * p.slices, s, pdl);
 }
