@@ -894,12 +894,18 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
                         for (int half = 0; half < G::HALVES; half++)
                             tma_box_2d(dst + half * G::HALF + lane * box * 128, side ? &vmap : &kmap, 64 * half, (int)q.row, bar);
                     if (fix) {
-                        // zeros behind the end and where there is no page; new tokens' infinities and NaN out, and marked
+                        // zeros behind the end (stored without a look at what is there: the last tile of a short sequence is mostly that,
+                        // and this warp's looking took 5 us of it) and where there is no page; new tokens' infinities and NaN out,
+                        // and marked
                         if (!(ok = wait(bar_land, lands++ & 1))) return;
                         bool hit = false;
                         constexpr int N = 4;                                 // chunks at a time (G::TT * D / 8 is a multiple of 32 N)
+                        const int end = (q.len * (D / 8) + 32 * N - 1) / (32 * N) * (32 * N);
+#pragma unroll 4
+                        for (int i = end + lane; i < G::TT * (D / 8); i += 32)
+                            sts128(dst + tc_chunk<G::TT>(i / (D / 8), i % (D / 8)), make_uint4(0, 0, 0, 0));
 #pragma unroll 1
-                        for (int i0 = (q.dead || (P::SHARED && q.lo) ? 0 : q.ctx) * (D / 8) / (32 * N) * (32 * N) + lane; i0 < G::TT * (D / 8); i0 += 32 * N) {
+                        for (int i0 = (q.dead || (P::SHARED && q.lo) ? 0 : q.ctx) * (D / 8) / (32 * N) * (32 * N) + lane; i0 < end; i0 += 32 * N) {
                             uint4 v[N];
 #pragma unroll
                             for (int n = 0; n < N; n++) v[n] = lds128(dst + tc_chunk<G::TT>((i0 + 32 * n) / (D / 8), (i0 + 32 * n) % (D / 8)));
