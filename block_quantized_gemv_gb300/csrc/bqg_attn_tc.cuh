@@ -492,141 +492,150 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
         float *const part_ml = p.part + (int64_t)2 * gridDim.x * G::ROWS * D;
         TcSet set{};                                                         // begun here, ended elsewhere
         int pieces = 0, tiles = 0, commits = 0, steps = 0;                   // before this piece
-        // A piece's queries are asked for before the results of the one before are written: its products are complete.
-        TcPiece d;                                                           // the piece before
-        bool have = false;
+        // of the piece being worked on
         int grow = 0, row = 0, qi = 0, qh = 0;
         bool row_ok = false, warp_ok = false;
         unsigned long long sees = 0;
         float top = NEG, sum = 0.f;
-        // queries, a row per CPR lanes: chunks per row, rows per step; bf16: the warp's 32 rows as they are; else rows that serve
-        // both streams, if there are two
-        constexpr int CPR = D / 8, RPI = 32 / CPR;
-        constexpr int QROWS = BF ? 32 : kTcHalf / G::SOFT, N = QROWS * CPR / 32;
-        const int first = BF ? (warp & 3) * 32 : warp * QROWS;
-        for (;;) {
-            const bool more = next();
-            if (!ok) break;
-            const uint32_t dst = sb + G::OFF_Q + (w.nq == 2 ? st : 0) * G::QTILE;
-            if (more) {
-                const int qrow = w.row0 + (BF ? (w.nq == 2 ? st * kTcHalf : 0) + r : first + lane % QROWS), i0 = qrow / p.group;
-                const int64_t mine = qrow < w.row0 + w.rows ? (int64_t)(w.s.q0 + i0) * p.q_stride
-                                                              + (int64_t)(w.h * p.group + qrow - i0 * p.group) * D : -1;
-                const int c = lane % CPR;
-#pragma unroll 4
-                for (int n = 0; n < N; n++) {
-                    const int64_t from = __shfl_sync(0xffffffffu, mine, n * RPI + lane / CPR);
-                    if (!BF || st == 0 || w.nq == 2)
-                        cp_async16(dst + tc_chunk<kTcHalf>(first + n * RPI + lane / CPR, c), p.q + (from >= 0 ? from + 8 * c : 0), from >= 0 ? 16 : 0);
-                }
-                cp_async_commit();
+        auto results = [&](const TcPiece &d) {
+            if (!(ok = wait(bar_meet, pieces & 1))) return;
+            tc_fence_after();
+            // nq = 2: this thread's row, all values; nq = 1: both streams hold the row, this thread takes half of its values
+            float w0 = 1.f, w1 = 0.f, mt = top, l = sum;
+            const bool both = !G::SINGLE && d.nq == 1;
+            if (both) {
+                const float m0 = ml[r * 2], l0 = ml[r * 2 + 1], m1 = ml[(kTcHalf + r) * 2], l1 = ml[(kTcHalf + r) * 2 + 1];
+                mt = fmaxf(m0, m1);
+                w0 = m0 == mt ? 1.f : ex2(m0 - mt);
+                w1 = m1 == mt ? 1.f : ex2(m1 - mt);
+                l = w0 * l0 + w1 * l1;
             }
-            if (have) {
-                if (!(ok = wait(bar_meet, pieces & 1))) break;
-                tc_fence_after();
-                // nq = 2: this thread's row, all values; nq = 1: both streams hold the row, this thread takes half of its values
-                float w0 = 1.f, w1 = 0.f, mt = top, l = sum;
-                const bool both = !G::SINGLE && d.nq == 1;
-                if (both) {
-                    const float m0 = ml[r * 2], l0 = ml[r * 2 + 1], m1 = ml[(kTcHalf + r) * 2], l1 = ml[(kTcHalf + r) * 2 + 1];
-                    mt = fmaxf(m0, m1);
-                    w0 = m0 == mt ? 1.f : ex2(m0 - mt);
-                    w1 = m1 == mt ? 1.f : ex2(m1 - mt);
-                    l = w0 * l0 + w1 * l1;
-                }
-                const uint32_t ta = lanes + G::O0 + (both ? 0 : 128 * st);
-                const int x0 = both ? st * (D / 2) : 0, x1 = both ? x0 + D / 2 : D;
-                const bool marked = nan_mark[pieces % kTcMarks] == (uint32_t)pieces + 1;
-                const int64_t slot = attn_slot_row<1>(blockIdx.x, d.c0, 0);
-                float lj = l;                                                    // with the shared tokens'
-                if (warp_ok) {
+            const uint32_t ta = lanes + G::O0 + (both ? 0 : 128 * st);
+            const int x0 = both ? st * (D / 2) : 0, x1 = both ? x0 + D / 2 : D;
+            const bool marked = nan_mark[pieces % kTcMarks] == (uint32_t)pieces + 1;
+            const int64_t slot = attn_slot_row<1>(blockIdx.x, d.c0, 0);
+            float lj = l;                                                    // with the shared tokens'
+            if (warp_ok) {
 #pragma unroll 1
-                    for (int x = x0; x < x1; x += 32) {
-                        uint32_t u[32];
-                        float v[32];
-                        tmem_ld32_nowait(ta + x, u);
-                        if (both) {
-                            uint32_t u1[32];
-                            tmem_ld32_nowait(lanes + G::O0 + 128 + x, u1);
-                            tmem_wait_ld(u);
-                            tmem_wait_ld(u1);
+                for (int x = x0; x < x1; x += 32) {
+                    uint32_t u[32];
+                    float v[32];
+                    tmem_ld32_nowait(ta + x, u);
+                    if (both) {
+                        uint32_t u1[32];
+                        tmem_ld32_nowait(lanes + G::O0 + 128 + x, u1);
+                        tmem_wait_ld(u);
+                        tmem_wait_ld(u1);
 #pragma unroll
-                            for (int y = 0; y < 32; y++) v[y] = __uint_as_float(u[y]) * w0 + __uint_as_float(u1[y]) * w1;
-                        } else {
-                            tmem_wait_ld(u);
+                        for (int y = 0; y < 32; y++) v[y] = __uint_as_float(u[y]) * w0 + __uint_as_float(u1[y]) * w1;
+                    } else {
+                        tmem_wait_ld(u);
 #pragma unroll
-                            for (int y = 0; y < 32; y++) v[y] = __uint_as_float(u[y]);
-                        }
-                        if (marked) {
-                            // infinities and NaN among the new tokens of this piece
-                            const int a = max(d.s.ctx, d.tile0 * G::TT), e = min(d.s.len, (d.tile0 + d.n) * G::TT);
+                        for (int y = 0; y < 32; y++) v[y] = __uint_as_float(u[y]);
+                    }
+                    if (marked) {
+                        // infinities and NaN among the new tokens of this piece
+                        const int a = max(d.s.ctx, d.tile0 * G::TT), e = min(d.s.len, (d.tile0 + d.n) * G::TT);
 #pragma unroll 1
-                            for (int t = a; t < e; t++) {
-                                const int page = p.table[(int64_t)attn_table_row(d.s) * p.max_pages + (t >> p.cache.lp)];
-                                if (page < 0 || page >= p.cache.n_pages) continue;
-                                const int64_t crow = kv_row(p.cache, ((int64_t)page << p.cache.lp) + (t & ((1 << p.cache.lp) - 1)), d.h);
-                                const bool see = (sees >> (t - d.s.ctx)) & 1;
+                        for (int t = a; t < e; t++) {
+                            const int page = p.table[(int64_t)attn_table_row(d.s) * p.max_pages + (t >> p.cache.lp)];
+                            if (page < 0 || page >= p.cache.n_pages) continue;
+                            const int64_t crow = kv_row(p.cache, ((int64_t)page << p.cache.lp) + (t & ((1 << p.cache.lp) - 1)), d.h);
+                            const bool see = (sees >> (t - d.s.ctx)) & 1;
 #pragma unroll
-                                for (int y = 0; y < 32; y++) {
-                                    const float f = tc_nonfinite<FMT, D>(p.cache, crow, x + y);
-                                    if (see) v[y] += f;
-                                }
+                            for (int y = 0; y < 32; y++) {
+                                const float f = tc_nonfinite<FMT, D>(p.cache, crow, x + y);
+                                if (see) v[y] += f;
                             }
-                        }
-                        if constexpr (P::SHARED)
-                            if (row_ok && d.c0 == d.c1) {
-                                const int64_t at = shared_row(p, d.s, d.h, row);
-                                float4 *shared = reinterpret_cast<float4 *>(p.rows + at * D + x);
-                                if (!p.own) {
-#pragma unroll
-                                    for (int y = 0; y < 32; y += 4) shared[y / 4] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
-                                } else if (d.s.lo) {
-                                    const float2 q = *reinterpret_cast<const float2 *>(p.rows_ml + at * 2);
-                                    const float up = fmaxf(mt, q.x);
-                                    const float a = mt == up ? 1.f : ex2(mt - up), b = q.x == up ? 1.f : ex2(q.x - up);
-                                    if (x == x0) lj = l * a + q.y * b;
-#pragma unroll
-                                    for (int y = 0; y < 32; y += 4) {
-                                        const float4 f = shared[y / 4];
-                                        v[y] = v[y] * a + f.x * b; v[y + 1] = v[y + 1] * a + f.y * b;
-                                        v[y + 2] = v[y + 2] * a + f.z * b; v[y + 3] = v[y + 3] * a + f.w * b;
-                                    }
-                                }
-                            }
-                        if (P::SHARED && !tc_own(p) && d.c0 == d.c1) {
-                            // (a prefix's rows have been written)
-                        } else if (row_ok && d.c0 == d.c1) {
-                            const float l = lj;
-                            const float inv_l = l == 0.f ? 0.f : 1.0f / l;
-                            uint16_t *dst = p.out + ((int64_t)(d.s.q0 + qi) * p.n_q + d.h * p.group + qh) * D + x;
-#pragma unroll
-                            for (int y = 0; y < 32; y += 8)
-                                *reinterpret_cast<uint4 *>(dst + y) =
-                                    make_uint4(pack2<true>(v[y] * inv_l, v[y + 1] * inv_l), pack2<true>(v[y + 2] * inv_l, v[y + 3] * inv_l),
-                                               pack2<true>(v[y + 4] * inv_l, v[y + 5] * inv_l), pack2<true>(v[y + 6] * inv_l, v[y + 7] * inv_l));
-                        } else if (row_ok) {
-                            float4 *dst = reinterpret_cast<float4 *>(p.part) + (slot * (D / 4) + x / 4) * G::ROWS + grow;
-#pragma unroll
-                            for (int y = 0; y < 32; y += 4) dst[y / 4 * G::ROWS] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
                         }
                     }
+                    if constexpr (P::SHARED)
+                        if (row_ok && d.c0 == d.c1) {
+                            const int64_t at = shared_row(p, d.s, d.h, row);
+                            float4 *shared = reinterpret_cast<float4 *>(p.rows + at * D + x);
+                            if (!p.own) {
+#pragma unroll
+                                for (int y = 0; y < 32; y += 4) shared[y / 4] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+                            } else if (d.s.lo) {
+                                const float2 q = *reinterpret_cast<const float2 *>(p.rows_ml + at * 2);
+                                const float up = fmaxf(mt, q.x);
+                                const float a = mt == up ? 1.f : ex2(mt - up), b = q.x == up ? 1.f : ex2(q.x - up);
+                                if (x == x0) lj = l * a + q.y * b;
+#pragma unroll
+                                for (int y = 0; y < 32; y += 4) {
+                                    const float4 f = shared[y / 4];
+                                    v[y] = v[y] * a + f.x * b; v[y + 1] = v[y + 1] * a + f.y * b;
+                                    v[y + 2] = v[y + 2] * a + f.z * b; v[y + 3] = v[y + 3] * a + f.w * b;
+                                }
+                            }
+                        }
+                    if (P::SHARED && !tc_own(p) && d.c0 == d.c1) {
+                        // (a prefix's rows have been written)
+                    } else if (row_ok && d.c0 == d.c1) {
+                        const float l = lj;
+                        const float inv_l = l == 0.f ? 0.f : 1.0f / l;
+                        uint16_t *dst = p.out + ((int64_t)(d.s.q0 + qi) * p.n_q + d.h * p.group + qh) * D + x;
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8)
+                            *reinterpret_cast<uint4 *>(dst + y) =
+                                make_uint4(pack2<true>(v[y] * inv_l, v[y + 1] * inv_l), pack2<true>(v[y + 2] * inv_l, v[y + 3] * inv_l),
+                                           pack2<true>(v[y + 4] * inv_l, v[y + 5] * inv_l), pack2<true>(v[y + 6] * inv_l, v[y + 7] * inv_l));
+                    } else if (row_ok) {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part) + (slot * (D / 4) + x / 4) * G::ROWS + grow;
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4) dst[y / 4 * G::ROWS] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+                    }
                 }
-                tc_fence_before();
-                if constexpr (P::SHARED)
-                    if (!p.own && d.c0 == d.c1 && row_ok && (d.nq == 2 || st == 0))
-                        *reinterpret_cast<float2 *>(p.rows_ml + shared_row(p, d.s, d.h, row) * 2) = make_float2(mt, l);
-                if (d.c0 != d.c1) {
-                    if (row_ok && (d.nq == 2 || st == 0))
-                        *reinterpret_cast<float2 *>(part_ml + (slot * G::ROWS + grow) * 2) = make_float2(mt, l);
-                    if (d.c0 == (int)blockIdx.x) set = TcSet{d.rows, d.row0, d.h, d.s.q0, d.c0, d.c1, attn_lo(d.s), 0};
-                }
-                tiles += d.n;
-                pieces++;
             }
-            if (!more) break;
-            d = w;
-            have = true;
-            const int np = d.n * d.nq;                                       // steps
+            tc_fence_before();
+            if constexpr (P::SHARED)
+                if (!p.own && d.c0 == d.c1 && row_ok && (d.nq == 2 || st == 0))
+                    *reinterpret_cast<float2 *>(p.rows_ml + shared_row(p, d.s, d.h, row) * 2) = make_float2(mt, l);
+            if (d.c0 != d.c1) {
+                if (row_ok && (d.nq == 2 || st == 0))
+                    *reinterpret_cast<float2 *>(part_ml + (slot * G::ROWS + grow) * 2) = make_float2(mt, l);
+                if (d.c0 == (int)blockIdx.x) set = TcSet{d.rows, d.row0, d.h, d.s.q0, d.c0, d.c1, attn_lo(d.s), 0};
+            }
+            tiles += d.n;
+            pieces++;
+        };
+        // Queries into shared memory, a row per CPR lanes: chunks per row, rows per step; bf16: the warp's 32 rows as they are; else
+        // rows that serve both streams, if there are two.
+        constexpr int CPR = D / 8, RPI = 32 / CPR;
+        constexpr int QROWS = BF ? 32 : kTcHalf / G::SOFT, N = QROWS * CPR / 32;
+        auto query_of = [&](int first) {                                     // this lane's row's, or -1
+            const int qrow = w.row0 + (BF ? (w.nq == 2 ? st * kTcHalf : 0) + r : first + lane % QROWS), i0 = qrow / p.group;
+            return qrow < w.row0 + w.rows
+                       ? (int64_t)(w.s.q0 + i0) * p.q_stride + (int64_t)(w.h * p.group + qrow - i0 * p.group) * D : -1;
+        };
+        // bf16: a piece's queries are asked for before the results of the one before (d) are written, whose products are complete by
+        // then (64 x 300 tokens, 16 new: 40.6 us, 45.0 otherwise; quantized, where they still have to be converted, 0 to 5 % slower).
+        TcPiece before;
+        bool have = false;
+        for (;;) {
+            if constexpr (BF) {
+                const bool more = next();
+                if (!ok) break;
+                if (more) {
+                    const int first = (warp & 3) * 32, c = lane % CPR;
+                    const int64_t mine = query_of(first);
+                    const uint32_t dst = sb + G::OFF_Q + (w.nq == 2 ? st : 0) * G::QTILE;
+#pragma unroll 4
+                    for (int n = 0; n < N; n++) {
+                        const int64_t from = __shfl_sync(0xffffffffu, mine, n * RPI + lane / CPR);
+                        if (st == 0 || w.nq == 2)
+                            cp_async16(dst + tc_chunk<kTcHalf>(first + n * RPI + lane / CPR, c), p.q + (from >= 0 ? from + 8 * c : 0), from >= 0 ? 16 : 0);
+                    }
+                    cp_async_commit();
+                }
+                if (have) results(before);
+                if (!ok || !more) break;
+                before = w;
+                have = true;
+            } else {
+                if (!next()) break;
+            }
+            const TcPiece &d = BF ? before : w;
             grow = d.nq == 2 ? st * kTcHalf + r : r;                         // row of the group
             row_ok = grow < d.rows;
             warp_ok = __any_sync(0xffffffffu, row_ok);
@@ -634,8 +643,24 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
             qi = row / p.group;
             qh = row - qi * p.group;
             sees = row_ok ? attn_sees(p, d.s, row) : 0;
-            cp_async_wait<0>();
-            if constexpr (!BF) {
+            if constexpr (BF) {
+                cp_async_wait<0>();
+            } else {
+                const int first = warp * QROWS, c = lane % CPR;
+                const int64_t mine = query_of(first);
+                const uint32_t dst = sb + G::OFF_Q;
+                constexpr int B = N < 16 ? N : 16;
+#pragma unroll 1
+                for (int n = 0; n < N; n += B) {
+                    uint4 v[B];
+#pragma unroll
+                    for (int i = 0; i < B; i++) {
+                        const int64_t from = __shfl_sync(0xffffffffu, mine, (n + i) * RPI + lane / CPR);
+                        v[i] = from >= 0 ? *reinterpret_cast<const uint4 *>(p.q + from + 8 * c) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < B; i++) sts128(dst + tc_chunk<kTcHalf>(first + (n + i) * RPI + lane / CPR, c), v[i]);
+                }
                 // two lanes per row: its largest value, the power of two, fp16
                 __syncwarp();
 #pragma unroll 1
@@ -670,6 +695,7 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_q);
 
+            const int np = d.n * d.nq;                                       // steps
             top = NEG;
             sum = 0.f;
             float rs = p.scale_log2;                                         // softmax scale of the row
@@ -761,8 +787,12 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
             ml[(st * kTcHalf + r) * 2 + 1] = sum;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_meet);
+            if constexpr (!BF) {
+                results(d);
+                if (!ok) break;
+            }
         }
-        cp_async_wait<0>();
+        if constexpr (BF) cp_async_wait<0>();                                // (after a wait that gave up)
         if (tid == 0) reinterpret_cast<TcSet *>(p.counters)[blockIdx.x] = ok ? set : TcSet{};
     } else if (warp < kTcBuildWarp) {
         if constexpr (G::QUANT) regs_less<G::REGS_OTHER>();
