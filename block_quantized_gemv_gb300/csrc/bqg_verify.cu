@@ -10,15 +10,20 @@
 //  * What decides on the drafts is a handful of numbers, loaded at once; a row of p (and q) is only read where a
 //    sum is needed: once per rejection of a sampled draft, once for the next token (the last rejection's sum serves for
 //    it).  So it is a stream of one or two rows per sequence, and for few sequences latency.
-//  * A cluster of up to 8 CTAs takes a sequence, each a contiguous part of the row.  The first one walks the tree and gives the
-//    others their orders (a sum, or the end) through shared memory, two cluster barriers each: who arrives how
+//  * A cluster of up to 8 CTAs takes a sequence, each warp a contiguous part of the row.  The first warp walks the tree and
+//    puts its orders (a sum, or the end) into every CTA's shared memory, two cluster barriers for each: who arrives how
 //    often is decided in one place.
 //  * An answer is a whole number and depends on where a sum of up to 2^18 terms crosses a border, so fp32 sums (off by 1e-7:
 //    another token once in some hundred draws) would not do, and fp64's rate is 1/64 of fp32's here: p - c q is
-//    formed as an fp32 pair with the products' and the difference's errors, and added with error-free sums:
-//    about 2^-45 of the sum.  The few numbers of the walk itself are fp64.
-//  * The crossing is looked for in the sums of CTAs, of warps (contiguous ranges), then in the warp's range, which one
-//    warp reads again: first lane by lane, then token by token.
+//    formed as an fp32 pair with the products' and the difference's errors, and added with error-free sums, two
+//    at a time: about 2^-45 of the sum.  The walk's few numbers are pairs too: with fp64 a draft cost 900 cycles, with pairs 200.
+//  * The crossing is looked for in the warps' sums, then by the warp that holds it in the sums that it kept (of 32 lanes and up
+//    to 16 steps), then in the 16 bytes of one lane: nothing of the row is read again but those.  There the sums are
+//    whole numbers of 2^-61 of all.  (Reading the warp's part again took 7 us of 18, most of it for fetching instructions that run once.)
+//  * Measured: one chain of 5 sampled drafts, 32,000 tokens, fp32: 9.0 us: about 3 for the launch, 1.6 until the deciding numbers
+//    are there, 3 for the rejection's sum (barriers 1.2), 1.9 for the token.  16 chosen trees, 100,003, bf16: 11 us.  64 sampled trees
+//    of up to 10, 131,072, fp32: 44 us, 10 for the bytes: the first sums run at the copy rate; then trees with up to five rejections wait
+//    for one pass after the other, from L2 (2.5 to 7 us each).
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -186,7 +191,7 @@ template <bool F32, bool DRAFT, int kWarps> struct Verify {
     static constexpr int E = Row<F32>::E;
     static constexpr int kStep = 32 * E;                  // values that a warp takes at once: 16 bytes per lane
     static constexpr int kKept = kWarps == 16 ? 8 : 16;   // parts of a warp's range whose sums are kept
-    static constexpr int U = kWarps == 16 ? 4 : 2;        // steps whose loads are in flight together
+    static constexpr int U = kWarps == 16 && !DRAFT ? 4 : 2;   // steps whose loads are in flight together
 
     // Which of the rejected tokens lie in [a, e).
     static __device__ __forceinline__ unsigned long long gone_in(const Order &o, int a, int e, int lane)
@@ -375,7 +380,7 @@ __device__ __forceinline__ bool accepted(const Draft &d, const Pair &r, const Pa
 }
 
 template <bool F32, bool DRAFT, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 1) verify_kernel(const VerifyParams p, int ctas)
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kernel(const VerifyParams p, int ctas)
 {
     namespace cg = cooperative_groups;
     using V = Verify<F32, DRAFT, kWarps>;
@@ -609,10 +614,11 @@ template <bool F32, bool DRAFT, int kWarps> cudaError_t run_warps(const VerifyPa
     cfg.numAttrs = pdl ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, verify_kernel<F32, DRAFT, kWarps>, p, ctas);
 }
-// 16 warps per CTA while all CTAs are resident together that way, for the shorter rows; else 8.
+// 16 warps per CTA, two CTAs per SM, while all clusters are resident together that way (with one CTA per SM a GPU's clusters of
+// 8 leave SMs over: 16 of them took 17 us instead of 11); else 8 warps, four CTAs per SM (64 sequences: 44 us, 48 with 16).
 template <bool F32, bool DRAFT> cudaError_t run(const VerifyParams &p, int ctas, int sms, cudaStream_t s, bool pdl)
 {
-    return (int64_t)p.n_seq * ctas <= sms ? run_warps<F32, DRAFT, 16>(p, ctas, s, pdl) : run_warps<F32, DRAFT, 8>(p, ctas, s, pdl);
+    return 2 * (int64_t)p.n_seq * ctas <= 3 * sms ? run_warps<F32, DRAFT, 16>(p, ctas, s, pdl) : run_warps<F32, DRAFT, 8>(p, ctas, s, pdl);
 }
 
 }  // namespace

@@ -134,6 +134,18 @@ def test_large_vocabularies(dtype, drafted, V):
     Case(V, [4, 7, 1], dtype, drafted, False, seed=V, sharp=3.0).check(number=float)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("drafted", [False, True])
+def test_many_large_vocabularies(dtype, drafted):
+    """More sequences than have sixteen warps per CTA, more tokens than a warp's kept sums are single steps of."""
+    Case(140001, [1, 2] * 18, dtype, drafted, False, seed=5, sharp=3.0).check(number=float)
+
+
+@pytest.mark.parametrize("drafted", [False, True])
+def test_the_largest_vocabularies(drafted):
+    Case(600011, [3, 1], torch.bfloat16, drafted, False, seed=6, sharp=3.0).check(number=float)
+
+
 @pytest.mark.parametrize("drafted", [False, True])
 @pytest.mark.parametrize("u", [0.0, 1 - 2.0 ** -24])
 def test_smallest_and_largest_numbers(drafted, u):
