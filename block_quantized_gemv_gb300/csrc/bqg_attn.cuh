@@ -224,7 +224,7 @@ struct SharedParams : AttnParams {
     int n_prefix, n_all;                     // prefixes, sequences (n_seq: sets of this pass)
     int64_t max_shared;                      // new tokens behind one prefix at most
     int own;                                 // the second pass
-    float *rows, *rows_ml;                   // [n_tokens][n_q][D] unnormalised, (maximum, sum) pairs
+    float *rows, *rows_ml;                   // unnormalised (see shared_at), (maximum, sum) pairs
 };
 // Prefix g: its sequences, their query tokens and the shared tokens (none where the arguments do not fit, which
 // `bad` then tells: both passes come to the same answer).
@@ -274,11 +274,16 @@ __device__ __forceinline__ SharedSeq attn_seq(const SharedParams &p, int b, int 
     }
     return s;
 }
-// Row `row` of (set, KV head) in SharedParams::rows.
+// Number of row `row` of (set, KV head) in SharedParams::rows: a set's rows follow each other.
 __device__ __forceinline__ int64_t shared_row(const SharedParams &p, const SharedSeq &s, int h, int row)
 {
-    const int i = row / p.group;
-    return (int64_t)(s.q0 + i) * p.n_q + h * p.group + (row - i * p.group);
+    return ((int64_t)h * p.n_tokens + s.q0) * p.group + row;
+}
+// Where values 4 i .. 4 i + 3 of it are: blocks of 32 rows, [D / 4][32][4], so that who has a row per lane (tcgen05's results) writes
+// and reads 512 contiguous bytes (with whole rows, 32 lines per instruction, a small prefix's results took 6 us of its 16).
+template <int D> __device__ __forceinline__ float4 *shared_at(const SharedParams &p, int64_t line, int i)
+{
+    return reinterpret_cast<float4 *>(p.rows) + ((line >> 5) * (D / 4) + i) * 32 + (line & 31);
 }
 // The set that lane `from` holds (but for its number).
 __device__ __forceinline__ AttnSeq attn_shfl(const AttnSeq &s, int from)
@@ -1102,9 +1107,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
                 if (last) {
                     if constexpr (P::SHARED) {                                // a prefix: for the second pass
                         const int64_t at = shared_row(p, s, h, row);
-                        float *dst = p.rows + at * D + lane * E;
+                        if constexpr (E == 2) {
+                            reinterpret_cast<float2 *>(shared_at<D>(p, at, lane >> 1))[lane & 1] = make_float2(v[0], v[1]);
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(dst + e) = make_float2(v[e], v[e + 1]);
+                            for (int e = 0; e < E; e += 4)
+                                *shared_at<D>(p, at, (lane * E + e) / 4) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        }
                         if (lane == 0) *reinterpret_cast<float2 *>(p.rows_ml + at * 2) = make_float2(mt, l);
                         continue;
                     }

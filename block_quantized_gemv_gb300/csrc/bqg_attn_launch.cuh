@@ -197,7 +197,7 @@ cudaError_t shared_call(SharedParams p, int *error, AttnPlan *plan, cudaStream_t
     const int64_t rows = (int64_t)p.max_q * p.group, shared = p.max_shared * p.group;
     if (cudaError_t e = attn_pick<FMT, D>(pre, shared, error, &a, s, pdl)) return e;
     if (cudaError_t e = own_pick<FMT, D>(p, rows, error, &b, s, pdl)) return e;
-    const size_t at = (std::max(a.ws_bytes, b.ws_bytes) + 255) & ~(size_t)255, all = (size_t)p.n_tokens * p.n_q;
+    const size_t at = (std::max(a.ws_bytes, b.ws_bytes) + 255) & ~(size_t)255, all = ((size_t)p.n_tokens * p.n_q + 31) & ~(size_t)31;
     if (plan) {
         plan->ws_bytes = at + all * (D + 2) * sizeof(float);
         return cudaSuccess;

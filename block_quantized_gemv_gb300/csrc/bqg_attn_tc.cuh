@@ -189,9 +189,20 @@ template <int NQ, int TT, typename P> struct TcWork {
             for (int b = lane + 32; b < p.n_seq; b += 32) n += p.cache.n_kv * pieces(p, attn_seq(p, b, ignored), m).head;
             return __reduce_add_sync(0xffffffffu, n);
         };
+        unsigned pieces_all = 0;
         if (total < (1 << 28) && (int64_t)p.n_seq * p.cache.n_kv <= gridDim.x) {
-            int lo = ((int)per + NQ - 1) / NQ - 1, hi = ((int)per + kTcSecond<NQ>) / NQ;      // too small; enough, if any is
-            if (count(hi * NQ) <= gridDim.x) {
+            // The smallest that leaves no CTA a second piece.  A few are tried one after the other, by one copy of the code: this runs once and
+            // mostly waits for its instructions.  (Not in the quantized kernels of bqg_tree_attention: their registers are at
+            // the limit, and with this they took up to 5 % longer.)
+            const int first = ((int)per + NQ - 1) / NQ, last = ((int)per + kTcSecond<NQ>) / NQ;
+            if constexpr (P::SHARED || NQ == 2) {
+#pragma unroll 1
+                for (int m = first; m <= last && !most; m++) {
+                    pieces_all = count(m * NQ);
+                    if (pieces_all <= gridDim.x) most = m * NQ;
+                }
+            } else if (count(last * NQ) <= gridDim.x) {
+                int lo = first - 1, hi = last;
                 while (hi - lo > 1) {
                     const int m = (lo + hi) >> 1;
                     (count(m * NQ) <= gridDim.x ? hi : lo) = m;
@@ -203,7 +214,7 @@ template <int NQ, int TT, typename P> struct TcWork {
             auto number = [&](const Seq &q) { return (int64_t)p.cache.n_kv * pieces(p, q, most).head; };
             mine = lane < p.n_seq ? number(s) : 0;
             cur = blockIdx.x;
-            end = min(cur + 1, (int64_t)count(most));
+            end = min(cur + 1, (int64_t)(P::SHARED || NQ == 2 ? pieces_all : count(most)));
             base = 0;
             if (cur < end) s = attn_find(p, cur, lane, number, s, mine, base);
             return;
@@ -552,10 +563,10 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
                     if constexpr (P::SHARED)
                         if (row_ok && d.c0 == d.c1) {
                             const int64_t at = shared_row(p, d.s, d.h, row);
-                            float4 *shared = reinterpret_cast<float4 *>(p.rows + at * D + x);
+                            float4 *shared = shared_at<D>(p, at, x / 4);
                             if (!p.own) {
 #pragma unroll
-                                for (int y = 0; y < 32; y += 4) shared[y / 4] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
+                                for (int y = 0; y < 32; y += 4) shared[y / 4 * 32] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
                             } else if (d.s.lo) {
                                 const float2 q = *reinterpret_cast<const float2 *>(p.rows_ml + at * 2);
                                 const float up = fmaxf(mt, q.x);
@@ -563,7 +574,7 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
                                 if (x == x0) lj = l * a + q.y * b;
 #pragma unroll
                                 for (int y = 0; y < 32; y += 4) {
-                                    const float4 f = shared[y / 4];
+                                    const float4 f = shared[y / 4 * 32];
                                     v[y] = v[y] * a + f.x * b; v[y + 1] = v[y + 1] * a + f.y * b;
                                     v[y + 2] = v[y + 2] * a + f.z * b; v[y + 3] = v[y + 3] * a + f.w * b;
                                 }
@@ -1195,10 +1206,10 @@ template <int D, int ROWS, typename P = AttnParams> __global__ void __launch_bou
         SharedSeq s{};
         s.q0 = set.q0;
         const int64_t at = shared_row(p, s, set.h, set.row0 + row);
-        float4 *shared = reinterpret_cast<float4 *>(p.rows + at * D + warp * 4 * V);
+        float4 *shared = shared_at<D>(p, at, warp * V);
         if (!p.own) {
 #pragma unroll
-            for (int i = 0; i < V; i++) shared[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < V; i++) shared[i * 32] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             if (warp == 0) *reinterpret_cast<float2 *>(p.rows_ml + at * 2) = make_float2(mt, l);
             return;
         }
@@ -1209,7 +1220,7 @@ template <int D, int ROWS, typename P = AttnParams> __global__ void __launch_bou
             l = l * a + q.y * b;
 #pragma unroll
             for (int i = 0; i < V; i++) {
-                const float4 f = shared[i];
+                const float4 f = shared[i * 32];
                 v[4 * i] = v[4 * i] * a + f.x * b; v[4 * i + 1] = v[4 * i + 1] * a + f.y * b;
                 v[4 * i + 2] = v[4 * i + 2] * a + f.z * b; v[4 * i + 3] = v[4 * i + 3] * a + f.w * b;
             }

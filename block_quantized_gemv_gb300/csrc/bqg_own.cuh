@@ -239,11 +239,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps) own_kernel(const SharedParams
                 };
                 float2 q[R];
                 float a[R][E];
-                auto fetch = [&](int i, const float *m, const float *src) {
+                // (far: from four values to the next four)
+                auto fetch = [&](int i, const float *m, const float *src, int far) {
                     q[i] = __ldcg(reinterpret_cast<const float2 *>(m));
 #pragma unroll
                     for (int e = 0; e < E; e += 2) {
-                        const float2 f = __ldcg(reinterpret_cast<const float2 *>(src + e));
+                        const float2 f = __ldcg(reinterpret_cast<const float2 *>(src + e / 4 * far + e % 4));
                         a[i][e] = f.x; a[i][e + 1] = f.y;
                     }
                 };
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) own_kernel(const SharedParams
                     for (int i = 0; i < R; i++)
                         if (row + i < rows) {
                             const int64_t at = attn_slot_row<ROWS>(c, c0, row + i);
-                            fetch(i, part_ml + at * 2, p.part + at * D + lane * E);
+                            fetch(i, part_ml + at * 2, p.part + at * D + lane * E, 4);
                         }
 #pragma unroll
                     for (int i = 0; i < R; i++)
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) own_kernel(const SharedParams
                     for (int i = 0; i < R; i++)
                         if (row + i < rows) {
                             const int64_t at = shared_row(p, s, h, row + i);
-                            fetch(i, p.rows_ml + at * 2, p.rows + at * D + lane * E);
+                            fetch(i, p.rows_ml + at * 2, reinterpret_cast<const float *>(shared_at<D>(p, at, lane * E / 4)) + lane * E % 4, 128);
                         }
                 }
                 if (c0 == c1) {
