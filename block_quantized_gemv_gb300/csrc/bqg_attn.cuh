@@ -351,7 +351,7 @@ __device__ __forceinline__ int64_t attn_total(const P &p, int lane, W weight, in
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     return total;
 }
-// The sequence that holds number u (below the total) of the line of all sequences' units; `base`: the number of its first.
+// The sequence that holds number u of the line of all sequences' units; `base`: the number of its first (past u: none does).
 template <typename P, typename W>
 __device__ __forceinline__ typename P::Seq attn_find(const P &p, int64_t u, int lane, W weight, typename P::Seq s, int64_t mine,
                                                      int64_t &base)
@@ -382,7 +382,8 @@ __device__ __forceinline__ typename P::Seq attn_find(const P &p, int64_t u, int 
         }
         base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    return s;            // not reached
+    base = u + 1;
+    return s;
 }
 
 // A finished row: E = D / 32 values per lane, divided by their sum of weights, in bf16.

@@ -87,12 +87,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps) own_kernel(const SharedParams
         attn_check_ends(p, bad);
         if (bad) atomicOr(error, bad);
     }
-    if (few) total = attn_total(p, lane, weight, bad, s, mine);
-    int64_t u = per * me;
-    const int64_t u_end = min(u + per, total);
-    if (u >= u_end) return pdl_wait();                                        // (this launch does not end before the first pass's)
-    int64_t base;
-    s = attn_find(p, u, lane, weight, s, mine, base);
+    int64_t u = per * me, base = u;
+    const int64_t u_end = few ? u + per : min(u + per, total);
+    if (u < u_end) {
+        mine = lane < p.n_seq ? weight(s) : 0;                                // (in whole ranges now)
+        s = attn_find(p, u, lane, weight, s, mine, base);
+    }
+    if (u >= u_end || base > u) return pdl_wait();                            // (this launch does not end before the first pass's)
     int pages_bad = 0;
 
     while (u < u_end) {
