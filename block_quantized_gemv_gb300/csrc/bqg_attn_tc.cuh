@@ -178,13 +178,22 @@ template <int NQ, int TT, typename P> struct TcWork {
     __device__ __forceinline__ void init(const P &p, int lane, int &bad)
     {
         auto weight = [&](const Seq &q) { return cost(p, q); };
-        int64_t mine;
-        const int64_t total = attn_total(p, lane, weight, bad, s, mine);
+        int64_t mine, total;
+        // One set of tokens (a prefix of all sequences, one sequence) needs no look at others: sums and searches over lanes are most of
+        // the planning's instructions.
+        const bool one = (P::SHARED || NQ == 2) && p.n_seq == 1;
+        if (one) {
+            s = attn_seq(p, 0, bad);
+            total = cost(p, s);
+        } else {
+            total = attn_total(p, lane, weight, bad, s, mine);
+        }
         // at least NQ, so that every range between a set's first and last holds the beginning of a tile
         per = max(div_pos(total + gridDim.x - 1, gridDim.x), (int64_t)NQ);
         most = 0;
         auto count = [&](int m) {
             int ignored = 0;
+            if (one) return (unsigned)(p.cache.n_kv * pieces(p, s, m).head);
             unsigned n = lane < p.n_seq ? p.cache.n_kv * pieces(p, s, m).head : 0;
             for (int b = lane + 32; b < p.n_seq; b += 32) n += p.cache.n_kv * pieces(p, attn_seq(p, b, ignored), m).head;
             return __reduce_add_sync(0xffffffffu, n);
@@ -212,17 +221,18 @@ template <int NQ, int TT, typename P> struct TcWork {
         }
         if (most) {
             auto number = [&](const Seq &q) { return (int64_t)p.cache.n_kv * pieces(p, q, most).head; };
-            mine = lane < p.n_seq ? number(s) : 0;
             cur = blockIdx.x;
             end = min(cur + 1, (int64_t)(P::SHARED || NQ == 2 ? pieces_all : count(most)));
             base = 0;
+            if (one) return;
+            mine = lane < p.n_seq ? number(s) : 0;
             if (cur < end) s = attn_find(p, cur, lane, number, s, mine, base);
             return;
         }
         cur = per * blockIdx.x;
         end = min(cur + per, total);
         base = 0;
-        if (cur < end) s = attn_find(p, cur, lane, weight, s, mine, base);
+        if (!one && cur < end) s = attn_find(p, cur, lane, weight, s, mine, base);
     }
     __device__ __forceinline__ bool next(const P &p, TcPiece &o)
     {
