@@ -80,7 +80,7 @@ def run(block, prompt=40, rounds=3, visit=None):
         probs, _, kept, path, token = got
         for b in range(2):
             answers[b] += [int(tokens[b * T + i]) for i in path[b, 1:int(kept[b])]] + [int(token[b])]
-        # the next trees: the new token, and the likeliest ones of this round's last row as its drafts
+        # the next trees: the new token, and the likeliest ones of the last accepted token's row as its drafts
         best = probs[torch.stack([path[b, int(kept[b]) - 1] + b * T for b in range(2)]).long()].topk(T - 1).indices.int()
         tokens, ctx = torch.cat([token[:, None], best], 1).reshape(-1).contiguous(), new
     return answers

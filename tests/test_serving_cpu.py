@@ -24,7 +24,7 @@ def verify(L, **kw):
 
 
 def compact(L, **kw):
-    a = dict(table=FAKE, pages=10, ctx=FAKE, path=FAKE, n_path=FAKE, n_seq=2, max_q=3, new=FAKE + 64)
+    a = dict(table=FAKE, pages=10, ctx=FAKE, path=FAKE + 128, n_path=FAKE + 256, n_seq=2, max_q=3, new=FAKE + 64)
     c = kw.pop("cache", {})
     a.update(kw)
     return L.bqg_kv_compact(cache(**c) if c is not None else None, *a.values(), None)
@@ -65,6 +65,7 @@ def test_bad_caches_are_refused(L, bad, status):
     (compact, dict(cache=None), 1), (compact, dict(table=None), 1), (compact, dict(ctx=None), 1), (compact, dict(path=None), 1),
     (compact, dict(n_path=None), 1), (compact, dict(n_seq=-1), 1), (compact, dict(max_q=0), 1), (compact, dict(pages=0), 1),
     (compact, dict(new=FAKE), 1), (compact, dict(new=FAKE + 4), 1), (compact, dict(ctx=FAKE + 68), 1),
+    (compact, dict(new=FAKE + 260), 1), (compact, dict(new=FAKE + 148), 1),
     (compact, dict(max_q=65), 2), (compact, dict(pages=1 << 32), 2),
     (compact, dict(table=FAKE + 2), 3), (compact, dict(path=FAKE + 1), 3), (compact, dict(new=FAKE + 66), 3),
     (fork, dict(cache=None), 1), (fork, dict(table=None), 1), (fork, dict(ctx=None), 1), (fork, dict(parent=None), 1),
