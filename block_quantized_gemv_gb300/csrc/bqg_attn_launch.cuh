@@ -193,11 +193,19 @@ cudaError_t shared_call(SharedParams p, int *error, AttnPlan *plan, cudaStream_t
     pre.n_seq = p.n_prefix;
     pre.max_q = (int)p.max_shared;
     p.own = 1;
-    AttnPlan a, b;
     const int64_t rows = (int64_t)p.max_q * p.group, shared = p.max_shared * p.group;
-    if (cudaError_t e = attn_pick<FMT, D>(pre, shared, error, &a, s, pdl)) return e;
-    if (cudaError_t e = own_pick<FMT, D>(p, rows, error, &b, s, pdl)) return e;
-    const size_t at = (std::max(a.ws_bytes, b.ws_bytes) + 255) & ~(size_t)255, all = ((size_t)p.n_tokens * p.n_q + 31) & ~(size_t)31;
+    // room for every kernel that as many rows or fewer go to: a workspace for more serves fewer
+    size_t at = 0;
+    for (const int64_t r : {(int64_t)1, (int64_t)9, (int64_t)17}) {
+        AttnPlan a{}, b{};
+        if (r <= shared)
+            if (cudaError_t e = attn_pick<FMT, D>(pre, r, error, &a, s, pdl)) return e;
+        if (r <= rows)
+            if (cudaError_t e = own_pick<FMT, D>(p, r, error, &b, s, pdl)) return e;
+        at = std::max({at, a.ws_bytes, b.ws_bytes});
+    }
+    at = (at + 255) & ~(size_t)255;
+    const size_t all = ((size_t)p.n_tokens * p.n_q + 31) & ~(size_t)31;
     if (plan) {
         plan->ws_bytes = at + all * (D + 2) * sizeof(float);
         return cudaSuccess;

@@ -286,3 +286,55 @@ def test_workspace_is_required():
     with pytest.raises(ValueError):
         c.prefix = torch.zeros(2, dtype=torch.int32, device="cuda")
         c.run(seq_start=None)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [1, 9])
+def test_pages_beyond_32_bits_of_bytes(fmt, T):
+    """The same pages at the end of a cache of more than 2^32 bytes a side: the same bits."""
+    small = Shared(fmt, 128, 2, 4, [100], [3], [40, 0, 70], [T, 1, T], page=64, seed=4)
+    want = small.run()
+    row = 2 * 64 * (256 if fmt == bqg.BF16 else 128 if fmt == bqg.Q8_0 else 64)
+    old = small.cache
+    shift = 2 ** 32 // row + 1
+    small.cache = bqg.kv_cache(fmt, shift + old.n_pages, 2, 64, 128)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        if getattr(old, name) is not None:
+            getattr(small.cache, name)[shift:] = getattr(old, name)
+    small.table = torch.where(small.table < 0, small.table, small.table + shift)
+    assert torch.equal(small.run().view(torch.int16), want.view(torch.int16))
+    assert bqg.last_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_calls_in_turn_on_one_workspace_leave_nothing_behind(fmt):
+    """Two captured calls of different sequences on one workspace, replayed in turns, with and without a prefix."""
+    a = Shared(fmt, 128, 2, 4, [300], [5], [30, 0, 70, 9, 1], [2, 1, 4, 1, 1], page=32, seed=4)
+    b = Shared(fmt, 128, 2, 4, [0, 50], [2, 3], [200, 0, 70, 9, 1], [1, 1, 30, 1, 3], page=32, seed=5)
+    ws = torch.zeros(max(a.ws.numel(), b.ws.numel()), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c in (a, b):
+        c.ws = ws
+        out = torch.zeros_like(c.q)
+        c.run(out=out)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(out=out)
+        graphs.append((c, g, out, c.run()))
+    for _ in range(3):
+        for c, g, out, want in graphs:
+            out.fill_(7)
+            g.replay()
+            assert torch.equal(out, want)
+            c.check(out)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_workspace_for_more_serves_fewer(fmt, D):
+    cache = bqg.kv_cache(fmt, 1, 1, 16, D)
+    size = lambda group, q, n, most: bqg.shared_prefix_attention_workspace(cache, group, 64, q, n, 1, max_shared=most).numel()
+    for group in (1, 2, 3, 5, 8, 16, 64):
+        for sizes in ([size(group, q, 64, 64) for q in range(1, 65)], [size(group, 1, 64, m) for m in range(0, 65)],
+                      [size(group, 3, n, 64) for n in range(1, 130)]):
+            assert sizes == sorted(sizes), (group, sizes)
