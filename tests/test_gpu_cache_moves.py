@@ -237,3 +237,33 @@ def test_streams_and_graphs():
         got = bqg.kv_compact(c.cache, **dict(a, n_path=i32([0, 0])))
     side.synchronize()
     assert got.tolist() == [40, 7]
+
+
+def test_pages_beyond_32_bits_of_bytes():
+    """A path and a fork at the end of a cache of more than 2^32 bytes a side."""
+    n_kv, page, D = 2, 64, 128
+    shift = 2 ** 32 // (n_kv * page * D * 2) + 1
+    c = bqg.kv_cache(bqg.BF16, shift + 8, n_kv, page, D)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for t in (c.k, c.v):
+        t[shift:] = torch.randn(8, n_kv, page, D, generator=g, device="cuda").to(torch.bfloat16)
+    k, v = c.k[shift:].clone(), c.v[shift:].clone()
+    ctx, path = 60, [0, 3, 9]
+    table = i32([[shift + 5, shift + 2]])
+    assert bqg.kv_compact(c, table, i32([ctx]), i32([path]), i32([3])).item() == 63
+    order = [5, 2]
+    for old, t in ((k, c.k), (v, c.v)):
+        want = old.clone()
+        for i, a in enumerate(path):
+            x, y = ctx + a, ctx + i
+            want[order[y // page], :, y % page] = old[order[x // page], :, x % page]
+        assert torch.equal(t[shift:], want) and not t[:8].any()
+    k, v = c.k[shift:].clone(), c.v[shift:].clone()
+    rows, n = i32([[shift + 5, shift + 2], [0, 0]]), i32([100, 0])
+    bqg.kv_fork(c, rows, n, i32([0]), i32([1]), i32([shift + 7]))
+    for old, t in ((k, c.k), (v, c.v)):
+        want = old.clone()
+        want[7, :, :36] = old[2, :, :36]
+        assert torch.equal(t[shift:], want) and not t[:8].any()
+    assert rows.tolist() == [[shift + 5, shift + 2], [shift + 5, shift + 7]] and n.tolist() == [100, 100]
+    assert bqg.last_device_error() == 0
