@@ -206,7 +206,6 @@ def _prepare_share(s, gen):
     for t in new:
         start.append(start[-1] + t)
     s["q_start"], s["tokens"] = _ints(start), start[-1]
-    s["most"] = max(start[(g + 1) * per] - start[g * per] for g in range(G))      # new tokens behind one prefix
     # as forks leave them: a prefix's full pages are shared, its last, partly filled one has a copy in each sequence
     most = max((prefix[i // per] + own_ctx[i] + new[i] + P - 1) // P for i in range(n))
     total = sum(p // P for p in prefix) + sum(
@@ -359,11 +358,10 @@ def _own(s):
         s["handle"] = bqg.KVCache(getattr(bqg, _FMT[c["fmt"]]), t["k"], t["v"], t["ks"], t["vs"])
         if c["op"] == "share":
             s["ws"] = bqg.shared_prefix_attention_workspace(s["handle"], c["heads"], c["groups"] * c["per"], c["tree"],
-                                                            s["tokens"], c["groups"], max_shared=s["most"])
+                                                            s["tokens"], c["groups"])
     if c["op"] == "share":
         return bqg.shared_prefix_attention(s["q"], s["handle"], s["pages"], s["ctx"], s["q_start"], c["tree"],
-                                           s["prefix_len"], s["seq_start"], max_shared=s["most"], mask=s["mask"],
-                                           scale=s["scale"], ws=s["ws"])
+                                           s["prefix_len"], s["seq_start"], mask=s["mask"], scale=s["scale"], ws=s["ws"])
     if c["op"] == "compact":
         ctx = bqg.kv_compact(s["handle"], s["pages"], s["ctx"], s["path"], s["n_path"])
         k, v = bqg.kv_read(s["handle"], s["kept"])
