@@ -227,7 +227,8 @@ struct SharedParams : AttnParams {
     float *rows, *rows_ml;                   // unnormalised (see shared_at), (maximum, sum) pairs
 };
 // Prefix g: its sequences, their query tokens and the shared tokens (none where the arguments do not fit, which
-// `bad` then tells: both passes come to the same answer).
+// `bad` then tells: both passes come to the same answer).  A prefix that fills its row of the table does not fit where there are
+// new tokens: a sequence with some has a token of its own (its last), so that its set is worked on and its rows are written.
 struct SharedGroup { int s0, s1, q0, T, len; };
 __device__ __forceinline__ int64_t attn_cap(const AttnParams &p) { return min((int64_t)0x7fff0000, p.max_pages << p.cache.lp); }
 __device__ __forceinline__ SharedGroup shared_group(const SharedParams &p, int g, int &bad)
@@ -239,10 +240,10 @@ __device__ __forceinline__ SharedGroup shared_group(const SharedParams &p, int g
     const int64_t q0 = min(max((int64_t)p.q_start[r.s0], (int64_t)0), p.n_tokens);
     const int64_t q1 = min(max((int64_t)p.q_start[r.s1], q0), p.n_tokens);
     const int64_t n = p.prefix_len[g];
+    const bool fits = n >= 0 && n < attn_cap(p) + (q1 == q0) && q1 - q0 <= p.max_shared;
     r.q0 = (int)q0; r.T = (int)(q1 - q0);
-    r.len = (int)min(max(n, (int64_t)0), attn_cap(p));
-    if (r.s0 != a || r.s1 != e || r.len != n || q1 - q0 > p.max_shared) bad |= BQG_DEVERR_LENGTH;
-    if (q1 - q0 > p.max_shared || r.s0 == r.s1) r.len = 0;
+    r.len = fits && r.s0 < r.s1 ? (int)n : 0;
+    if (r.s0 != a || r.s1 != e || !fits) bad |= BQG_DEVERR_LENGTH;
     return r;
 }
 __device__ __forceinline__ SharedSeq attn_seq(const SharedParams &p, int b, int &bad)

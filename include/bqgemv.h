@@ -401,8 +401,8 @@ size_t bqg_tree_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int
  * (a prefix need not end with a page: the page where it ends is then read in part from both, and a place of it that is
  * not needed is not read).  prefix_len: n_prefix int32; seq_start: n_prefix + 1 int32, ascending from 0, the last one
  * n_seq; NULL: one prefix, which all sequences share.  max_shared: query tokens behind one
- * prefix at most (it picks the kernels; n_tokens is always enough); a prefix with more counts as not shared, and
- * BQG_DEVERR_LENGTH is set.  n_prefix >= 1; max_shared * n_q / n_kv at most 2^30.
+ * prefix at most (it picks the kernels; n_tokens is always enough); a prefix with more counts as not shared, as does one whose prefix_len
+ * is below 0 or leaves a row of the table no place for a new token, and BQG_DEVERR_LENGTH is set.  n_prefix >= 1; max_shared * n_q / n_kv at most 2^30.
  * Roundings as bqg_tree_attention's, keys as codes for the shared tokens where max_shared * n_q / n_kv is at most 16, for
  * the own ones where max_q * n_q / n_kv is; what the two parts come to is put together in fp32.
  * ws: bqg_shared_prefix_attention_workspace_size(...) bytes, 16-byte aligned, ZERO before the first call on it; one made
