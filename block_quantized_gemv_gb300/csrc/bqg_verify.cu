@@ -15,8 +15,8 @@
 //    often is decided in one place.
 //  * An answer is a whole number and depends on where a sum of up to 2^18 terms crosses a border, so fp32 sums (off by 1e-7:
 //    another token once in some hundred draws) would not do, and fp64's rate is 1/64 of fp32's here: p - c q is
-//    formed as an fp32 pair with the products' and the difference's errors, and added with error-free sums, two
-//    at a time: about 2^-45 of the sum.  The walk's few numbers are pairs too: with fp64 a draft cost 900 cycles, with pairs 200.
+//    formed as an fp32 pair, off by 2^-47 of what c takes off beyond the first rejection (rest2), and added with error-free sums, two
+//    at a time: about 2^-45 of the sum, or of the largest one behind that token, the first rejection's.  The walk's few numbers are pairs too: with fp64 a draft cost 900 cycles, with pairs 200.
 //  * The crossing is looked for in the warps' sums, then by the warp that holds it in the sums that it kept (of 32 lanes and up
 //    to 16 steps), then in the 16 bytes of one lane: nothing of the row is read again but those.  There the sums are
 //    whole numbers of 2^-61 of all.  (Reading the warp's part again took 7 us of 18, most of it for fetching instructions that run once.)
@@ -47,6 +47,13 @@ struct Pair {
         hi = __fadd_rn(a, b);
         lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(b, __fsub_rn(hi, a)), l));
     }
+    // the same sum, hi the nearest fp32 number to it (|hi| >= |lo|)
+    __device__ __forceinline__ void tidy()
+    {
+        const float s = __fadd_rn(hi, lo);
+        lo = __fsub_rn(lo, __fsub_rn(s, hi));
+        hi = s;
+    }
 };
 // hi + lo of a pair, hi the nearest fp32 number (|hi| >= |lo| or near it).
 __device__ __forceinline__ Pair tidy(float hi, float lo)
@@ -55,6 +62,20 @@ __device__ __forceinline__ Pair tidy(float hi, float lo)
     two_sum(hi, lo, r.hi, r.lo);
     return r;
 }
+// An unevaluated sum of three, for what large numbers that are all but equal are taken off from each other with: a pair would know
+// the small rest of them to 2^-48 of the large ones.
+struct Triple {
+    float hi = 0.f, mid = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x)
+    {
+        float h, m, e;
+        two_sum(hi, x, h, e);
+        two_sum(mid, e, m, e);
+        lo = __fadd_rn(lo, e);
+        two_sum(h, m, hi, m);
+        two_sum(m, lo, mid, lo);
+    }
+};
 // Parts of a row's sum as whole numbers: units of about 2^-61 of it, so that what follows is exact and quick (fp64 takes
 // 16 cycles per warp and operation here, and its latency).
 struct Units {
@@ -78,6 +99,7 @@ __device__ __forceinline__ float lower(F2 x) { return __uint_as_float((uint32_t)
 __device__ __forceinline__ float upper(F2 x) { return __uint_as_float((uint32_t)(x.v >> 32)); }
 __device__ __forceinline__ F2 add2(F2 a, F2 b) { F2 r; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { F2 r; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v)); return r; }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { F2 r; asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v)); return r; }
 __device__ __forceinline__ F2 sub2(F2 a, F2 b) { return fma2(b, f2(-1.f, -1.f), a); }      // (one rounding: b times -1 is exact)
 // Two pairs at once.
 struct Pair2 {
@@ -100,7 +122,8 @@ struct Pair2 {
 struct Order {
     int sum;                           // 0: the end; the token is looked for with what follows as it was
     int row;                           // of target and draft
-    float c_hi, c_lo;                  // what q is taken off with
+    int minus;                         // 1: r is max(p - (1 + s) q, 0); 0: p (and s is 0)
+    Pair s;
     int at;                            // the end: which of all warps looks for the token (-1: none does)
     float whole;                       // ... with Units(whole)
     long long goal;
@@ -151,37 +174,31 @@ template <bool F32> struct Row {
     }
 };
 
-// max(p - c q, 0) as a pair; ONE: c is 1, as it is after a first rejection.
-template <bool ONE> __device__ __forceinline__ void rest(float p, float q, float ch, float cl, float &hi, float &lo)
+// max(p - c q, 0) of two tokens, as pairs, with c = 1 + s; ONE: s is 0, as it is after a first rejection.
+// p and c q may be all but equal over a whole row (a draft near its target), and what is left of them decides.  So it is
+// formed as (p - q) - s q, the first difference exact, the product's error along with it, the sign taken from all of it: off by
+// 2^-47 of s q and of itself, where a rounded c q or c would be off by as much of c q.
+template <bool ONE> __device__ __forceinline__ void rest2(float p0, float p1, float q0, float q1, const Pair &s, F2 &hi, F2 &lo)
 {
-    if constexpr (ONE) {
-        const float a = fmaxf(p, q);                       // a - q and its error, exact as a >= q
-        hi = __fsub_rn(a, q);
-        lo = __fsub_rn(__fsub_rn(a, hi), q);
-    } else {
-        const float m = __fmul_rn(q, ch);
-        const float me = __fadd_rn(fmaf(q, ch, -m), __fmul_rn(q, cl));
-        const float a = fmaxf(p, m);
-        hi = __fsub_rn(a, m);
-        lo = __fsub_rn(__fsub_rn(__fsub_rn(a, hi), m), me);
-        lo = p >= m ? fmaxf(lo, -hi) : 0.f;
+    const F2 a = f2(fmaxf(p0, q0), fmaxf(p1, q1)), q = f2(q0, q1);
+    hi = sub2(a, q);                                               // a - q and its error, exact as a >= q
+    lo = sub2(sub2(a, hi), q);
+    if constexpr (!ONE) {
+        const F2 m = mul2(q, f2(s.hi, s.hi));
+        const F2 e = fma2(q, f2(-s.lo, -s.lo), fma2(q, f2(-s.hi, -s.hi), m));      // m - s q
+        const F2 h = sub2(hi, m);                                  // as above where something is left
+        lo = add2(sub2(sub2(hi, h), m), add2(lo, e));
+        const F2 all = add2(h, lo);
+        hi = f2(lower(all) > 0.f ? lower(h) : 0.f, upper(all) > 0.f ? upper(h) : 0.f);
+        lo = f2(lower(all) > 0.f ? lower(lo) : 0.f, upper(all) > 0.f ? upper(lo) : 0.f);
     }
 }
-
-// Two at once.
-template <bool ONE> __device__ __forceinline__ void rest2(float p0, float p1, float q0, float q1, float ch, float cl, F2 &hi, F2 &lo)
+// Of one.
+__device__ __forceinline__ Pair rest(float p, float q, const Pair &s)
 {
-    if constexpr (ONE) {
-        const F2 a = f2(fmaxf(p0, q0), fmaxf(p1, q1)), q = f2(q0, q1);
-        hi = sub2(a, q);
-        lo = sub2(sub2(a, hi), q);
-    } else {
-        float h[2], l[2];
-        rest<false>(p0, q0, ch, cl, h[0], l[0]);
-        rest<false>(p1, q1, ch, cl, h[1], l[1]);
-        hi = f2(h[0], h[1]);
-        lo = f2(l[0], l[1]);
-    }
+    F2 hi, lo;
+    rest2<false>(p, p, q, q, s, hi, lo);
+    return Pair{lower(hi), lower(lo)};
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -221,7 +238,7 @@ template <bool F32, bool DRAFT, int kWarps> struct Verify {
 #pragma unroll
         for (int i = 0; i < E; i += 2) {
             F2 hi = f2(p[i], p[i + 1]), lo = f2(0.f, 0.f);
-            if constexpr (DRAFT) rest2<FIRST>(p[i], p[i + 1], q[i], q[i + 1], o.c_hi, o.c_lo, hi, lo);
+            if constexpr (DRAFT) rest2<FIRST>(p[i], p[i + 1], q[i], q[i + 1], o.s, hi, lo);
             if (i == 0) { s.hi = hi; s.lo = lo; }
             else s.add(hi, lo);
         }
@@ -234,7 +251,7 @@ template <bool F32, bool DRAFT, int kWarps> struct Verify {
     {
         const Row<F32> target(p.target, (int64_t)o.row * p.target_stride, p.vocab), draft(p.draft, (int64_t)o.row * p.draft_stride, p.vocab);
         const unsigned long long gone = gone_in(o, a, e, lane);
-        const bool q = DRAFT && (FIRST || o.c_hi > 0.f);
+        const bool q = DRAFT && o.minus;
         Pair2 all{f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll 1
         for (int k0 = 0; a + k0 * kStep < e; k0 += U) {
@@ -316,7 +333,7 @@ template <bool F32, bool DRAFT, int kWarps> struct Verify {
         const int part = cross(lane % L ? 0 : units.of(s), goal, lane) / L;
         a += part * steps * kStep;
         const Row<F32> target(p.target, (int64_t)o.row * p.target_stride, p.vocab), draft(p.draft, (int64_t)o.row * p.draft_stride, p.vocab);
-        const bool q = DRAFT && o.c_hi > 0.f;
+        const bool q = DRAFT && o.minus;
         long long v;
         if (steps == 1) {
             const float2 f = kept[part][lane];
@@ -326,11 +343,11 @@ template <bool F32, bool DRAFT, int kWarps> struct Verify {
         }
         // the lane, then its token
         const int l = cross(v, goal, lane), x = a + E * l + lane;
-        Pair r;
+        Pair r{0.f, 0.f};
         if (lane < E && x >= 0 && x < e) {
             r.hi = load_prob<F32>(target.at, x);
             if constexpr (DRAFT)
-                if (q) rest<false>(r.hi, load_prob<F32>(draft.at, x), o.c_hi, o.c_lo, r.hi, r.lo);
+                if (q) r = rest(r.hi, load_prob<F32>(draft.at, x), o.s);
             if (!DRAFT)
                 for (int i = 0; i < o.n_gone; i++)
                     if (o.gone[i] == x) r.hi = 0.f;
@@ -350,7 +367,7 @@ template <bool F32, bool DRAFT, int kWarps> struct Verify {
             uint4 pw = make_uint4(0, 0, 0, 0), qw = pw;
             if (x < e) {
                 pw = target.load(x, true);
-                if (DRAFT && o.c_hi > 0.f) qw = draft.load(x, draft.off == target.off);
+                if (DRAFT && o.minus) qw = draft.load(x, draft.off == target.off);
             }
             const long long v = units.of(some<false>(o, pw, qw, x, gone).both()), all = over_lanes(v);
             if (all > goal || last == a) return v;
@@ -424,7 +441,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kerne
         }
         int a, e;
         range(order.row, rank * kWarps + warp, a, e);
-        const Pair s = order.c_hi == 1.f && order.c_lo == 0.f ? V::template sum<true>(p, order, a, e, steps, kept[warp], lane)
+        const Pair s = order.s.hi == 0.f && order.s.lo == 0.f ? V::template sum<true>(p, order, a, e, steps, kept[warp], lane)
                                                               : V::template sum<false>(p, order, a, e, steps, kept[warp], lane);
         if (lane == 0) warp_sum[warp] = s;
         meet();
@@ -468,12 +485,12 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kerne
     if (bad) atomicOr(p.error, bad);
     __syncwarp();
     if (ctas > 1) cluster_wait();
-    const Pair zero, one{1.f, 0.f};
+    const Pair one{1.f, 0.f};
     // A round: the warps' sums, in their order, each lane the next few.
     constexpr int NE = kMaxCtas * kWarps / 32;
     const int each = max(ctas * kWarps / 32, 1);
     Pair parts[NE];
-    auto give = [&](int sum, int64_t row, const Pair &c, int n_gone, int at = -1, float whole = 1.f, long long goal = 0) {
+    auto give = [&](int sum, int64_t row, const Pair &s, int minus, int n_gone, int at = -1, float whole = 1.f, long long goal = 0) {
         __syncwarp();
         if (lane < ctas) {                                // to one CTA per lane
             Order *o = ctas > 1 ? cluster.map_shared_rank(&order, lane) : &order;
@@ -483,15 +500,15 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kerne
             o->goal = goal;
             if (sum) {
                 o->row = (int)row;
-                o->c_hi = c.hi;
-                o->c_lo = c.lo;
+                o->s = s;
+                o->minus = minus;
                 o->n_gone = n_gone;
                 if (lane)
                     for (int i = 0; i < n_gone; i++) o->gone[i] = order.gone[i];
             }
         }
         __syncwarp();
-        if (!round()) return zero;
+        if (!round()) return Pair();
 #pragma unroll
         for (int i = 0; i < NE; i++) {
             const int w = lane * each + i;
@@ -511,7 +528,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kerne
     long long goal = 0;
     if (T > 0) {
         int last = 0, n_gone = 0;                         // the last draft looked at
-        Pair Z = one, c;
+        Pair Z = one, s;                                  // c = minus + s
+        int minus = 0;
+        Triple left{1.f, 0.f, 0.f};                       // chosen drafts: Z
         bool known = false;                               // `parts` and what the CTAs hold are those of r
         for (;;) {
             unsigned long long below = (unsigned long long)__ballot_sync(0xffffffffu, up[0] == node) |
@@ -523,7 +542,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kerne
             Draft d = drafts[i];
             Pair r{d.p, 0.f};
             if constexpr (DRAFT) {
-                rest<false>(d.p, d.q, c.hi, c.lo, r.hi, r.lo);
+                r = rest(d.p, minus ? d.q : 0.f, s);
             } else {
                 const bool again = (lane < n_gone && order.gone[lane] == d.token) || (lane + 32 < n_gone && order.gone[lane + 32] == d.token);
                 if (__any_sync(0xffffffffu, again)) r.hi = 0.f;
@@ -533,19 +552,22 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kerne
                 if (lane == (count & 31)) place[count >> 5] = i;
                 count++;
                 Z = one;
-                c = zero;
+                minus = 0;
+                s = Pair();
+                left = Triple{1.f, 0.f, 0.f};
                 n_gone = 0;
                 known = false;
             } else if constexpr (DRAFT) {
-                float h, l;
-                two_sum(c.hi, Z.hi, h, l);
-                c = tidy(h, __fadd_rn(l, __fadd_rn(c.lo, Z.lo)));
-                Z = give(1, q0 + node, c, 0);
+                if (minus) {
+                    s.add(Z.hi, Z.lo);
+                    s.tidy();
+                }
+                minus = 1;
+                Z = give(1, q0 + node, s, minus, 0);
                 known = true;
             } else {
-                float h, l;
-                two_sum(Z.hi, -r.hi, h, l);
-                Z = tidy(h, __fadd_rn(l, Z.lo));
+                left.add(-r.hi);
+                Z = Pair{left.hi, left.mid};
                 __syncwarp();
                 if (lane == 0) order.gone[n_gone] = d.token;
                 n_gone++;
@@ -553,10 +575,10 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kerne
             }
         }
         if (!known) {
-            Z = give(1, q0 + node, zero, n_gone);
+            Z = give(1, q0 + node, Pair(), 0, n_gone);
         }
         if (!(Z.hi > 0.f) && (known || n_gone)) {         // nothing left: the target's own
-            Z = give(1, q0 + node, zero, 0);
+            Z = give(1, q0 + node, Pair(), 0, 0);
         }
         if (Z.hi > 0.f) {
             // u Z: what the running sum has to exceed, in whole units
@@ -595,7 +617,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 8 ? 4 : 2) verify_kerne
 #pragma unroll
     for (int j = 0; j < 2; j++)
         if (lane + 32 * j < p.max_q) p.path[(int64_t)b * p.max_q + lane + 32 * j] = place[j];
-    give(0, 0, zero, 0, finder, whole, goal);
+    give(0, 0, Pair(), 0, 0, finder, whole, goal);
 }
 
 template <bool F32, bool DRAFT, int kWarps> cudaError_t run_warps(const VerifyParams &p, int ctas, cudaStream_t s, bool pdl)
