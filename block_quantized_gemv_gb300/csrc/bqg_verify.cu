@@ -47,7 +47,8 @@ struct Pair {
         hi = __fadd_rn(a, b);
         lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(b, __fsub_rn(hi, a)), l));
     }
-    // the same sum, hi the nearest fp32 number to it (|hi| >= |lo|)
+    // the same sum, hi the nearest fp32 number to it (|hi| >= |lo|): what is added to lo afterwards is rounded to 2^-48 of hi, where
+    // the errors of n additions that lo had gathered would make that n 2^-48
     __device__ __forceinline__ void tidy()
     {
         const float s = __fadd_rn(hi, lo);
@@ -110,6 +111,12 @@ struct Pair2 {
         const F2 e = add2(sub2(hi, sub2(s, b)), sub2(h, b));       // Knuth's: no comparison, which would not be packed
         hi = s;
         lo = add2(lo, add2(e, l));
+    }
+    __device__ __forceinline__ void tidy()
+    {
+        const F2 s = add2(hi, lo);
+        lo = sub2(lo, sub2(s, hi));
+        hi = s;
     }
     __device__ __forceinline__ Pair both() const
     {
@@ -245,14 +252,16 @@ template <bool F32, bool DRAFT, int kWarps> struct Verify {
         return s;
     }
     // The sum of r over a warp's tokens, from a on and before e, in lane 0.  kept[k][lane]: the sums of the lane's tokens in the k-th
-    // `steps` steps of it.
+    // `steps` steps of it, its part k.
     template <bool FIRST>
     static __device__ __forceinline__ Pair sum(const VerifyParams &p, const Order &o, int a, int e, int steps, float2 (*kept)[32], int lane)
     {
         const Row<F32> target(p.target, (int64_t)o.row * p.target_stride, p.vocab), draft(p.draft, (int64_t)o.row * p.draft_stride, p.vocab);
         const unsigned long long gone = gone_in(o, a, e, lane);
         const bool q = DRAFT && o.minus;
-        Pair2 all{f2(0.f, 0.f), f2(0.f, 0.f)};
+        Pair all;
+        Pair2 part{f2(0.f, 0.f), f2(0.f, 0.f)};
+        int left = steps;                                              // of the part
 #pragma unroll 1
         for (int k0 = 0; a + k0 * kStep < e; k0 += U) {
             uint4 pw[U], qw[U];
@@ -267,24 +276,25 @@ template <bool F32, bool DRAFT, int kWarps> struct Verify {
             }
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                const int k = k0 + u, x = a + k * kStep;
+                const int x = a + (k0 + u) * kStep;
                 if (x >= e) break;
                 const Pair2 s = some<FIRST>(o, pw[u], qw[u], x + E * lane, gone);
-                all.add(s.hi, s.lo);
-                Pair one = s.both();
-                if (steps == 1) {
-                    kept[k][lane] = make_float2(one.hi, one.lo);
+                if (left == steps) {
+                    part = s;
                 } else {
-                    const int at = k / steps;
-                    if (at * steps != k) {
-                        const float2 f = kept[at][lane];
-                        one.add(f.x, f.y);
-                    }
-                    kept[at][lane] = make_float2(one.hi, one.lo);
+                    part.add(s.hi, s.lo);
+                    part.tidy();
+                }
+                if (--left == 0 || x + kStep >= e) {
+                    const Pair one = part.both();
+                    (*kept++)[lane] = make_float2(one.hi, one.lo);
+                    all.add(one.hi, one.lo);
+                    all.tidy();
+                    left = steps;
                 }
             }
         }
-        return over_lanes(all.both());
+        return over_lanes(all);
     }
     static __device__ __forceinline__ Pair over_lanes(Pair v)
     {

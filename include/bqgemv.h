@@ -433,8 +433,8 @@ size_t bqg_shared_prefix_attention_workspace_size(const bqg_kv_cache *cache, int
  * distributed as the target's.
  * n_accepted: n_seq int32, the accepted tokens with token 0 (0: a sequence without tokens); path: n_seq rows of max_q int32,
  * their places, ascending from 0, then -1; next_token: n_seq int32 (-1: no token, or a row without a probability).
- * Sums are kept to about 2^-45 of themselves, after several rejections behind a token of what the first one left: answers are
- * those of the formulas but where u is that near to a border.
+ * Sums are kept to about 2^-45 of themselves (2^-42 at 2^30 tokens), after several rejections behind a token of what the first
+ * one left: answers are those of the formulas but where u is that near to a border.
  * Token rows and numbers in device memory; pointers aligned to their values; 1 <= max_q <= 64; vocab at most 2^30.
  * One launch. */
 int bqg_tree_verify(const void *target, const void *draft, int x_dtype, int64_t target_stride, int64_t draft_stride,

@@ -163,3 +163,34 @@ def test_acceptance_of_a_chosen_draft_after_rejections(side):
     p[200] = np.float32(float(left / 2))
     want = call(p, None, tokens, u)
     assert want[0] == [2 if side > 0 else 1]
+
+
+@pytest.mark.parametrize("V", [131075, 1 << 22, 1 << 24])
+@pytest.mark.parametrize("side", [-1, 1])
+def test_next_token_of_a_long_row_beside_a_large_probability(V, side):
+    """A lane adds its part of the row to one large number.  At 2^24 tokens that is 128 additions one after the other, each off by
+    2^-48 of it at most: 2^-45 in random directions, and the border is put 2^-42 away."""
+    near = NEAR * 2 if V == 1 << 24 else NEAR
+    rng = np.random.default_rng(V % 1000)
+    tail = rng.random(V) * 0.1 / V * 2
+    p = tail.astype(np.float32)
+    p[0] = np.float32(0.9123456)
+    p[-3:] = 0
+    unit = 60
+    whole = np.round(p.astype(np.float64) * 2.0 ** unit).astype(np.int64)     # exact where a value is a multiple of 2^-60
+    p = (whole.astype(np.float64) * 2.0 ** -unit).astype(np.float32)
+    whole = (p.astype(np.float64) * 2.0 ** unit).astype(np.int64)
+    assert (whole.astype(np.float64) * 2.0 ** -unit == p).all()
+    total, run = sum(int(x) for x in np.add.reduceat(whole, np.arange(0, V, 4096))), np.cumsum(whole)
+    u = float(np.float32(0.96))
+    x = int(np.searchsorted(run, int(Fraction(u) * total), side="right"))
+    over = int(run[x]) - Fraction(u) * total
+    # over - u tau = +- near of the whole
+    tau = (over - side * near * total) / Fraction(u) / 2 ** unit
+    assert tau > 0
+    p[-3:] = pieces(tau)
+    t = sum(Fraction(float(v)) for v in p[-3:])
+    exact = (Fraction(int(run[x]), 2 ** unit) - Fraction(u) * (Fraction(total, 2 ** unit) + t)) / Fraction(total, 2 ** unit)
+    assert abs(exact / (side * near) - 1) < 0.1
+    nxt = x if side > 0 else x + 1 + int(np.argmax(p[x + 1:] > 0))
+    call(p, None, [0], [u], want=([1], [[0]], [nxt]))
