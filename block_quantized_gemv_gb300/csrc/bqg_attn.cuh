@@ -71,6 +71,8 @@ struct SharedSeq : AttnSeq {
 // Tokens that a set leaves out; its row of the block table.
 __device__ __forceinline__ int attn_lo(const AttnSeq &) { return 0; }
 __device__ __forceinline__ int attn_lo(const SharedSeq &s) { return s.lo; }
+__device__ __forceinline__ bool attn_left_out(const AttnSeq &, int) { return false; }
+__device__ __forceinline__ bool attn_left_out(const SharedSeq &s, int tok) { return tok < s.lo; }
 __device__ __forceinline__ int attn_table_row(const AttnSeq &s) { return s.b; }
 __device__ __forceinline__ int attn_table_row(const SharedSeq &s) { return s.row; }
 
@@ -135,6 +137,7 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4])
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) { uint32_t v; asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory"); return v; }
 __device__ __forceinline__ uint2 lds64(uint32_t a) { uint2 v; asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory"); return v; }
 __device__ __forceinline__ uint4 lds128(uint32_t a)
@@ -561,7 +564,8 @@ template <int FMT, int D, int RT> struct AttnKernel {
     }
 
     // Copies of strip tokens tok0 .. tok0 + 15 of (sequence, head) into `st`; ok: the page is in the cache.
-    static __device__ __forceinline__ void issue(const AttnParams &p, const AttnSeq &s, int h, int tok0, int page, bool ok,
+    template <typename Seq>
+    static __device__ __forceinline__ void issue(const AttnParams &p, const Seq &s, int h, int tok0, int page, bool ok,
                                                  uint32_t st, int lane)
     {
         const int at = tok0 & ((1 << p.cache.lp) - 1);
@@ -572,7 +576,7 @@ template <int FMT, int D, int RT> struct AttnKernel {
         const uint8_t *sc = nullptr;
         if constexpr (!BF)
             sc = reinterpret_cast<const uint8_t *>((lane < CH ? p.cache.k_scale : p.cache.v_scale) + row * G::NB) + lane % CH * 16;
-        if (n >= kStrip) {
+        if (n >= kStrip && !attn_left_out(s, tok0)) {
 #pragma unroll
             for (int i = 0; i < G::CPT / 2; i++) {
                 const uint32_t d = st + chunk_at<G::CPT>((i * 32 + lane) / G::CPT, lane % G::CPT);
@@ -581,12 +585,12 @@ template <int FMT, int D, int RT> struct AttnKernel {
             }
             if constexpr (!BF)
                 if (lane < 2 * CH) cp_async16(st + 2 * kStrip * G::RB + lane * 16, sc, 16);
-        } else {                                                                 // zeros behind the end
+        } else {                                                                 // zeros behind the end, and for tokens left out
 #pragma unroll
             for (int i = 0; i < G::CPT / 2; i++) {
                 const int tok = (i * 32 + lane) / G::CPT;
                 const uint32_t d = st + chunk_at<G::CPT>(tok, lane % G::CPT);
-                const int bytes = tok < n ? 16 : 0;
+                const int bytes = tok < n && !attn_left_out(s, tok0 + tok) ? 16 : 0;
                 cp_async16(d, bytes ? k + i * 512 : p.cache.k, bytes);
                 cp_async16(d + kStrip * G::RB, bytes ? v + i * 512 : p.cache.v, bytes);
             }
@@ -784,6 +788,16 @@ template <int FMT, int D, int RT> struct AttnKernel {
             }
         }
         return __any_sync(0xffffffffu, bad);
+    }
+    // The staged strip's first n tokens are left out, and their codes zeros (issue): zeros for their values' scales, of which 16 bytes
+    // belong to several tokens and come together.
+    static __device__ __forceinline__ void leave_out(uint32_t st, int n, int lane)
+    {
+        if constexpr (!BF) {
+#pragma unroll 1
+            for (int i = lane; i < n * (G::NB / 2); i += 32) sts32(st + 2 * kStrip * G::RB + G::SCALES + 4 * i, 0);
+            __syncwarp();
+        }
     }
 
     // What a warp has of its rows (this lane: 8 m + 2 t and the next): outputs and their maximum and sum so far.

@@ -165,7 +165,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps) own_kernel(const SharedParams
             const uint32_t st = ring + stage * G::STAGE;
             const bool ok = (valid >> stage) & 1;
             stage = stage + 1 == S ? 0 : stage + 1;
-            A::strip(st, lane, qf, smem_u32(row_bias) + t * 8, row_sees, s, (strip0 + j) * kStrip, ok, pw, r);
+            const int tok0 = (strip0 + j) * kStrip;
+            // the prefix's places in this sequence's page: whatever they hold, a NaN too, the result's bits are the same
+            if (tok0 < s.lo) A::leave_out(st, s.lo - tok0, lane);
+            A::strip(st, lane, qf, smem_u32(row_bias) + t * 8, row_sees, s, tok0, ok, pw, r);
         }
         cp_async_wait<0>();
         __syncwarp();                                                         // the ring's memory is free

@@ -398,8 +398,8 @@ size_t bqg_tree_attention_workspace_size(const bqg_kv_cache *cache, int n_q, int
  * tokens' keys and values are read and multiplied once for all sequences behind them, not once for each.
  * Sequences seq_start[g] .. seq_start[g + 1] - 1 begin with the same prefix_len[g] tokens: 0 <= prefix_len[g] <= the
  * ctx_len of each.  These are taken from the pages of the first of them; tokens from there on come from each one's own
- * (a prefix need not end with a page: the page where it ends is then read in part from both, and a place of it that is
- * not needed is not read).  prefix_len: n_prefix int32; seq_start: n_prefix + 1 int32, ascending from 0, the last one
+ * (a prefix need not end with a page: each sequence's own page where it ends holds the tokens behind it, and what that
+ * page has in the prefix's places may be read but changes nothing).  prefix_len: n_prefix int32; seq_start: n_prefix + 1 int32, ascending from 0, the last one
  * n_seq; NULL: one prefix, which all sequences share.  max_shared: query tokens behind one
  * prefix at most (it picks the kernels; n_tokens is always enough); a prefix with more counts as not shared, as does one whose prefix_len
  * is below 0 or leaves a row of the table no place for a new token, and BQG_DEVERR_LENGTH is set.  n_prefix >= 1; max_shared * n_q / n_kv at most 2^30.

@@ -1,4 +1,4 @@
-"""Attention behind shared prefixes where lengths do not fit."""
+"""Attention behind shared prefixes where lengths do not fit, and where a page's unneeded places hold no numbers."""
 import pytest
 import torch
 
@@ -48,3 +48,14 @@ def test_a_prefix_that_fills_the_table_of_sequences_without_new_tokens(fmt, T):
     c = Shared(fmt, 128, 2, 2, [32, 7], [2, 1], [0, 0, 2], [0, 0, T], page=16, seed=6, spoil=False)
     c.prefix[0] = c.ctx[0] = c.ctx[1] = c.table.shape[1] * 16
     c.check()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,group", [(1, 1), (2, 4), (9, 4), (20, 5)])
+def test_places_of_the_prefix_in_other_pages_change_nothing(fmt, D, T, group):
+    """What a sequence's own page holds in the shared tokens' places, numbers or none, does not show in a single bit."""
+    make = lambda spoil: Shared(fmt, D, 2, group, [45, 70], [3, 2], [10, 300, 0, 3, 40], [T, 1, T, 1, T], page=32, seed=7, spoil=spoil)
+    a, b = make(False), make(True)
+    assert torch.equal(a.run().view(torch.int16), b.run().view(torch.int16))
+    b.check()
