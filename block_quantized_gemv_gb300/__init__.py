@@ -850,7 +850,7 @@ def _table(t, cur):
 def kv_compact(cache: KVCache, block_table, ctx_len, path, n_path, out=None, stream=None) -> torch.Tensor:
     """The accepted path's keys and values moved behind the context: new token path[b, k] of sequence b goes to place
     ctx_len[b] + k, for k < n_path[b] (path int32 [n_seq, max_q], ascending; as tree_verify gives them).  Returns the new
-    lengths ctx_len + n_path, int32 [n_seq] (`out` must be none of the arguments)."""
+    lengths ctx_len + n_path, int32 [n_seq] (`out` may overlap none of ctx_len, path and n_path)."""
     cur = _current_device()
     bp, (n_seq, max_pages) = _table(block_table, cur)
     if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[0] != n_seq:

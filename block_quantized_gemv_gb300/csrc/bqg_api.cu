@@ -1365,13 +1365,16 @@ int bqg_kv_compact(const bqg_kv_cache *cache, const int32_t *block_table, int64_
     if (!aligned(block_table, 4) || !aligned(ctx_len, 4) || !aligned(path, 4) || !aligned(n_path, 4) || !aligned(new_ctx, 4))
         return BQG_ERR_MISALIGNED;
     // several CTAs read a sequence's length and path, one writes the new length
-    auto over = [&](const int32_t *x, int64_t n) { return new_ctx < x + n && x < new_ctx + n_seq; };
+    auto over = [&](const int32_t *x, int64_t n) {
+        return (uintptr_t)new_ctx < (uintptr_t)x + 4 * (uint64_t)n && (uintptr_t)x < (uintptr_t)new_ctx + 4 * (uint64_t)n_seq;
+    };
     if (n_seq && new_ctx && (over(ctx_len, n_seq) || over(n_path, n_seq) || over(path, (int64_t)n_seq * max_q)))
         return BQG_ERR_INVALID_ARG;
     p.table = block_table; p.max_pages = max_pages;
     p.ctx_len = ctx_len; p.path = path; p.n_path = n_path;
     p.n_seq = n_seq; p.max_q = max_q;
     p.ctx_out = new_ctx;
+    p.ctx_in_table = new_ctx && over(block_table, std::min<int64_t>(n_seq * max_pages, (int64_t)1 << 56));
     DevInfo dev;
     if (int st = current_device(&dev)) return st;
     if (n_seq == 0) return BQG_OK;

@@ -47,6 +47,33 @@ template <int FMT, int D> struct Sides {
     }
 };
 
+// What a sequence keeps of its path, by one warp: places lane and 32 + lane of it, good while they ascend and lie in the sequence's
+// pages; how many are; its length made to fit; BQG_DEVERR_LENGTH.
+struct Path { int a[2], kept, bad; int64_t ctx; };
+__device__ __forceinline__ Path path_of(const CompactParams &p, int b, int lane)
+{
+    Path r;
+    const int64_t cap = min((int64_t)0x7fff0000, p.max_pages << p.cache.lp);
+    const int said = p.n_path[b], n = min(max(said, 0), p.max_q), c = p.ctx_len[b];
+    r.ctx = min(max((int64_t)c, (int64_t)0), cap);
+    const int32_t *path = p.path + (int64_t)b * p.max_q;
+    bool good[2];
+#pragma unroll
+    for (int j = 0; j < 2; j++) r.a[j] = lane + 32 * j < n ? path[lane + 32 * j] : -1;
+    const int low_last = __shfl_sync(0xffffffffu, r.a[0], 31);
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+        int before = __shfl_up_sync(0xffffffffu, r.a[j], 1);
+        if (lane == 0) before = j ? low_last : -1;
+        good[j] = lane + 32 * j < n && r.a[j] > before && r.ctx + r.a[j] < cap;
+    }
+    const unsigned long long ok = (unsigned long long)__ballot_sync(0xffffffffu, good[0]) |
+                                  (unsigned long long)__ballot_sync(0xffffffffu, good[1]) << 32;
+    r.kept = ~ok ? __ffsll(~ok) - 1 : 64;                     // up to the first that is not
+    r.bad = n != said || r.kept != n || r.ctx != c ? BQG_DEVERR_LENGTH : 0;
+    return r;
+}
+
 template <int FMT, int D> __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p)
 {
     using S = Sides<FMT, D>;
@@ -59,33 +86,16 @@ template <int FMT, int D> __global__ void __launch_bounds__(kThreads) compact_ke
     pdl_launch_dependents();
     const int P = 1 << p.cache.lp;
     if (tid < 32) {
-        // places lane and 32 + lane of the path: good while they ascend and lie in the sequence's pages
-        const int64_t cap = min((int64_t)0x7fff0000, p.max_pages << p.cache.lp);
-        const int said = p.n_path[b], n = min(max(said, 0), p.max_q), c = p.ctx_len[b];
-        const int64_t ctx = min(max((int64_t)c, (int64_t)0), cap);
-        const int32_t *path = p.path + (int64_t)b * p.max_q;
-        int a[2];
-        bool good[2];
-#pragma unroll
-        for (int j = 0; j < 2; j++) a[j] = lane + 32 * j < n ? path[lane + 32 * j] : -1;
-        const int low_last = __shfl_sync(0xffffffffu, a[0], 31);
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-            int before = __shfl_up_sync(0xffffffffu, a[j], 1);
-            if (lane == 0) before = j ? low_last : -1;
-            good[j] = lane + 32 * j < n && a[j] > before && ctx + a[j] < cap;
-        }
-        const unsigned long long ok = (unsigned long long)__ballot_sync(0xffffffffu, good[0]) |
-                                      (unsigned long long)__ballot_sync(0xffffffffu, good[1]) << 32;
-        const int kept = ~ok ? __ffsll(~ok) - 1 : 64;         // up to the first that is not
-        int bad = n != said || kept != n || ctx != c ? BQG_DEVERR_LENGTH : 0, moves = 0;
+        const Path path = path_of(p, b, lane);
+        const int64_t ctx = path.ctx;
+        int bad = path.bad, moves = 0;
 #pragma unroll
         for (int j = 0; j < 2; j++) {
             const int k = lane + 32 * j;
             int64_t src = -1, dst = -1;
-            bool move = k < kept && a[j] != k;
+            bool move = k < path.kept && path.a[j] != k;
             if (move) {
-                const int64_t x = ctx + a[j], y = ctx + k;
+                const int64_t x = ctx + path.a[j], y = ctx + k;
                 const int32_t *row = p.table + (int64_t)b * p.max_pages;
                 const int px = row[x >> p.cache.lp], py = row[y >> p.cache.lp];
                 if (px < 0 || px >= p.cache.n_pages || py < 0 || py >= p.cache.n_pages) {
@@ -104,7 +114,7 @@ template <int FMT, int D> __global__ void __launch_bounds__(kThreads) compact_ke
         if (slice == 0 && bad) atomicOr(p.error, bad);
         if (lane == 0) {
             n_moves = moves;
-            if (slice == 0 && p.ctx_out) p.ctx_out[b] = (int)ctx + kept;
+            if (slice == 0 && p.ctx_out) p.ctx_out[b] = (int)ctx + path.kept;
         }
     }
     __syncthreads();
@@ -137,6 +147,17 @@ template <int FMT, int D> __global__ void __launch_bounds__(kThreads) compact_ke
             }
         }
     }
+}
+
+// The new lengths alone, a warp per sequence.
+__global__ void __launch_bounds__(kThreads) lengths_kernel(const CompactParams p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t b = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (b >= p.n_seq) return;
+    const Path path = path_of(p, (int)b, threadIdx.x & 31);
+    if ((threadIdx.x & 31) == 0) p.ctx_out[b] = (int)path.ctx + path.kept;
 }
 
 // `bytes` (a multiple of 4, both sides 16-byte aligned) by one warp.
@@ -232,7 +253,12 @@ cudaError_t launch_compact(CompactParams p, int fmt, int D, int sms, cudaStream_
     // as many CTAs as are resident together, if there are heads for them
     p.slices = (int)std::min<int64_t>(2 * p.cache.n_kv, std::max<int64_t>(1, (int64_t)sms * 6 / p.n_seq));
     auto fn = fmt == BQG_Q8_0 ? compact_fn<BQG_Q8_0>(D) : fmt == BQG_Q4_0 ? compact_fn<BQG_Q4_0>(D) : compact_fn<BQG_BF16>(D);
-    return launch(fn, p, (int64_t)p.n_seq * p.slices, s, pdl);
+    int32_t *const apart = p.ctx_in_table ? p.ctx_out : nullptr;
+    if (apart) p.ctx_out = nullptr;
+    if (cudaError_t e = launch(fn, p, (int64_t)p.n_seq * p.slices, s, pdl)) return e;
+    if (!apart) return cudaSuccess;
+    p.ctx_out = apart;                                        // behind all reads of the table
+    return launch(lengths_kernel, p, ((int64_t)p.n_seq + kWarps - 1) / kWarps, s, pdl);
 }
 
 cudaError_t launch_fork(ForkParams p, int fmt, int D, int sms, cudaStream_t s, bool pdl)

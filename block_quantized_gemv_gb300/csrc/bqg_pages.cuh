@@ -12,6 +12,7 @@ struct CompactParams {
     const int32_t *ctx_len, *path, *n_path;
     int n_seq, max_q;
     int32_t *ctx_out;                    // null: not wanted
+    bool ctx_in_table;                   // some of it lies in the table, which other CTAs read: written by a launch of its own
     int slices;                          // CTAs per sequence
     int *error;                          // device_error_word, set by the launch
 };

@@ -446,9 +446,10 @@ int bqg_tree_verify(const void *target, const void *draft, int x_dtype, int64_t 
  * + path[b][k], as bqg_tree_attention has it) goes to place ctx_len[b] + k, for k < n_path[b], codes and scales as they
  * are.  path: n_seq rows of max_q int32, ascending (as bqg_tree_verify gives it); what stands behind
  * the kept tokens stays as it is.  new_ctx (may be NULL): n_seq int32, ctx_len[b] + n_path[b]; not overlapping ctx_len, path
- * or n_path.
+ * or n_path (refused).
  * A path that stops ascending or leaves the sequence's pages is cut off there (BQG_DEVERR_LENGTH); a move from or to a
- * page outside the cache is left out (BQG_DEVERR_PAGE).  1 <= max_q <= 64.  One launch. */
+ * page outside the cache is left out (BQG_DEVERR_PAGE).  1 <= max_q <= 64.  One launch; two where new_ctx lies in block_table,
+ * which is then written when every sequence has read its pages. */
 int bqg_kv_compact(const bqg_kv_cache *cache, const int32_t *block_table, int64_t max_pages, const int32_t *ctx_len,
                    const int32_t *path, const int32_t *n_path, int n_seq, int max_q, int32_t *new_ctx, cudaStream_t stream);
 
