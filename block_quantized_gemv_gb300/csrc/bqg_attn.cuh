@@ -829,7 +829,7 @@ template <int FMT, int D, int RT> struct AttnKernel {
         const int g = lane >> 2, t = lane & 3;
         float sc[RT][4];
         scores(st, lane, qf, bias, sc);
-        const bool edge = tok0 + kStrip > s.ctx || !ok || tok0 < attn_lo(s);   // new tokens, the end, no page, shared ones
+        const bool edge = tok0 + kStrip > s.ctx || !ok || attn_left_out(s, tok0);   // new tokens, the end, no page, shared ones
         if (edge) {
 #pragma unroll
             for (int m = 0; m < RT; m++)
@@ -839,7 +839,7 @@ template <int FMT, int D, int RT> struct AttnKernel {
 #pragma unroll
                     for (int x = 0; x < 2; x++) {
                         const int tok = tok0 + 8 * x + g;
-                        const bool see = ok && tok >= attn_lo(s) && (tok < s.ctx || (tok < s.len && ((sees >> (tok - s.ctx)) & 1)));
+                        const bool see = ok && !attn_left_out(s, tok) && (tok < s.ctx || (tok < s.len && ((sees >> (tok - s.ctx)) & 1)));
                         if (!see) sc[m][2 * x + r] = NEG;
                     }
                 }

@@ -735,7 +735,7 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
                     tmem_ld32_nowait(ts + 32, v1);
                     tmem_wait_ld(v0);
                     tmem_wait_ld(v1);
-                    if (tok0 + 64 > d.s.ctx || dead || tok0 < attn_lo(d.s)) {   // tokens that this row does not see
+                    if (tok0 + 64 > d.s.ctx || dead || attn_left_out(d.s, tok0)) {   // tokens that this row does not see
 #pragma unroll
                         for (int c = 0; c < 2; c++) {
                             const int t0 = tok0 + 32 * c, before = d.s.ctx - t0, all = d.s.len - t0;
@@ -1003,7 +1003,7 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
                 const int32_t *table = p.table + (int64_t)attn_table_row(w.s) * p.max_pages;
                 auto page_of = [&](int t) {
                     const int tok = t * G::TT + lane * box;
-                    return (lane < boxes && tok < w.s.len && tok + box > attn_lo(w.s)) ? table[tok >> p.cache.lp] : -2;
+                    return (lane < boxes && tok < w.s.len && !attn_left_out(w.s, tok + box - 1)) ? table[tok >> p.cache.lp] : -2;
                 };
                 int next_page = page_of(w.tile0);
                 for (int t = w.tile0; t < w.tile0 + w.n && ok; t++) {
@@ -1015,12 +1015,12 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
                     q.valid = __ballot_sync(0xffffffffu, q.have);
                     // strip i lies in box 16 i / box
                     q.dead = __ballot_sync(0xffffffffu, lane < G::TT / 16 && t * G::TT + 16 * lane < w.s.len &&
-                                                            t * G::TT + 16 * lane + 16 > attn_lo(w.s) &&
+                                                            !attn_left_out(w.s, t * G::TT + 16 * lane + 15) &&
                                                             !((q.valid >> (16 * (lane & 7) / box)) & 1));
                     q.ctx = min(max(0, w.s.ctx - t * G::TT), G::TT);
                     q.len = min(w.s.len - t * G::TT, G::TT);
                     q.mark = pieces + 1;
-                    q.lo = min(max(0, attn_lo(w.s) - t * G::TT), G::TT);
+                    q.lo = P::SHARED ? min(max(0, attn_lo(w.s) - t * G::TT), G::TT) : 0;
                     if (side == 0 && lane == 0) {
                         dead_strips[(tiles + t - w.tile0) % kTcMarks] = (uint8_t)q.dead;
                         if (q.dead) atomicOr(error, BQG_DEVERR_PAGE);
