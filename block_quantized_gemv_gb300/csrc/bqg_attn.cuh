@@ -936,7 +936,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps) attn_kernel(const P p, int *e
     float *const row_bias = reinterpret_cast<float *>(smem + G::OFF_BIAS);
     unsigned long long *const row_sees = reinterpret_cast<unsigned long long *>(smem + G::OFF_VIS);
     float *const merged = reinterpret_cast<float *>(smem);                    // [warp][row][D + PAD]
-    pdl_wait();
+    pdl_wait();                              // (own_kernel relies on this order)
     pdl_launch_dependents();
 
     // This CTA's range of units.  Where there may be half as many sets (sequence, KV head) as CTAs, CTAs

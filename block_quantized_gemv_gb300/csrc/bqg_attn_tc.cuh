@@ -481,7 +481,7 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *base_word;
-    pdl_wait();
+    pdl_wait();                              // (own_kernel relies on this order)
     pdl_launch_dependents();
 
     // a wait that gives up ends its role's work; every other wait then gives up in its turn
@@ -1174,7 +1174,7 @@ attn_tc_kernel(const P p, const __grid_constant__ CUtensorMap kmap, const __grid
 // per warp.  In the order of the CTAs.
 template <int D, int ROWS, typename P = AttnParams> __global__ void __launch_bounds__(256) attn_tc_join_kernel(const P p, int ctas)
 {
-    pdl_wait();
+    pdl_wait();                              // (own_kernel relies on this order)
     pdl_launch_dependents();
     const TcSet set = reinterpret_cast<const TcSet *>(p.counters)[blockIdx.x];
     const int row = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
