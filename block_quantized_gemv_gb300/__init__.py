@@ -750,7 +750,8 @@ def shared_prefix_attention(q, cache: KVCache, block_table, ctx_len, q_start, ma
     Arguments and result as tree_attention's (ctx_len and block_table with the shared tokens), and: prefix_len int32
     [n_prefix], the tokens that sequences seq_start[g] .. seq_start[g + 1] - 1 share (at most the ctx_len of
     each; taken from the first one's pages); seq_start int32 [n_prefix + 1], or None for one prefix of all
-    sequences; max_shared: query tokens behind one prefix at most (default: all of the call's); ws: from
+    sequences; max_shared: query tokens behind one prefix at most (default: all of the call's, which with several
+    prefixes may pick a slower kernel); ws: from
     shared_prefix_attention_workspace, and a call without one is refused."""
     cur = _current_device()
     n, n_q, _ = _shape3(q, "q")

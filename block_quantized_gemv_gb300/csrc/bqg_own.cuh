@@ -23,7 +23,11 @@
 
 namespace bqg {
 
-constexpr int kOwnLeast = 8, kOwnLead = 4;      // strips
+// Strips of a range at least, and what beginning a set counts as.  The call's time (A: 96 sequences of 75 to 300 tokens behind 6 prefixes of
+// 300, 32 KV heads, q4_0; B: 1024 x 50 behind 1000, 2 KV heads, bf16; C: 4 x 600 behind 1000, 8 KV heads, bf16):
+//  * a lead of 0, 2, 4, 8: A 67, 64, 60, 61 us; B 80, 72, 67, 67;
+//  * at least 4, 8, 16, 32: B 67, 67, 79, 95; C 21.7, 21.1, 24.0, 30.1; 4 x 77 behind 1000, q8_0: 18.2, 16.5, 16.4, 16.4.
+constexpr int kOwnLeast = 8, kOwnLead = 4;
 
 template <int FMT, int D, int RT> struct OwnGeom {
     using G = AttnGeom<FMT, D, RT>;
@@ -81,7 +85,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps) own_kernel(const SharedParams
         total = attn_total(p, lane, [&](const SharedSeq &q) { sets += sets_of(q); return weight(q); }, bad, s, mine);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sets += __shfl_xor_sync(0xffffffffu, sets, o);
-        // With few sets each begins with a range, so that a warp has one set's: at most total / per + sets ranges.
+        // With few sets each begins with a range, so that a warp has one set's: at most total / per + sets ranges.  (Without it 4 x 77
+        // behind 1000, q8_0, take 24 us instead of 16, 150 x 40 behind 300 37 instead of 31; nearer to as many sets as warps the
+        // ranges that are left would be too long.)
         const bool fit = 8 * sets < 7 * (int64_t)workers;
         const int64_t to = fit ? workers - sets : workers;
         per = max(div_pos(total + to - 1, to), (int64_t)(kOwnLeast + kOwnLead));

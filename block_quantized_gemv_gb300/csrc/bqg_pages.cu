@@ -250,7 +250,7 @@ template <int FMT> void (*fork_fn(int D))(ForkParams)
 cudaError_t launch_compact(CompactParams p, int fmt, int D, int sms, cudaStream_t s, bool pdl)
 {
     if (cudaError_t e = device_error_word(&p.error)) return e;
-    // as many CTAs as are resident together, if there are heads for them
+    // six CTAs per SM, if there are heads for them (resident together but for bf16 of 256 values, where registers let four be)
     p.slices = (int)std::min<int64_t>(2 * p.cache.n_kv, std::max<int64_t>(1, (int64_t)sms * 6 / p.n_seq));
     auto fn = fmt == BQG_Q8_0 ? compact_fn<BQG_Q8_0>(D) : fmt == BQG_Q4_0 ? compact_fn<BQG_Q4_0>(D) : compact_fn<BQG_BF16>(D);
     int32_t *const apart = p.ctx_in_table ? p.ctx_out : nullptr;
@@ -264,6 +264,7 @@ cudaError_t launch_compact(CompactParams p, int fmt, int D, int sms, cudaStream_
 cudaError_t launch_fork(ForkParams p, int fmt, int D, int sms, cudaStream_t s, bool pdl)
 {
     if (cudaError_t e = device_error_word(&p.error)) return e;
+    // eight CTAs per SM, if there are runs for them (five are resident for bf16, three for codes: 48 and 75 to 80 registers)
     const int runs = (2 * p.cache.n_kv + kWarps - 1) / kWarps;
     p.slices = (int)std::min<int64_t>(runs, std::max<int64_t>(1, (int64_t)sms * 8 / p.n));
     auto fn = fmt == BQG_Q8_0 ? fork_fn<BQG_Q8_0>(D) : fmt == BQG_Q4_0 ? fork_fn<BQG_Q4_0>(D) : fork_fn<BQG_BF16>(D);

@@ -20,8 +20,8 @@
 //  * The crossing is looked for in the warps' sums, then by the warp that holds it in the sums that it kept (of 32 lanes and up
 //    to 16 steps), then in the 16 bytes of one lane: nothing of the row is read again but those.  There the sums are
 //    whole numbers of 2^-61 of all.  (Reading the warp's part again took 7 us of 18, most of it for fetching instructions that run once.)
-//  * Measured: one chain of 5 sampled drafts, 32,000 tokens, fp32: 9.0 us: about 3 for the launch, 1.6 until the deciding numbers
-//    are there, 3 for the rejection's sum (barriers 1.2), 1.9 for the token.  16 chosen trees, 100,003, bf16: 11 us.  64 sampled trees
+//  * Measured: one chain of 5 sampled drafts, 32,000 tokens, fp32: 9.4 us: about 3 for the launch, 1.6 until the deciding numbers
+//    are there, 3 for the rejection's sum (barriers 1.2), 1.9 for the token.  16 chosen trees, 100,003, bf16: 12 us.  64 sampled trees
 //    of up to 10, 131,072, fp32: 44 us, 10 for the bytes: the first sums run at the copy rate; then trees with up to five rejections wait
 //    for one pass after the other, from L2 (2.5 to 7 us each).
 #include <climits>
@@ -35,7 +35,9 @@ namespace bqg {
 namespace {
 
 constexpr int kMaxCtas = 8, kMaxDrafts = 64;
-constexpr int kLeast = 2048;           // values of a row that a CTA is taken for
+// Values of a row that a CTA is taken for.  With 512, 2048, 8192, 32768 (trees of 6): 1 sequence of 1000, fp32: 8.9, 7.2, 7.2, 7.2 us; of
+// 5000: 9.3, 9.0, 8.5, 8.5; of 32,000: 9.4, 9.4, 10.0, 15.5; 64 of 32,000: 25, 25, 34, 53; 128 of 5000, bf16: 15.8, 9.6, 8.8, 8.8.
+constexpr int kLeast = 2048;
 
 // An unevaluated sum of two fp32 numbers, none of which is negative.
 struct Pair {
