@@ -246,7 +246,7 @@ __device__ __forceinline__ SharedGroup shared_group(const SharedParams &p, int g
     const bool fits = n >= 0 && n < attn_cap(p) + (q1 == q0) && q1 - q0 <= p.max_shared;
     r.q0 = (int)q0; r.T = (int)(q1 - q0);
     r.len = fits && r.s0 < r.s1 ? (int)n : 0;
-    if (r.s0 != a || r.s1 != e || !fits) bad |= BQG_DEVERR_LENGTH;
+    if (r.s0 != a || r.s1 != e || (!fits && r.s0 < r.s1)) bad |= BQG_DEVERR_LENGTH;
     return r;
 }
 __device__ __forceinline__ SharedSeq attn_seq(const SharedParams &p, int b, int &bad)

@@ -50,6 +50,15 @@ def test_a_prefix_that_fills_the_table_of_sequences_without_new_tokens(fmt, T):
     c.check()
 
 
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("length", [10 ** 6, 2 ** 31 - 1, -1])
+def test_a_prefix_without_sequences_may_have_any_length(T, length):
+    """It is nobody's, so nothing does not fit."""
+    c = Shared(bqg.Q8_0, 128, 2, 2, [32, 9, 7], [2, 0, 1], [5, 0, 2], [T, 0, T], page=16, seed=6)
+    c.prefix[1] = length
+    c.check()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("T,group", [(1, 1), (2, 4), (9, 4), (20, 5)])
